@@ -249,10 +249,11 @@ def _router_plain(st):
     load = p.sum(0) / rows
     share = counts.float() / (rows * k)
     loss = st["coef"] * e * (share * load).sum().reshape(1)
-    out = {"experts": experts, "gates": gates, "counts": counts, "load": load, "loss": loss}
+    slope = st["coef"] * e * share / rows  # of the loss against each row's probabilities
+    out = {"experts": experts, "gates": gates, "counts": counts, "load": load, "slope": slope, "loss": loss}
     if st["train"]:
         dg = torch.where(chosen, st["dgates"], torch.zeros_like(st["dgates"]))
-        up = st["dloss"] * st["coef"] * e * share.unsqueeze(0) / rows
+        up = st["dloss"] * slope.unsqueeze(0)
         if st["normalize"]:
             direct = gates * (dg - (gates * dg).sum(1, keepdim=True))
             dx = p * (up - (p * up).sum(1, keepdim=True))
@@ -361,12 +362,12 @@ def _run_own(st):
         experts = torch.empty(st["rows"], k, dtype=torch.int32, device=dev)
         gates = torch.empty(st["rows"], k, device=dev)
         counts = torch.empty(e, dtype=torch.int32, device=dev)
-        load, loss = torch.empty(e, device=dev), torch.empty(1, device=dev)
-        lpc.lpc_router_forward(x, experts, gates, counts, load, loss, coef=st["coef"], normalize=st["normalize"], mask=st["mask"])
-        out = {"experts": experts, "gates": gates, "counts": counts, "load": load, "loss": loss}
+        load, slope, loss = torch.empty(e, device=dev), torch.empty(e, device=dev), torch.empty(1, device=dev)
+        lpc.lpc_router_forward(x, experts, gates, counts, load, slope, loss, coef=st["coef"], normalize=st["normalize"], mask=st["mask"])
+        out = {"experts": experts, "gates": gates, "counts": counts, "load": load, "slope": slope, "loss": loss}
         if st["train"]:
             out["dlogits"] = torch.empty_like(x)
-            lpc.lpc_router_backward(x, experts, counts, st["dgates"], st["dloss"], out["dlogits"], coef=st["coef"],
+            lpc.lpc_router_backward(x, experts, slope, st["dgates"], st["dloss"], out["dlogits"], coef=st["coef"],
                                     normalize=st["normalize"], mask=st["mask"])
         return out
     if "plan" not in st:  # the program's optimizer object: one view per tensor, checked once
@@ -398,7 +399,7 @@ def work(case):
     if case["op"] == "router":
         rows, e, k = case["rows"], case["experts"], case["topk"]
         size = 2 if case["logits"] == "bf16" else 4
-        forward = rows * e * size + rows * k * 8 + e * 8
+        forward = rows * e * size + rows * k * 8 + e * 12
         backward = rows * e * size + rows * k * 4
         return {"bytes": forward + (backward if case["train"] else 0) + (rows if case["masked"] else 0),
                 "flops": rows * e * (4 + (6 if case["train"] else 0))}
@@ -500,7 +501,7 @@ def _router64(st):
     gates = raw / total if st["normalize"] else raw
     counts = torch.bincount(which[taken], minlength=e)
     load, share = p.sum(0) / rows, counts.double() / (rows * k)
-    out = {"experts": None, "gates": gates, "counts": None, "load": load,
+    out = {"experts": None, "gates": gates, "counts": None, "load": load, "slope": st["coef"] * e * share / rows,
            "loss": (st["coef"] * e * (load * share).sum()).reshape(1)}
     if st["train"]:
         slot = st["dgates"].double() * taken
