@@ -367,7 +367,7 @@ def _run_own(st):
         out = {"experts": experts, "gates": gates, "counts": counts, "load": load, "slope": slope, "loss": loss}
         if st["train"]:
             out["dlogits"] = torch.empty_like(x)
-            lpc.lpc_router_backward(x, experts, slope, st["dgates"], st["dloss"], out["dlogits"], coef=st["coef"],
+            lpc.lpc_router_backward(x, experts, slope, st["dgates"], st["dloss"], out["dlogits"],
                                     normalize=st["normalize"], mask=st["mask"])
         return out
     if "plan" not in st:  # the program's optimizer object: one view per tensor, checked once
