@@ -26,7 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblpc.so")
 SOURCES = [os.path.join(CSRC, n) for n in ("lpc_kernels.hip", "lpc_api.hip", "lpc_allreduce.hip",
-                                           "lpc_measure.hip")]
+                                           "lpc_measure.hip", "lpc_ops_api.hip", "lpc_gemm.hip",
+                                           "lpc_cols.hip", "lpc_router.hip", "lpc_adamw.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

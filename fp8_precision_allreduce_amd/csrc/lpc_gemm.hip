@@ -1,0 +1,284 @@
+// lpc_gemm.hip -- FP8 block-scaled products and the gradient of the weights.
+//
+// Both are sums over blocks of 128 along the contraction,
+//   out[q, p] = sum_b qs[q, b] * ps[p, b] * (Q[q, b] . P[p, b]),
+// with Q and P rows of E4M3 codes that lie along the contraction:
+//   product  Q = rows of x (one scale per row and block), P = rows of a weight
+//            (one scale per 128 rows and block)
+//   wgrad    Q = columns of the incoming gradient, P = columns of x, both with
+//            one scale per column and block, over one group's padded rows
+// The matrix cores give the inner product of a whole block for 16 x 16 outputs;
+// the scales are FP32 with any mantissa, so the block's sum is then scaled and
+// added to the FP32 accumulators by the vector unit.  P is the matrix core's
+// row operand: a lane then holds four neighbouring p of one q, so qs is one
+// value per lane and an output store is 4 elements wide.
+//
+// Two instructions, by the type of the output:
+//   bf16  v_mfma_f32_16x16x128_f8f6f4 on the codes.  Measured on this card, it
+//         aligns the products of each 8 neighbouring contraction indices to the
+//         largest of them and drops what is below 2^-14 of its power of two;
+//         the sums of 8 are added in FP32.  On normally distributed data the
+//         block's sum is off by 1.3e-5 of itself (2-norm), 1/100 of what
+//         rounding the result to bf16 (2^-8 at most, 1.7e-3 in the 2-norm) adds.
+//   fp32  four v_mfma_f32_16x16x32_f16 on the codes widened to fp16, which is
+//         exact (E4M3's smallest value is 2^-9, its largest 448).  Products and
+//         sums then hold FP32's precision: off by 1e-8 of the block's sum on the
+//         same data.  Half the rate of the first.
+//
+// Which contraction index a lane's bytes stand for does not matter as long as
+// both operands are loaded alike: lane l holds bytes 32 (l/16) .. + 31 of row
+// l % 16.
+#include "lpc_ops.hpp"
+
+namespace lpc {
+namespace {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+enum Mode { kProduct, kWgrad };
+
+struct GemmArgs {
+    const uint8_t* q;
+    const uint8_t* p;
+    const float* qs;
+    const float* ps;
+    const int32_t* counts;
+    void* out;
+    uint32_t groups, rows;  // rows of x
+    uint32_t nq, np;        // wgrad: outputs along q; both: outputs along p
+    size_t ld;              // bytes between rows of q and of p
+};
+
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+// a lane's 32 codes of one row, as the instruction takes them
+template <typename Out> struct Fragment;
+
+template <>
+struct Fragment<uint16_t> {
+    i32x8_t c;
+    __device__ Fragment() = default;
+    __device__ __forceinline__ explicit Fragment(i32x8_t codes) : c(codes) {}
+};
+
+template <>
+struct Fragment<float> {
+    f16x8_t h[4];
+    __device__ Fragment() = default;
+    __device__ __forceinline__ explicit Fragment(i32x8_t codes) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const f16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.0f, false);
+            const f16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.0f, true);
+            h[i / 2][4 * (i % 2)] = lo[0];
+            h[i / 2][4 * (i % 2) + 1] = lo[1];
+            h[i / 2][4 * (i % 2) + 2] = hi[0];
+            h[i / 2][4 * (i % 2) + 3] = hi[1];
+        }
+    }
+};
+
+// sums over a block of 128 for 16 x 16 outputs
+__device__ __forceinline__ f32x4_t block_sum(const Fragment<uint16_t>& p, const Fragment<uint16_t>& q) {
+    const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p.c, q.c, zero, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x4_t block_sum(const Fragment<float>& p, const Fragment<float>& q) {
+    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(p.h[i], q.h[i], s, 0, 0, 0);
+    return s;
+}
+
+__device__ __forceinline__ i32x8_t join(i32x4_t a, i32x4_t b) {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// 32 bytes of one row
+__device__ __forceinline__ i32x8_t load_fragment(const uint8_t* __restrict__ p) {
+    const i32x4_t* v = reinterpret_cast<const i32x4_t*>(p);
+    return join(v[0], v[1]);
+}
+
+// four neighbouring outputs; `wide`: np is a multiple of 4, so all four exist and are aligned
+__device__ __forceinline__ void store4(float* __restrict__ o, const f32x4_t& v, uint32_t left, bool wide) {
+    if (wide) {
+        *reinterpret_cast<f32x4_t*>(o) = v;
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            if (i < left) o[i] = v[i];
+    }
+}
+
+__device__ __forceinline__ void store4(uint16_t* __restrict__ o, const f32x4_t& v, uint32_t left, bool wide) {
+    const u32x2_t w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    if (wide) {
+        *reinterpret_cast<u32x2_t*>(o) = w;
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            if (i < left) o[i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+    }
+}
+
+// What one workgroup computes: outputs [q0, q0 + nq) x [p0, ...) from blocks [b0, b1).
+struct Work {
+    uint32_t q0, nq, b0, b1;
+    const uint8_t* p;  // group's P and scales
+    const float* ps;
+    size_t out;        // element of out where output row 0 of the q numbering starts
+    bool none;         // nothing at all to do
+};
+
+template <int M, uint32_t BQ>
+__device__ __forceinline__ Work find_work(const GemmArgs& a, uint32_t tq, uint32_t z) {
+    Work w;
+    if constexpr (M == kProduct) {
+        const GroupTile t = find_tile(a.counts, a.groups, a.rows, BQ, tq);
+        const uint32_t blocks = (uint32_t)(a.ld / kBlock);
+        const size_t g = t.group < a.groups ? t.group : 0;
+        w.q0 = t.row;
+        w.nq = t.rows;
+        w.b0 = 0;
+        w.b1 = t.group < a.groups ? blocks : 0;  // rows past the last group: an empty sum
+        w.p = a.p + g * a.np * a.ld;
+        w.ps = a.ps + g * ((a.np + kBlock - 1) / kBlock) * blocks;
+        w.out = 0;
+        w.none = t.rows == 0;
+    } else {
+        const GroupTile t = find_group(a.counts, a.rows, kBlock, z);
+        w.q0 = tq * BQ;
+        w.nq = min(BQ, a.nq - w.q0);
+        w.b0 = t.before;
+        w.b1 = t.before + t.tiles;
+        w.p = a.p;
+        w.ps = a.ps;
+        w.out = (size_t)z * a.nq * a.np;
+        w.none = false;
+    }
+    return w;
+}
+
+// ---------------------------------------------------------------------------
+// split: 16 QF x 16 PF outputs per workgroup, its 8 wavefronts take every
+// eighth block and their sums are joined through LDS, in the wavefronts' order.
+// Operands go straight to registers.
+// ---------------------------------------------------------------------------
+
+constexpr int kSplitWaves = 8;
+
+template <int M, typename Out, int QF, int PF>
+__global__ __launch_bounds__(kSplitWaves * 64) void gemm_split_kernel(GemmArgs a) {
+    constexpr uint32_t BQ = 16 * QF, BP = 16 * PF;
+    __shared__ f32x4_t sums[kSplitWaves][QF * PF][64];
+    const uint32_t np_tiles = (a.np + BP - 1) / BP;
+    const uint32_t tile = (uint32_t)xcd_tile();
+    const Work w = find_work<M, BQ>(a, tile / np_tiles, blockIdx.y);
+    if (w.none) return;
+    const uint32_t p0 = tile % np_tiles * BP;
+    const uint32_t wave = threadIdx.x >> 6, l = threadIdx.x & 63, l16 = l & 15, l4 = l >> 4;
+
+    const uint8_t* qrow[QF];
+    const uint8_t* prow[PF];
+    uint32_t qi[QF];
+#pragma unroll
+    for (int f = 0; f < QF; ++f) {  // rows past the tile's repeat its last one; their sums are not stored
+        qi[f] = w.q0 + min(16 * f + l16, w.nq - 1);
+        qrow[f] = a.q + (size_t)qi[f] * a.ld + 32 * l4;
+    }
+#pragma unroll
+    for (int f = 0; f < PF; ++f) prow[f] = w.p + (size_t)min(p0 + 16 * f + l16, a.np - 1) * a.ld + 32 * l4;
+    const uint32_t blocks = (uint32_t)(a.ld / kBlock);
+
+    f32x4_t acc[QF][PF];
+#pragma unroll
+    for (int i = 0; i < QF; ++i)
+#pragma unroll
+        for (int j = 0; j < PF; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    for (uint32_t b = w.b0 + wave; b < w.b1; b += kSplitWaves) {
+        i32x8_t qc[QF], pc[PF];
+        float qs[QF];
+#pragma unroll
+        for (int f = 0; f < PF; ++f) pc[f] = load_fragment(prow[f] + (size_t)b * kBlock);
+#pragma unroll
+        for (int f = 0; f < QF; ++f) {
+            qc[f] = load_fragment(qrow[f] + (size_t)b * kBlock);
+            qs[f] = M == kProduct ? a.qs[(size_t)qi[f] * blocks + b] : a.qs[(size_t)b * a.nq + qi[f]];
+        }
+        Fragment<Out> qv[QF];
+#pragma unroll
+        for (int f = 0; f < QF; ++f) qv[f] = Fragment<Out>(qc[f]);
+#pragma unroll
+        for (int j = 0; j < PF; ++j) {
+            const Fragment<Out> pv(pc[j]);
+            f32x4_t ps;
+            if constexpr (M == kProduct) {
+                const float s = w.ps[(size_t)((p0 + 16 * j) / kBlock) * blocks + b];
+                ps = f32x4_t{s, s, s, s};
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ps[i] = w.ps[(size_t)b * a.np + min(p0 + 16 * j + 4 * l4 + i, a.np - 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < QF; ++i) {
+                const f32x4_t part = block_sum(pv, qv[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[e], qs[i] * ps[e], acc[i][j][e]);
+            }
+        }
+    }
+
+#pragma unroll
+    for (int i = 0; i < QF; ++i)
+#pragma unroll
+        for (int j = 0; j < PF; ++j) sums[wave][i * PF + j][l] = acc[i][j];
+    __syncthreads();
+    Out* out = static_cast<Out*>(a.out) + w.out;
+    for (uint32_t f = wave; f < QF * PF; f += kSplitWaves) {
+        f32x4_t v = sums[0][f][l];
+#pragma unroll
+        for (int s = 1; s < kSplitWaves; ++s) v += sums[s][f][l];
+        const uint32_t q = f / PF * 16 + l16, p = p0 + f % PF * 16 + 4 * l4;
+        if (q < w.nq && p < a.np) store4(out + (size_t)(w.q0 + q) * a.np + p, v, a.np - p, a.np % 4 == 0);
+    }
+}
+
+template <int M, typename Out, int QF, int PF>
+hipError_t launch_split(const GemmArgs& a, uint32_t tiles_q, uint32_t z, hipStream_t stream) {
+    const uint64_t wgs = (uint64_t)tiles_q * ((a.np + 16 * PF - 1) / (16 * PF));
+    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    return enqueue(gemm_split_kernel<M, Out, QF, PF>, dim3((uint32_t)wgs, z), dim3(kSplitWaves * 64), stream, a);
+}
+
+// Tiles of T rows that any counts can make of `rows` rows in `groups` groups and
+// the rows past them: every group and the rest may end in a short tile.
+uint32_t most_tiles(const GemmArgs& a, uint32_t T) {
+    return (uint32_t)((a.rows + (uint64_t)T - 1) / T) + (a.counts ? a.groups : 0);
+}
+
+template <typename Out>
+hipError_t launch_product(const GemmArgs& a, hipStream_t stream) {
+    return launch_split<kProduct, Out, 4, 4>(a, most_tiles(a, 64), 1, stream);
+}
+
+}  // namespace
+
+hipError_t launch_gemm(const uint8_t* x, const float* xs, size_t rows, size_t k, const uint8_t* w, const float* ws,
+                       size_t n, int groups, const int32_t* counts, void* out, int out_bf16, hipStream_t stream) {
+    const GemmArgs a{x, w, xs, ws, counts, out, (uint32_t)groups, (uint32_t)rows, 0, (uint32_t)n, k};
+    return out_bf16 ? launch_product<uint16_t>(a, stream) : launch_product<float>(a, stream);
+}
+
+hipError_t launch_wgrad(const uint8_t* yt, const float* ys, size_t n, const uint8_t* xt, const float* xs, size_t k,
+                        size_t rows, size_t padded, int groups, const int32_t* counts, float* dw,
+                        hipStream_t stream) {
+    const GemmArgs a{yt, xt, ys, xs, counts, dw, (uint32_t)groups, (uint32_t)rows, (uint32_t)n, (uint32_t)k, padded};
+    return launch_split<kWgrad, float, 4, 4>(a, (uint32_t)((n + 63) / 64), (uint32_t)groups, stream);
+}
+
+}  // namespace lpc

@@ -1,0 +1,117 @@
+// lpc_ops.hpp -- shared by the operators declared in include/lpc_ops.h: their
+// launchers (called by lpc_ops_api.hip with checked arguments) and the device
+// code that finds a group's rows.  Internal to liblpc.so.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <tuple>
+
+#include "lpc.h"
+#include "lpc_device.hpp"
+#include "lpc_ops.h"
+
+namespace lpc {
+
+// Enqueue one kernel: converts the arguments to the kernel's parameter types
+// and returns the status of this launch itself.
+template <typename... P, typename... A>
+static hipError_t enqueue(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t stream, A... args) {
+    static_assert(sizeof...(P) == sizeof...(A) && sizeof...(P) > 0, "argument count");
+    std::tuple<P...> vals(args...);
+    return std::apply(
+        [&](auto&... v) {
+            void* ptrs[] = {static_cast<void*>(&v)...};
+            return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, ptrs, 0, stream);
+        },
+        vals);
+}
+
+// The rows of one tile: tiles of `T` rows are laid over each group in turn, a
+// group's last tile may be short.
+struct GroupTile {
+    uint32_t group;      // == groups: the rows past the last group
+    uint32_t row, rows;  // first row of the tile and how many are the group's (0: no such tile)
+    uint32_t before;     // tiles before this group
+    uint32_t tiles;      // tiles of this group
+};
+
+// Rows of group g: the count on the device, no less than 0 and no more than
+// what the buffer has left.
+__device__ __forceinline__ uint32_t group_rows(const int32_t* __restrict__ counts, uint32_t g, uint32_t left) {
+    if (!counts) return left;
+    const int32_t c = counts[g];
+    return c < 0 ? 0u : min((uint32_t)c, left);
+}
+
+// Tile number t.  The counts are read in order by the scalar unit; the loop is
+// uniform over the wavefront.
+__device__ __forceinline__ GroupTile find_tile(const int32_t* __restrict__ counts, uint32_t groups, uint32_t rows,
+                                               uint32_t T, uint32_t t) {
+    uint32_t row = 0, before = 0;
+    for (uint32_t g = 0; g < groups; ++g) {
+        const uint32_t c = group_rows(counts, g, rows - row);
+        const uint32_t n = (c + T - 1) / T;
+        if (t - before < n) {
+            const uint32_t off = (t - before) * T;
+            return {g, row + off, min(T, c - off), before, n};
+        }
+        row += c;
+        before += n;
+    }
+    const uint32_t left = rows - row, n = (left + T - 1) / T, off = (t - before) * T;
+    if (t - before < n) return {groups, row + off, min(T, left - off), before, n};
+    return {groups, rows, 0u, before, n};
+}
+
+// First tile and number of tiles of group g.
+__device__ __forceinline__ GroupTile find_group(const int32_t* __restrict__ counts, uint32_t rows, uint32_t T,
+                                                uint32_t g) {
+    uint32_t row = 0, before = 0;
+    for (uint32_t i = 0; i < g; ++i) {
+        const uint32_t c = group_rows(counts, i, rows - row);
+        row += c;
+        before += (c + T - 1) / T;
+    }
+    const uint32_t c = group_rows(counts, g, rows - row);
+    return {g, row, c, before, (c + T - 1) / T};
+}
+
+hipError_t launch_gemm(const uint8_t* x, const float* xs, size_t rows, size_t k, const uint8_t* w, const float* ws,
+                       size_t n, int groups, const int32_t* counts, void* out, int out_bf16, hipStream_t stream);
+hipError_t launch_wgrad(const uint8_t* yt, const float* ys, size_t n, const uint8_t* xt, const float* xs, size_t k,
+                        size_t rows, size_t padded, int groups, const int32_t* counts, float* dw,
+                        hipStream_t stream);
+hipError_t launch_quantize_cols(const void* y, int in_bf16, size_t rows, size_t n, size_t padded, int groups,
+                                const int32_t* counts, uint8_t* codes_t, float* scales_t, uint8_t* codes,
+                                float* scales, hipStream_t stream);
+hipError_t launch_requantize_cols(const uint8_t* x, const float* xs, size_t rows, size_t k, size_t padded,
+                                  int groups, const int32_t* counts, uint8_t* codes_t, float* scales_t,
+                                  hipStream_t stream);
+
+size_t router_workspace_bytes(size_t rows, int experts);
+hipError_t launch_router_forward(const void* logits, int in_bf16, size_t rows, int experts, int topk, int normalize,
+                                 float coef, const uint8_t* mask, int32_t* out_experts, float* gates,
+                                 int32_t* counts, float* load, float* slope, float* loss, void* workspace,
+                                 hipStream_t stream);
+hipError_t launch_router_backward(const void* logits, int in_bf16, size_t rows, int experts, int topk, int normalize,
+                                  const uint8_t* mask, const int32_t* out_experts, const float* slope,
+                                  const float* dgates, const float* dloss, void* dlogits, hipStream_t stream);
+
+// elements of a tensor that one workgroup of the AdamW kernel updates
+constexpr size_t kAdamwChunk = 4096;
+
+// A plan is the chunks (which tensor, and the chunk's number within it), up to a
+// multiple of 16 bytes, then the tensors as the caller gave them.
+struct AdamwChunk {
+    uint32_t tensor, index;
+};
+inline __host__ __device__ size_t adamw_chunk_bytes(size_t chunks) { return (chunks * sizeof(AdamwChunk) + 15) / 16 * 16; }
+struct AdamwScalars {
+    float beta1, rest1, beta2, rest2, keep, rate, root, eps;
+};
+hipError_t launch_adamw(const void* plan, size_t chunks, int grad_bf16, int state_bits, const AdamwScalars& s,
+                        const float* grad_scale, hipStream_t stream);
+
+}  // namespace lpc

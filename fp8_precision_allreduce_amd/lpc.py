@@ -22,6 +22,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblpc.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "lpc.h")
 MEASURE_HEADER = os.path.join(os.path.dirname(_HERE), "include", "lpc_measure.h")
+OPS_HEADER = os.path.join(os.path.dirname(_HERE), "include", "lpc_ops.h")
 
 BLOCK = 128
 MAX_RANKS = 8
@@ -42,7 +43,13 @@ class LpcError(RuntimeError):
         self.status_name = STATUS[status] if 0 <= status < len(STATUS) else str(status)
 
 
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("param", "grad", "m", "v", "m_scales", "v_scales", "copy")] + [
+        ("n", ctypes.c_size_t)]
+
+
 _vp, _sz, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_f32, _f64, _szp, _tp = ctypes.c_float, ctypes.c_double, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(_AdamwTensor)
 _pp = ctypes.POINTER(ctypes.c_void_p)
 SIGNATURES = {
     "lpc_quantize_fp8": [_vp, _int, _sz, _vp, _vp, _vp],
@@ -61,10 +68,24 @@ SIGNATURES = {
     "lpc_allreduce_workspace_bytes": [_int, _int, _sz, _int, ctypes.POINTER(ctypes.c_size_t)],
     "lpc_allreduce_emulated": [_pp, _int, _sz, _int, _int, _vp, _sz, _vp],
     "lpc_allreduce_emulated_noalloc": [_pp, _int, _sz, _int, _int, _vp],
+    # training and serving operators (include/lpc_ops.h)
+    "lpc_gemm_fp8": [_vp, _vp, _sz, _sz, _vp, _vp, _sz, _int, _vp, _vp, _int, _vp],
+    "lpc_padded_rows": [_sz, _int],
+    "lpc_quantize_fp8_cols": [_vp, _int, _sz, _sz, _int, _vp, _vp, _vp, _vp, _vp, _vp],
+    "lpc_requantize_fp8_cols": [_vp, _vp, _sz, _sz, _int, _vp, _vp, _vp, _vp],
+    "lpc_gemm_fp8_wgrad": [_vp, _vp, _sz, _vp, _vp, _sz, _sz, _int, _vp, _vp, _vp],
+    "lpc_router_workspace_bytes": [_sz, _int],
+    "lpc_router_forward": [_vp, _int, _sz, _int, _int, _int, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "lpc_router_backward": [_vp, _int, _sz, _int, _int, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "lpc_adamw_plan_bytes": [_tp, _int],
+    "lpc_adamw_plan": [_tp, _int, _int, _int, _vp, _sz, _szp],
+    "lpc_adamw_step": [_vp, _sz, _int, _int, ctypes.c_int64, _f64, _f64, _f64, _f64, _f64, _vp, _vp],
     # reference kernels for measurement (include/lpc_measure.h)
     "lpc_measure_stream": [_vp, _sz, _vp, _sz, _int, _vp],
     "lpc_measure_empty": [ctypes.c_uint, ctypes.c_uint, ctypes.c_uint, _sz, _vp, _vp],
 }
+
+SIZES = ("lpc_padded_rows", "lpc_router_workspace_bytes", "lpc_adamw_plan_bytes")  # these return a size_t, not a status
 
 _lock = threading.Lock()
 _lib = None
@@ -84,7 +105,7 @@ def lib() -> ctypes.CDLL:
             for name, args in SIGNATURES.items():
                 f = getattr(L, name)
                 f.argtypes = args
-                f.restype = ctypes.c_int
+                f.restype = ctypes.c_size_t if name in SIZES else ctypes.c_int
             L.lpc_status_string.argtypes = [ctypes.c_int]
             L.lpc_status_string.restype = ctypes.c_char_p
             L.lpc_abi_version.argtypes = []
@@ -306,3 +327,230 @@ def lpc_measure_empty(grid_x: int, grid_y: int, threads: int, kernarg_bytes: int
 def lpc_e4m3_encode(x: torch.Tensor, codes: torch.Tensor, stream=None):
     n = x.numel()
     _call("lpc_e4m3_encode", _dev(x, "x", _F32), n, _dev(codes, "codes", _U8, n), _stream(stream))
+
+
+# ---------------------------------------------------------------------------
+# training and serving operators (include/lpc_ops.h)
+#
+# One operator call is a few microseconds of GPU work at its smallest, so these
+# marshal with plain integers and run on the tensors' own device: all tensors of
+# a call must be on one GPU, and the work goes to that GPU's current stream
+# unless another is given.
+# ---------------------------------------------------------------------------
+
+class _Args:
+    """Pointers of one call's tensors, checked as _dev checks them and to be on one GPU."""
+
+    __slots__ = ("device",)
+
+    def __init__(self):
+        self.device = None
+
+    def __call__(self, t, what, dtypes, numel, exact=False):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch tensor" % what)
+        if not t.is_cuda:
+            raise ValueError("%s must be a GPU tensor" % what)
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % what)
+        if t.dtype not in dtypes:
+            raise TypeError("%s has dtype %s, expected one of %s" % (what, t.dtype, dtypes))
+        n = t.numel()
+        if n < numel or (exact and n != numel):
+            raise ValueError("%s holds %d elements, needs %d" % (what, n, numel))
+        d = t.get_device()
+        if self.device is None:
+            self.device = d
+        elif self.device != d:
+            raise ValueError("%s is on cuda:%d, the other tensors on cuda:%d" % (what, d, self.device))
+        return t.data_ptr()
+
+    def optional(self, t, what, dtypes, numel):
+        return None if t is None else self(t, what, dtypes, numel)
+
+
+def _run(name, device, stream, *args):
+    """Call an entry point whose last argument is the stream, with `device` current."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    f = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == device:
+        st = f(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, stream)
+    if st != 0:
+        raise LpcError(name, st, lpc_status_string(st))
+
+
+def _shape2(t, what):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError("%s must be a 2-D tensor" % what)
+    return t.shape
+
+
+def _groups(counts):
+    return 1 if counts is None else counts.numel()
+
+
+def _blocks(n):
+    return -(-n // BLOCK)
+
+
+def lpc_gemm_fp8(x, xs, w, ws, out, counts=None, stream=None):
+    """out [rows, n] = x [rows, k] times w [groups, n, k] (or [n, k]) transposed, E4M3 codes with scales
+    xs [rows, k/128] and ws [groups, ceil(n/128), k/128]; counts [groups] int32: rows of each group."""
+    rows, k = _shape2(x, "x")
+    n, kw = w.shape[-2:]
+    groups = _groups(counts)
+    if kw != k or w.dim() not in (2, 3) or w.numel() != groups * n * k:
+        raise ValueError("w has shape %s, expected [%d, n, %d]" % (tuple(w.shape), groups, k))
+    if _shape2(out, "out") != (rows, n):
+        raise ValueError("out has shape %s, expected [%d, %d]" % (tuple(out.shape), rows, n))
+    p = _Args()
+    args = (p(x, "x", _U8, 0), p(xs, "xs", _F32, rows * (k // BLOCK), True), rows, k, p(w, "w", _U8, 0),
+            p(ws, "ws", _F32, groups * _blocks(n) * (k // BLOCK), True), n, groups,
+            p.optional(counts, "counts", _I32, 1), p(out, "out", _FB, 0), _dtype(out))
+    _run("lpc_gemm_fp8", p.device, stream, *args)
+
+
+def lpc_padded_rows(rows: int, groups: int) -> int:
+    """Rows of the padded column layout for any counts (no GPU call)."""
+    return lib().lpc_padded_rows(rows, groups)
+
+
+def lpc_quantize_fp8_cols(y, codes_t, scales_t, codes=None, scales=None, counts=None, stream=None):
+    """Column codes [n, padded] and scales [padded/128, n] of y [rows, n], and in the same pass its row
+    codes [rows, n] and scales [rows, n/128] where those are given."""
+    rows, n = _shape2(y, "y")
+    groups = _groups(counts)
+    padded = lpc_padded_rows(rows, groups)
+    p = _Args()
+    args = (p(y, "y", _FB, 0), _dtype(y), rows, n, groups, p.optional(counts, "counts", _I32, 1),
+            p(codes_t, "codes_t", _U8, padded * n, True), p(scales_t, "scales_t", _F32, padded // BLOCK * n, True),
+            p.optional(codes, "codes", _U8, rows * n), p.optional(scales, "scales", _F32, rows * n // BLOCK))
+    _run("lpc_quantize_fp8_cols", p.device, stream, *args)
+
+
+def lpc_requantize_fp8_cols(x, xs, codes_t, scales_t, counts=None, stream=None):
+    """Column codes [k, padded] and scales [padded/128, k] of the rows that codes x [rows, k] and scales
+    xs [rows, k/128] hold."""
+    rows, k = _shape2(x, "x")
+    groups = _groups(counts)
+    padded = lpc_padded_rows(rows, groups)
+    p = _Args()
+    args = (p(x, "x", _U8, 0), p(xs, "xs", _F32, rows * (k // BLOCK), True), rows, k, groups,
+            p.optional(counts, "counts", _I32, 1), p(codes_t, "codes_t", _U8, padded * k, True),
+            p(scales_t, "scales_t", _F32, padded // BLOCK * k, True))
+    _run("lpc_requantize_fp8_cols", p.device, stream, *args)
+
+
+def lpc_gemm_fp8_wgrad(yt, ys, xt, xs, dw, rows: int, counts=None, stream=None):
+    """dw [groups, n, k] (or [n, k]) fp32 from the column forms of the incoming gradient, yt [n, padded],
+    and of the rows, xt [k, padded]."""
+    n, k = dw.shape[-2:]
+    groups = _groups(counts)
+    if dw.dim() not in (2, 3) or dw.numel() != groups * n * k:
+        raise ValueError("dw has shape %s, expected [%d, n, k]" % (tuple(dw.shape), groups))
+    padded = lpc_padded_rows(rows, groups)
+    p = _Args()
+    args = (p(yt, "yt", _U8, n * padded, True), p(ys, "ys", _F32, n * (padded // BLOCK), True), n,
+            p(xt, "xt", _U8, k * padded, True), p(xs, "xs", _F32, k * (padded // BLOCK), True), k, rows, groups,
+            p.optional(counts, "counts", _I32, 1), p(dw, "dw", _F32, 0))
+    _run("lpc_gemm_fp8_wgrad", p.device, stream, *args)
+
+
+def lpc_router_workspace_bytes(rows: int, experts: int) -> int:
+    """Device workspace of lpc_router_forward (no GPU call)."""
+    return lib().lpc_router_workspace_bytes(rows, experts)
+
+
+def lpc_router_forward(logits, experts, gates, counts, load, slope, loss, coef: float, normalize: bool = True,
+                       mask=None, workspace=None, stream=None):
+    """Routing of logits [rows, E]: experts (int32) and gates [rows, topk], counts (int32), load and slope [E],
+    loss [1].  Without a workspace (uint8, lpc_router_workspace_bytes) one is taken from torch's allocator."""
+    rows, e = _shape2(logits, "logits")
+    r2, topk = _shape2(experts, "experts")
+    if r2 != rows:
+        raise ValueError("experts has %d rows, expected %d" % (r2, rows))
+    p = _Args()
+    args = [p(logits, "logits", _FB, 0), _dtype(logits), rows, e, topk, 1 if normalize else 0, coef,
+            p.optional(mask, "mask", (torch.uint8, torch.bool), rows), p(experts, "experts", _I32, 0),
+            p(gates, "gates", _F32, rows * topk, True), p(counts, "counts", _I32, e, True),
+            p(load, "load", _F32, e, True), p(slope, "slope", _F32, e, True), p(loss, "loss", _F32, 1, True)]
+    need = lpc_router_workspace_bytes(rows, e)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=logits.device)
+        if stream is not None:  # allocated for the current stream, used on the given one
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(int(stream), device=logits.device))
+    _run("lpc_router_forward", p.device, stream, *args, p(workspace, "workspace", _U8, 0), workspace.numel())
+
+
+def lpc_router_backward(logits, experts, slope, dgates, dloss, dlogits, normalize: bool = True, mask=None, stream=None):
+    """dlogits [rows, E] from dgates [rows, topk] and dloss [1], with the forward call's experts and slope."""
+    rows, e = _shape2(logits, "logits")
+    r2, topk = _shape2(experts, "experts")
+    if r2 != rows or dlogits.dtype != logits.dtype:
+        raise ValueError("experts and dlogits do not match logits")
+    p = _Args()
+    args = (p(logits, "logits", _FB, 0), _dtype(logits), rows, e, topk, 1 if normalize else 0,
+            p.optional(mask, "mask", (torch.uint8, torch.bool), rows), p(experts, "experts", _I32, 0),
+            p(slope, "slope", _F32, e, True), p(dgates, "dgates", _F32, rows * topk, True),
+            p(dloss, "dloss", _F32, 1, True), p(dlogits, "dlogits", _FB, rows * e, True))
+    _run("lpc_router_backward", p.device, stream, *args)
+
+
+class AdamW:
+    """AdamW over many tensors in one launch a step (lpc_adamw_plan, lpc_adamw_step).
+
+    params (fp32), grads (all fp32 or all bf16) and the moments m, v are lists of contiguous tensors, checked once
+    and updated in place; the tensors must stay where they are.  With m_scales and v_scales the moments are E4M3
+    codes (uint8) with one fp32 scale per 128 elements, v holding the root of the second moment.  copies: bf16
+    tensors that get the updated params.  A step reads no tensor's address again, so it can be captured in a graph
+    (its hyperparameters are then the captured ones)."""
+
+    def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, copies=None):
+        if (m_scales is None) != (v_scales is None):
+            raise ValueError("m_scales and v_scales come together")
+        self.state_bits = 32 if m_scales is None else 8
+        lists = {"grads": grads, "m": m, "v": v, "m_scales": m_scales, "v_scales": v_scales, "copies": copies}
+        for what, ts in lists.items():
+            if ts is not None and len(ts) != len(params):
+                raise ValueError("%s has %d tensors, params %d" % (what, len(ts), len(params)))
+        state = _F32 if self.state_bits == 32 else _U8
+        p, table = _Args(), (_AdamwTensor * max(len(params), 1))()
+        for i, t in enumerate(params):
+            row = table[i]
+            row.param = p(t, "params[%d]" % i, _F32, 0)
+            row.n = n = t.numel()
+            row.grad = p(grads[i], "grads[%d]" % i, (grads[0].dtype,), n, True)
+            row.m = p(m[i], "m[%d]" % i, state, n, True)
+            row.v = p(v[i], "v[%d]" % i, state, n, True)
+            if self.state_bits == 8:
+                row.m_scales = p(m_scales[i], "m_scales[%d]" % i, _F32, _blocks(n), True)
+                row.v_scales = p(v_scales[i], "v_scales[%d]" % i, _F32, _blocks(n), True)
+            if copies is not None:
+                row.copy = p(copies[i], "copies[%d]" % i, (torch.bfloat16,), n, True)
+        self.grad_dtype = _dtype(grads[0]) if len(params) else LPC_F32
+        self.device = p.device
+        self._tensors = (list(params), {k: list(ts) for k, ts in lists.items() if ts is not None})  # kept alive
+        size = lib().lpc_adamw_plan_bytes(table, len(params))
+        host = torch.empty(size, dtype=torch.uint8)
+        chunks = ctypes.c_size_t(0)
+        _call("lpc_adamw_plan", table, len(params), self.grad_dtype, self.state_bits, host.data_ptr() if size else None, size,
+              ctypes.byref(chunks))
+        self._chunks = chunks.value
+        self._plan = host.to("cuda:%d" % self.device) if self._chunks else None
+
+    def step(self, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+             weight_decay: float = 0.01, grad_scale=None, stream=None):
+        """Update `step` (counted from 1); grad_scale: a GPU tensor whose first element multiplies every gradient."""
+        if self._plan is None:
+            return
+        p = _Args()
+        p.device = self.device
+        _run("lpc_adamw_step", self.device, stream, self._plan.data_ptr(), self._chunks, self.grad_dtype,
+             self.state_bits, step, lr, beta1, beta2, eps, weight_decay, p.optional(grad_scale, "grad_scale", _F32, 1))
