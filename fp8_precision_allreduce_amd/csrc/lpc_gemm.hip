@@ -255,14 +255,225 @@ hipError_t launch_split(const GemmArgs& a, uint32_t tiles_q, uint32_t z, hipStre
     return enqueue(gemm_split_kernel<M, Out, QF, PF>, dim3((uint32_t)wgs, z), dim3(kSplitWaves * 64), stream, a);
 }
 
+// ---------------------------------------------------------------------------
+// tiled: one workgroup of 8 wavefronts per BQ x BP outputs.  Blocks of both
+// operands go to LDS by asynchronous loads, two stages deep; a wavefront owns
+// 16 F Phases x 64 outputs.
+//
+// The wavefronts form two groups, one of each on every SIMD, that take turns:
+// in every slot between two barriers one group reads its fragments of a phase
+// from LDS while the other multiplies, and then they change over.
+//   slot           0     1     2     3    ...         (Phases == 1)
+//   group 0      read0 mult0 read1 mult1
+//   group 1        -   read0 mult0 read1
+// All wavefronts start the loads of block b + 1 in slot 2 Phases b, when the
+// last reads of block b - 1 (same stage) have ended, and have waited for them
+// when slot 2 Phases (b + 1) begins.
+//
+// LDS keeps a row's 128 bytes in 8 pieces of 16, piece c of row r at place
+// c ^ (r % 8): the lanes of a fragment read 16 rows at one piece, and the
+// permutation spreads these over the banks.  An asynchronous load writes lane
+// after lane, so the permutation is made by the addresses it reads.
+// ---------------------------------------------------------------------------
+
+constexpr int kTiledWaves = 8;
+constexpr uint32_t kBand = 4;  // tiles along q that neighbouring workgroups share P with
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// 16 (4) bytes a lane from base + off to LDS at `to` + 16 (4) lane.  The compiler does not count
+// these loads: lds_arrived() waits for them.  M0 is read one wait state after it is written.
+__device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base));
+}
+__device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base));
+}
+__device__ __forceinline__ void lds_arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Ends a slot: this wavefront's reads of LDS are done, and no instruction moves across.
+__device__ __forceinline__ void end_slot() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int M, typename Out, int WavesQ, int F, int Phases>
+__global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArgs a) {
+    constexpr int WavesP = kTiledWaves / WavesQ, PF = 4, QW = 16 * F * Phases, PW = 16 * PF;
+    constexpr uint32_t BQ = WavesQ * QW, BP = WavesP * PW;
+    constexpr int QLoads = BQ / 64, PLoads = BP / 64;  // rows of 128 bytes: 64 by one load of 512 lanes
+    struct Stage {
+        uint8_t q[BQ * kBlock];
+        uint8_t p[BP * kBlock];
+        float qs[BQ];
+        float ps[BP];  // product: one per 64 columns
+    };
+    __shared__ __attribute__((aligned(128))) Stage stage[2];
+
+    const uint32_t np_tiles = (a.np + BP - 1) / BP;
+    uint32_t tq, tp;
+    {  // bands of kBand tiles along q, and in a band tile after tile along p
+        const uint32_t tile = (uint32_t)xcd_tile(), nq_tiles = gridDim.x / np_tiles;
+        const uint32_t band = tile / (kBand * np_tiles), in = tile - band * kBand * np_tiles;
+        const uint32_t high = min(kBand, nq_tiles - band * kBand);
+        tp = in / high;
+        tq = band * kBand + in - tp * high;
+    }
+    const Work w = find_work<M, BQ>(a, tq, blockIdx.y);
+    if (w.none) return;
+    const uint32_t p0 = tp * BP, np = min(BP, a.np - p0);
+    const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t group = wave / 4, wq = wave % WavesQ, wp = wave / WavesQ;
+    const uint32_t blocks = (uint32_t)(a.ld / kBlock), nb = w.b1 - w.b0;
+
+    f32x4_t acc[Phases * F][PF];
+#pragma unroll
+    for (int i = 0; i < Phases * F; ++i)
+#pragma unroll
+        for (int j = 0; j < PF; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    if (nb != 0) {
+        // rows past the tile's repeat its last one; their sums are not stored
+        const uint32_t lr = lane >> 3, piece = ((lane & 7) ^ lr) * 16;
+        uint32_t qoff[QLoads], poff[PLoads];
+#pragma unroll
+        for (int i = 0; i < QLoads; ++i) qoff[i] = min(64 * i + 8 * wave + lr, w.nq - 1) * (uint32_t)a.ld + piece;
+#pragma unroll
+        for (int i = 0; i < PLoads; ++i) poff[i] = min(64 * i + 8 * wave + lr, np - 1) * (uint32_t)a.ld + piece;
+        const uint8_t* qbase = a.q + (size_t)w.q0 * a.ld + (size_t)w.b0 * kBlock;
+        const uint8_t* pbase = w.p + (size_t)p0 * a.ld + (size_t)w.b0 * kBlock;
+        // scales: one load of wavefronts 0 .. BQ/64 - 1 (Q) and of the last ones (P)
+        constexpr uint32_t PSWaves = M == kProduct ? 1 : BP / 64;
+        static_assert(BQ / 64 + PSWaves <= kTiledWaves, "a wavefront loads scales of one operand");
+        const uint32_t qsrow = min(64 * wave + lane, w.nq - 1), pswave = wave - (kTiledWaves - PSWaves);
+        const uint32_t psrow = M == kProduct ? min(64 * lane, np - 1) / kBlock : min(64 * pswave + lane, np - 1);
+        const uint32_t qsoff = 4 * (M == kProduct ? qsrow * blocks : qsrow);
+        const uint32_t psoff = 4 * (M == kProduct ? psrow * blocks : psrow);
+        const size_t qstep = M == kProduct ? 1 : a.nq, pstep = M == kProduct ? 1 : a.np;
+        const float* qsbase = a.qs + (M == kProduct ? (size_t)w.q0 * blocks + w.b0 : (size_t)w.b0 * a.nq + w.q0);
+        const float* psbase = w.ps + (M == kProduct ? (size_t)(p0 / kBlock) * blocks + w.b0 : (size_t)w.b0 * a.np + p0);
+        static_assert(BP % kBlock == 0, "tiles of P start where a scale of the weight does");
+
+        auto load_stage = [&](uint32_t b) {
+            Stage& s = stage[b & 1];
+            const uint8_t* q = qbase + (size_t)b * kBlock;
+            const uint8_t* p = pbase + (size_t)b * kBlock;
+            const uint32_t at = wave * 1024;
+#pragma unroll
+            for (int i = 0; i < QLoads; ++i) load_lds16(q, qoff[i], lds_address(s.q) + i * 8192 + at);
+#pragma unroll
+            for (int i = 0; i < PLoads; ++i) load_lds16(p, poff[i], lds_address(s.p) + i * 8192 + at);
+            if (wave < BQ / 64) load_lds4(qsbase + b * qstep, qsoff, lds_address(s.qs) + wave * 256);
+            if (wave >= kTiledWaves - PSWaves) load_lds4(psbase + b * pstep, psoff, lds_address(s.ps) + pswave * 256);
+        };
+
+        load_stage(0);
+        lds_arrived();
+        end_slot();
+        if (group == 1) {
+            if (nb > 1) load_stage(1);
+            end_slot();
+        }
+        const uint32_t in_row = l16 * kBlock, lo = ((2 * l4) ^ (l16 & 7)) * 16, hi = ((2 * l4 + 1) ^ (l16 & 7)) * 16;
+        const uint32_t q_at = wq * QW * kBlock + in_row, p_at = wp * PW * kBlock + in_row;
+        for (uint32_t b = 0; b < nb; ++b) {
+            const Stage& s = stage[b & 1];
+            Fragment<Out> pv[PF];
+            float qs[F];
+            f32x4_t ps[PF];
+#pragma unroll
+            for (int ph = 0; ph < Phases; ++ph) {
+                if (group == 0 && ph == 0 && b + 1 < nb) load_stage(b + 1);
+                Fragment<Out> qv[F];
+                if (ph == 0) {
+#pragma unroll
+                    for (int j = 0; j < PF; ++j) {
+                        const uint8_t* r = s.p + p_at + j * 16 * kBlock;
+                        pv[j] = Fragment<Out>(join(*reinterpret_cast<const i32x4_t*>(r + lo),
+                                                   *reinterpret_cast<const i32x4_t*>(r + hi)));
+                        if constexpr (M == kProduct) {
+                            if (j == 0) ps[0][0] = s.ps[wp];
+                        } else {
+                            ps[j] = *reinterpret_cast<const f32x4_t*>(s.ps + wp * PW + 16 * j + 4 * l4);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < F; ++i) {
+                    const uint8_t* r = s.q + q_at + (ph * F + i) * 16 * kBlock;
+                    qv[i] = Fragment<Out>(join(*reinterpret_cast<const i32x4_t*>(r + lo),
+                                               *reinterpret_cast<const i32x4_t*>(r + hi)));
+                    qs[i] = s.qs[wq * QW + (ph * F + i) * 16 + l16];
+                    if constexpr (M == kProduct) qs[i] *= ps[0][0];
+                }
+                if (group == 1 && ph == Phases - 1) lds_arrived();
+                end_slot();
+                if (group == 1 && ph == Phases - 1 && b + 2 < nb) load_stage(b + 2);
+                __builtin_amdgcn_s_setprio(1);
+                // a product's sum is taken up two products later: the matrix cores never wait for it
+                f32x4_t part[F * PF];
+#pragma unroll
+                for (int t = 0; t < F * PF + 2; ++t) {
+                    if (t < F * PF) part[t] = block_sum(pv[t % PF], qv[t / PF]);
+                    if (t >= 2) {
+                        const int i = (t - 2) / PF, j = (t - 2) % PF;
+                        f32x4_t& c = acc[ph * F + i][j];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            c[e] = __builtin_fmaf(part[t - 2][e], M == kProduct ? qs[i] : qs[i] * ps[j][e], c[e]);
+                        asm volatile("" : "+v"(c));  // here, not where the sum is next needed
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                __builtin_amdgcn_s_setprio(0);
+                if (group == 0 && ph == Phases - 1) lds_arrived();
+                end_slot();
+            }
+        }
+        if (group == 0) end_slot();
+    }
+
+    Out* out = static_cast<Out*>(a.out) + w.out;
+#pragma unroll
+    for (int i = 0; i < Phases * F; ++i) {
+        const uint32_t q = wq * QW + 16 * i + l16;
+#pragma unroll
+        for (int j = 0; j < PF; ++j) {
+            const uint32_t p = p0 + wp * PW + 16 * j + 4 * l4;
+            if (q < w.nq && p < a.np)
+                store4(out + (size_t)(w.q0 + q) * a.np + p, acc[i][j], a.np - p, a.np % 4 == 0);
+        }
+    }
+}
+
+template <int M, typename Out, int WavesQ, int F, int Phases>
+hipError_t launch_tiled(const GemmArgs& a, uint32_t tiles_q, uint32_t z, hipStream_t stream) {
+    constexpr uint32_t BP = kTiledWaves / WavesQ * 64;
+    const uint64_t wgs = (uint64_t)tiles_q * ((a.np + BP - 1) / BP);
+    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    return enqueue(gemm_tiled_kernel<M, Out, WavesQ, F, Phases>, dim3((uint32_t)wgs, z), dim3(kTiledWaves * 64),
+                   stream, a);
+}
+
 // Tiles of T rows that any counts can make of `rows` rows in `groups` groups and
 // the rows past them: every group and the rest may end in a short tile.
 uint32_t most_tiles(const GemmArgs& a, uint32_t T) {
     return (uint32_t)((a.rows + (uint64_t)T - 1) / T) + (a.counts ? a.groups : 0);
 }
 
+// Offsets within a tile of up to 256 rows are held in 32 bits.
+bool tiled_offsets(const GemmArgs& a) { return a.ld < (1ull << 23); }
+
 template <typename Out>
 hipError_t launch_product(const GemmArgs& a, hipStream_t stream) {
+    if (a.rows >= 512 && a.np >= 512 && tiled_offsets(a)) {
+        if constexpr (sizeof(Out) == 2) return launch_tiled<kProduct, Out, 2, 4, 2>(a, most_tiles(a, 256), 1, stream);
+        else return launch_tiled<kProduct, Out, 4, 4, 1>(a, most_tiles(a, 256), 1, stream);
+    }
     return launch_split<kProduct, Out, 4, 4>(a, most_tiles(a, 64), 1, stream);
 }
 
@@ -278,6 +489,8 @@ hipError_t launch_wgrad(const uint8_t* yt, const float* ys, size_t n, const uint
                         size_t rows, size_t padded, int groups, const int32_t* counts, float* dw,
                         hipStream_t stream) {
     const GemmArgs a{yt, xt, ys, xs, counts, dw, (uint32_t)groups, (uint32_t)rows, (uint32_t)n, (uint32_t)k, padded};
+    if (n >= 256 && k >= 256 && tiled_offsets(a))
+        return launch_tiled<kWgrad, float, 4, 4, 1>(a, (uint32_t)((n + 255) / 256), (uint32_t)groups, stream);
     return launch_split<kWgrad, float, 4, 4>(a, (uint32_t)((n + 63) / 64), (uint32_t)groups, stream);
 }
 
