@@ -28,6 +28,8 @@
 // Which contraction index a lane's bytes stand for does not matter as long as
 // both operands are loaded alike: lane l holds bytes 32 (l/16) .. + 31 of row
 // l % 16.
+#include <stddef.h>
+
 #include "lpc_ops.hpp"
 
 namespace lpc {
@@ -257,8 +259,8 @@ hipError_t launch_split(const GemmArgs& a, uint32_t tiles_q, uint32_t z, hipStre
 
 // ---------------------------------------------------------------------------
 // tiled: one workgroup of 8 wavefronts per BQ x BP outputs.  Blocks of both
-// operands go to LDS by asynchronous loads, two stages deep; a wavefront owns
-// 16 F Phases x 64 outputs.
+// operands go to LDS by asynchronous loads, two or three stages deep; a
+// wavefront owns 16 F Phases x 64 outputs.
 //
 // The wavefronts form two groups, one of each on every SIMD, that take turns:
 // in every slot between two barriers one group reads its fragments of a phase
@@ -266,14 +268,19 @@ hipError_t launch_split(const GemmArgs& a, uint32_t tiles_q, uint32_t z, hipStre
 //   slot           0     1     2     3    ...         (Phases == 1)
 //   group 0      read0 mult0 read1 mult1
 //   group 1        -   read0 mult0 read1
-// All wavefronts start the loads of block b + 1 in slot 2 Phases b, when the
-// last reads of block b - 1 (same stage) have ended, and have waited for them
-// when slot 2 Phases (b + 1) begins.
+// Loads of a part of LDS start in the slot after its last reads, and are waited
+// for, by every wavefront for its own, in the slot before its first:
+//   Phases == 2, two stages   P, scales and the Q of phase 0 of block c start
+//                   in slot 4 c - 6 and arrive before 4 c, the Q of phase 1
+//                   from 4 c - 4 to 4 c + 2
+//   Phases == 1, three stages  everything from slot 2 c - 4 to 2 c
+// In both a wavefront waits until only one block's worth of loads is on its way.
 //
 // LDS keeps a row's 128 bytes in 8 pieces of 16, piece c of row r at place
-// c ^ (r % 8): the lanes of a fragment read 16 rows at one piece, and the
-// permutation spreads these over the banks.  An asynchronous load writes lane
-// after lane, so the permutation is made by the addresses it reads.
+// c ^ (r % 8), and a fragment's lane reads pieces l/16 and l/16 + 4 of row
+// l % 16: the 16 lanes that LDS serves together then use all its banks.  An
+// asynchronous load writes lane after lane, so the permutation is made by the
+// addresses it reads.
 // ---------------------------------------------------------------------------
 
 constexpr int kTiledWaves = 8;
@@ -284,14 +291,17 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 // 16 (4) bytes a lane from base + off to LDS at `to` + 16 (4) lane.  The compiler does not count
-// these loads: lds_arrived() waits for them.  M0 is read one wait state after it is written.
+// these loads: lds_arrived() waits until at most `Left` of them are on their way.  M0 is read one wait state after it is written.
 __device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base));
 }
 __device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base));
 }
-__device__ __forceinline__ void lds_arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <int Left>
+__device__ __forceinline__ void lds_arrived() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Left) : "memory");
+}
 
 // Ends a slot: this wavefront's reads of LDS are done, and no instruction moves across.
 __device__ __forceinline__ void end_slot() {
@@ -311,7 +321,8 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
         float qs[BQ];
         float ps[BP];  // product: one per 64 columns
     };
-    __shared__ __attribute__((aligned(128))) Stage stage[2];
+    constexpr uint32_t Stages = Phases == 1 ? 3 : 2;
+    __shared__ __attribute__((aligned(128))) Stage stage[Stages];
 
     const uint32_t np_tiles = (a.np + BP - 1) / BP;
     uint32_t tq, tp;
@@ -346,48 +357,75 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
         for (int i = 0; i < PLoads; ++i) poff[i] = min(64 * i + 8 * wave + lr, np - 1) * (uint32_t)a.ld + piece;
         const uint8_t* qbase = a.q + (size_t)w.q0 * a.ld + (size_t)w.b0 * kBlock;
         const uint8_t* pbase = w.p + (size_t)p0 * a.ld + (size_t)w.b0 * kBlock;
-        // scales: one load of wavefronts 0 .. BQ/64 - 1 (Q) and of the last ones (P)
-        constexpr uint32_t PSWaves = M == kProduct ? 1 : BP / 64;
-        static_assert(BQ / 64 + PSWaves <= kTiledWaves, "a wavefront loads scales of one operand");
-        const uint32_t qsrow = min(64 * wave + lane, w.nq - 1), pswave = wave - (kTiledWaves - PSWaves);
-        const uint32_t psrow = M == kProduct ? min(64 * lane, np - 1) / kBlock : min(64 * pswave + lane, np - 1);
-        const uint32_t qsoff = 4 * (M == kProduct ? qsrow * blocks : qsrow);
-        const uint32_t psoff = 4 * (M == kProduct ? psrow * blocks : psrow);
-        const size_t qstep = M == kProduct ? 1 : a.nq, pstep = M == kProduct ? 1 : a.np;
-        const float* qsbase = a.qs + (M == kProduct ? (size_t)w.q0 * blocks + w.b0 : (size_t)w.b0 * a.nq + w.q0);
-        const float* psbase = w.ps + (M == kProduct ? (size_t)(p0 / kBlock) * blocks + w.b0 : (size_t)w.b0 * a.np + p0);
+        // scales: one load a wavefront, of Q's by the first BQ/64 and of P's by the others, which repeat each other's
+        constexpr uint32_t QSWaves = BQ / 64, PSWaves = M == kProduct ? 1 : BP / 64;
+        static_assert(QSWaves + PSWaves <= kTiledWaves, "a wavefront loads scales of one operand");
+        const bool loads_qs = wave < QSWaves;
+        const uint32_t sat = loads_qs ? wave : (wave - QSWaves) % PSWaves;
+        const uint32_t srow = loads_qs             ? min(64 * sat + lane, w.nq - 1)
+                              : M == kProduct ? min(64 * lane, np - 1) / kBlock
+                                              : min(64 * sat + lane, np - 1);
+        const uint32_t soff = 4 * (M == kProduct ? srow * blocks : srow);
+        const size_t sstep = M == kProduct ? 1 : loads_qs ? a.nq : a.np;
+        const float* sbase = (loads_qs ? a.qs : w.ps) +
+                             (M == kProduct ? (size_t)(loads_qs ? w.q0 : p0 / kBlock) * blocks + w.b0
+                                            : w.b0 * sstep + (loads_qs ? w.q0 : p0));
+        const uint32_t sto = (loads_qs ? (uint32_t)offsetof(Stage, qs) : (uint32_t)offsetof(Stage, ps)) + sat * 256;
         static_assert(BP % kBlock == 0, "tiles of P start where a scale of the weight does");
 
-        auto load_stage = [&](uint32_t b) {
-            Stage& s = stage[b & 1];
-            const uint8_t* q = qbase + (size_t)b * kBlock;
-            const uint8_t* p = pbase + (size_t)b * kBlock;
-            const uint32_t at = wave * 1024;
+        // load n of a block's: the scales, P and the Q of phase 0, then (from kEarly on) the Q of phase 1
+        constexpr int kLoads = 1 + PLoads + QLoads, kEarly = kLoads - (Phases == 1 ? 0 : QLoads / 2);
+        static_assert(Phases == 1 || QW == 128, "loads of 64 rows: even ones are phase 0, odd ones phase 1");
+        auto load = [&](int n, uint32_t c, uint32_t at) {
+            const uint32_t to = lds_address(&stage[at]);
+            if (n == 0) {
+                load_lds4(sbase + c * sstep, soff, to + sto);
+            } else if (n <= PLoads) {
+                load_lds16(pbase + (size_t)c * kBlock, poff[n - 1],
+                           to + (uint32_t)offsetof(Stage, p) + (n - 1) * 8192 + wave * 1024);
+            } else {
+                const int m = n - 1 - PLoads;
+                const int i = Phases == 1 ? m : m < QLoads / 2 ? 2 * m : 2 * (m - QLoads / 2) + 1;
+                load_lds16(qbase + (size_t)c * kBlock, qoff[i], to + i * 8192 + wave * 1024);
+            }
+        };
+        auto load_range = [&](int from, int to, uint32_t c, uint32_t at) {
 #pragma unroll
-            for (int i = 0; i < QLoads; ++i) load_lds16(q, qoff[i], lds_address(s.q) + i * 8192 + at);
-#pragma unroll
-            for (int i = 0; i < PLoads; ++i) load_lds16(p, poff[i], lds_address(s.p) + i * 8192 + at);
-            if (wave < BQ / 64) load_lds4(qsbase + b * qstep, qsoff, lds_address(s.qs) + wave * 256);
-            if (wave >= kTiledWaves - PSWaves) load_lds4(psbase + b * pstep, psoff, lds_address(s.ps) + pswave * 256);
+            for (int n = 0; n < kLoads; ++n)
+                if (n >= from && n < to) load(n, c, at);
+        };
+        // before the first reads of a part of block c
+        auto arrived = [&](uint32_t c) {
+            if (c + 1 < nb) lds_arrived<kLoads>();
+            else lds_arrived<0>();
         };
 
-        load_stage(0);
-        lds_arrived();
+        load_range(0, kLoads, 0, 0);
+        if (nb > 1) load_range(0, kEarly, 1, 1);
+        if (nb > 1) lds_arrived<kLoads>();  // what is left: the late ones of block 0 and the early ones of block 1
+        else lds_arrived<0>();
         end_slot();
         if (group == 1) {
-            if (nb > 1) load_stage(1);
+            if (Phases == 2 && nb > 1) load_range(kEarly, kLoads, 1, 1);
+            if (Phases == 1 && nb > 2) load_range(0, kLoads, 2, 2);
             end_slot();
         }
-        const uint32_t in_row = l16 * kBlock, lo = ((2 * l4) ^ (l16 & 7)) * 16, hi = ((2 * l4 + 1) ^ (l16 & 7)) * 16;
+        const uint32_t in_row = l16 * kBlock, lo = (l4 ^ (l16 & 7)) * 16, hi = lo ^ 64;
         const uint32_t q_at = wq * QW * kBlock + in_row, p_at = wp * PW * kBlock + in_row;
+        uint32_t at = 0;  // stage of block b
         for (uint32_t b = 0; b < nb; ++b) {
-            const Stage& s = stage[b & 1];
+            const Stage& s = stage[at];
+            const uint32_t after = at + 1 == Stages ? 0 : at + 1, last = Stages == 2 ? after : 3 - at - after;
             Fragment<Out> pv[PF];
-            float qs[F];
+            float qs[Phases * F];
             f32x4_t ps[PF];
 #pragma unroll
             for (int ph = 0; ph < Phases; ++ph) {
-                if (group == 0 && ph == 0 && b + 1 < nb) load_stage(b + 1);
+                if (group == 0) {
+                    if (Phases == 1 && b + 2 < nb) load_range(0, kLoads, b + 2, last);
+                    if (Phases == 2 && ph == 0 && b + 1 < nb) load_range(kEarly, kLoads, b + 1, after);
+                    if (Phases == 2 && ph == 1 && b + 2 < nb) load_range(0, kEarly, b + 2, at);
+                }
                 Fragment<Out> qv[F];
                 if (ph == 0) {
 #pragma unroll
@@ -395,11 +433,13 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
                         const uint8_t* r = s.p + p_at + j * 16 * kBlock;
                         pv[j] = Fragment<Out>(join(*reinterpret_cast<const i32x4_t*>(r + lo),
                                                    *reinterpret_cast<const i32x4_t*>(r + hi)));
-                        if constexpr (M == kProduct) {
-                            if (j == 0) ps[0][0] = s.ps[wp];
-                        } else {
+                        if constexpr (M == kWgrad)
                             ps[j] = *reinterpret_cast<const f32x4_t*>(s.ps + wp * PW + 16 * j + 4 * l4);
-                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < Phases * F; ++i) {
+                        qs[i] = s.qs[wq * QW + i * 16 + l16];
+                        if constexpr (M == kProduct) qs[i] *= s.ps[wp];
                     }
                 }
 #pragma unroll
@@ -407,12 +447,17 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
                     const uint8_t* r = s.q + q_at + (ph * F + i) * 16 * kBlock;
                     qv[i] = Fragment<Out>(join(*reinterpret_cast<const i32x4_t*>(r + lo),
                                                *reinterpret_cast<const i32x4_t*>(r + hi)));
-                    qs[i] = s.qs[wq * QW + (ph * F + i) * 16 + l16];
-                    if constexpr (M == kProduct) qs[i] *= ps[0][0];
                 }
-                if (group == 1 && ph == Phases - 1) lds_arrived();
+                if (group == 1) {
+                    if (Phases == 2 && ph == 0) arrived(b);
+                    else if (b + 1 < nb) arrived(b + 1);
+                }
                 end_slot();
-                if (group == 1 && ph == Phases - 1 && b + 2 < nb) load_stage(b + 2);
+                if (group == 1) {
+                    if (Phases == 1 && b + 3 < nb) load_range(0, kLoads, b + 3, at);
+                    if (Phases == 2 && ph == 0 && b + 2 < nb) load_range(0, kEarly, b + 2, at);
+                    if (Phases == 2 && ph == 1 && b + 2 < nb) load_range(kEarly, kLoads, b + 2, at);
+                }
                 __builtin_amdgcn_s_setprio(1);
                 // a product's sum is taken up two products later: the matrix cores never wait for it
                 f32x4_t part[F * PF];
@@ -420,8 +465,8 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
                 for (int t = 0; t < F * PF + 2; ++t) {
                     if (t < F * PF) part[t] = block_sum(pv[t % PF], qv[t / PF]);
                     if (t >= 2) {
-                        const int i = (t - 2) / PF, j = (t - 2) % PF;
-                        f32x4_t& c = acc[ph * F + i][j];
+                        const int i = ph * F + (t - 2) / PF, j = (t - 2) % PF;
+                        f32x4_t& c = acc[i][j];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             c[e] = __builtin_fmaf(part[t - 2][e], M == kProduct ? qs[i] : qs[i] * ps[j][e], c[e]);
@@ -430,9 +475,13 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 __builtin_amdgcn_s_setprio(0);
-                if (group == 0 && ph == Phases - 1) lds_arrived();
+                if (group == 0) {
+                    if (Phases == 2 && ph == 0) arrived(b);
+                    else if (b + 1 < nb) arrived(b + 1);
+                }
                 end_slot();
             }
+            at = after;
         }
         if (group == 0) end_slot();
     }
