@@ -63,6 +63,7 @@ struct Fragment<uint16_t> {
     i32x8_t c;
     __device__ Fragment() = default;
     __device__ __forceinline__ explicit Fragment(i32x8_t codes) : c(codes) {}
+    __device__ __forceinline__ void pin() {}
 };
 
 template <>
@@ -80,6 +81,8 @@ struct Fragment<float> {
             h[i / 2][4 * (i % 2) + 3] = hi[1];
         }
     }
+    // the widening is done by here
+    __device__ __forceinline__ void pin() { asm volatile("" : "+v"(h[0]), "+v"(h[1]), "+v"(h[2]), "+v"(h[3])); }
 };
 
 // sums over a block of 128 for 16 x 16 outputs
@@ -448,6 +451,13 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
                     qv[i] = Fragment<Out>(join(*reinterpret_cast<const i32x4_t*>(r + lo),
                                                *reinterpret_cast<const i32x4_t*>(r + hi)));
                 }
+                // widened here, while the other group multiplies
+                if (ph == 0) {
+#pragma unroll
+                    for (int j = 0; j < PF; ++j) pv[j].pin();
+                }
+#pragma unroll
+                for (int i = 0; i < F; ++i) qv[i].pin();
                 if (group == 1) {
                     if (Phases == 2 && ph == 0) arrived(b);
                     else if (b + 1 < nb) arrived(b + 1);
@@ -459,20 +469,42 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
                     if (Phases == 2 && ph == 1 && b + 2 < nb) load_range(kEarly, kLoads, b + 2, at);
                 }
                 __builtin_amdgcn_s_setprio(1);
-                // a product's sum is taken up two products later: the matrix cores never wait for it
+                // element e of product t of this phase, added to its accumulator here and not where that is next needed
                 f32x4_t part[F * PF];
+                auto take_up = [&](int t, int e) {
+                    const int i = ph * F + t / PF, j = t % PF;
+                    float c = __builtin_fmaf(part[t][e], M == kProduct ? qs[i] : qs[i] * ps[j][e], acc[i][j][e]);
+                    asm volatile("" : "+v"(c));
+                    acc[i][j][e] = c;
+                };
+                // A sum is taken up once the matrix core has started on two products after it, between their
+                // instructions: neither the vector unit nor the matrix core then waits for the other.
+                if constexpr (sizeof(Out) == 2) {
 #pragma unroll
-                for (int t = 0; t < F * PF + 2; ++t) {
-                    if (t < F * PF) part[t] = block_sum(pv[t % PF], qv[t / PF]);
-                    if (t >= 2) {
-                        const int i = ph * F + (t - 2) / PF, j = (t - 2) % PF;
-                        f32x4_t& c = acc[i][j];
+                    for (int t = 0; t < F * PF + 2; ++t) {
+                        if (t < F * PF) part[t] = block_sum(pv[t % PF], qv[t / PF]);
+                        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            c[e] = __builtin_fmaf(part[t - 2][e], M == kProduct ? qs[i] : qs[i] * ps[j][e], c[e]);
-                        asm volatile("" : "+v"(c));  // here, not where the sum is next needed
+                            if (t >= 2) take_up(t - 2, e);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < F * PF + 2; t += 2) {
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {  // two products' chains of four instructions in turn
+                            const int u = t + n % 2;
+                            if (t < F * PF) {
+                                if (n < 2) part[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                                part[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pv[u % PF].h[n / 2],
+                                                                                 qv[u / PF].h[n / 2], part[u], 0, 0, 0);
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                            if (t >= 2) take_up(t - 2 + n / 4, n % 4);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
                 }
                 __builtin_amdgcn_s_setprio(0);
                 if (group == 0) {
