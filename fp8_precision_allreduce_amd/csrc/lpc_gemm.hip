@@ -271,12 +271,13 @@ hipError_t launch_split(const GemmArgs& a, uint32_t tiles_q, uint32_t z, hipStre
 //   slot           0     1     2     3    ...         (Phases == 1)
 //   group 0      read0 mult0 read1 mult1
 //   group 1        -   read0 mult0 read1
-// Loads of a part of LDS start in the slot after its last reads, and are waited
-// for, by every wavefront for its own, in the slot before its first:
+// Loads of a part of LDS start in the reading slot after its last reads by either
+// group, and are waited for, by every wavefront for its own, in the slot before
+// its first:
 //   Phases == 2, two stages   P, scales and the Q of phase 0 of block c start
-//                   in slot 4 c - 6 and arrive before 4 c, the Q of phase 1
-//                   from 4 c - 4 to 4 c + 2
-//   Phases == 1, three stages  everything from slot 2 c - 4 to 2 c
+//                   in slot 4 c - 6 (group 1: - 5) and arrive before 4 c, the Q
+//                   of phase 1 from 4 c - 4 (- 3) to 4 c + 2
+//   Phases == 1, three stages  everything from slot 2 c - 4 (- 3) to 2 c
 // In both a wavefront waits until only one block's worth of loads is on its way.
 //
 // LDS keeps a row's 128 bytes in 8 pieces of 16, piece c of row r at place
@@ -408,11 +409,7 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
         if (nb > 1) lds_arrived<kLoads>();  // what is left: the late ones of block 0 and the early ones of block 1
         else lds_arrived<0>();
         end_slot();
-        if (group == 1) {
-            if (Phases == 2 && nb > 1) load_range(kEarly, kLoads, 1, 1);
-            if (Phases == 1 && nb > 2) load_range(0, kLoads, 2, 2);
-            end_slot();
-        }
+        if (group == 1) end_slot();
         const uint32_t in_row = l16 * kBlock, lo = (l4 ^ (l16 & 7)) * 16, hi = lo ^ 64;
         const uint32_t q_at = wq * QW * kBlock + in_row, p_at = wp * PW * kBlock + in_row;
         uint32_t at = 0;  // stage of block b
@@ -424,11 +421,6 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
             f32x4_t ps[PF];
 #pragma unroll
             for (int ph = 0; ph < Phases; ++ph) {
-                if (group == 0) {
-                    if (Phases == 1 && b + 2 < nb) load_range(0, kLoads, b + 2, last);
-                    if (Phases == 2 && ph == 0 && b + 1 < nb) load_range(kEarly, kLoads, b + 1, after);
-                    if (Phases == 2 && ph == 1 && b + 2 < nb) load_range(0, kEarly, b + 2, at);
-                }
                 Fragment<Out> qv[F];
                 if (ph == 0) {
 #pragma unroll
@@ -451,6 +443,10 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
                     qv[i] = Fragment<Out>(join(*reinterpret_cast<const i32x4_t*>(r + lo),
                                                *reinterpret_cast<const i32x4_t*>(r + hi)));
                 }
+                __builtin_amdgcn_sched_barrier(0);
+                if (Phases == 1 && b + 2 < nb) load_range(0, kLoads, b + 2, last);
+                if (Phases == 2 && ph == 0 && b + 1 < nb) load_range(kEarly, kLoads, b + 1, after);
+                if (Phases == 2 && ph == 1 && b + 2 < nb) load_range(0, kEarly, b + 2, at);
                 // widened here, while the other group multiplies
                 if (ph == 0) {
 #pragma unroll
@@ -463,11 +459,6 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
                     else if (b + 1 < nb) arrived(b + 1);
                 }
                 end_slot();
-                if (group == 1) {
-                    if (Phases == 1 && b + 3 < nb) load_range(0, kLoads, b + 3, at);
-                    if (Phases == 2 && ph == 0 && b + 2 < nb) load_range(0, kEarly, b + 2, at);
-                    if (Phases == 2 && ph == 1 && b + 2 < nb) load_range(kEarly, kLoads, b + 2, at);
-                }
                 __builtin_amdgcn_s_setprio(1);
                 // element e of product t of this phase, added to its accumulator here and not where that is next needed
                 f32x4_t part[F * PF];
