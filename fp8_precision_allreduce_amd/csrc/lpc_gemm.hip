@@ -314,32 +314,34 @@ __device__ __forceinline__ void end_slot() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int M, typename Out, int WavesQ, int F, int Phases>
-__global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArgs a) {
-    constexpr int WavesP = kTiledWaves / WavesQ, PF = 4, QW = 16 * F * Phases, PW = 16 * PF;
-    constexpr uint32_t BQ = WavesQ * QW, BP = WavesP * PW;
-    constexpr int QLoads = BQ / 64, PLoads = BP / 64;  // rows of 128 bytes: 64 by one load of 512 lanes
+// Shape of a tile: WavesQ wavefronts along q, each with 16 F Phases x 16 PF outputs.
+template <int WQ, int F_, int Phases_, int PF_>
+struct Shape {
+    static constexpr int WavesQ = WQ, WavesP = kTiledWaves / WQ, F = F_, Phases = Phases_, PF = PF_;
+    static constexpr int QW = 16 * F * Phases, PW = 16 * PF;
+    static constexpr uint32_t BQ = WavesQ * QW, BP = WavesP * PW, Stages = Phases == 1 ? 3 : 2;
     struct Stage {
         uint8_t q[BQ * kBlock];
         uint8_t p[BP * kBlock];
         float qs[BQ];
         float ps[BP];  // product: one per 64 columns
     };
-    constexpr uint32_t Stages = Phases == 1 ? 3 : 2;
-    __shared__ __attribute__((aligned(128))) Stage stage[Stages];
+    static constexpr size_t kBytes = Stages * sizeof(Stage);
+};
+// bf16 out 256 x 256, fp32 out 256 x 128; and the parts that a last round's tiles are split into
+template <typename Out> struct Large : Shape<2, 4, 2, 4> {};
+template <> struct Large<float> : Shape<4, 4, 1, 4> {};
+struct Small : Shape<2, 4, 1, 2> {};
 
-    const uint32_t np_tiles = (a.np + BP - 1) / BP;
-    uint32_t tq, tp;
-    {  // bands of kBand tiles along q, and in a band tile after tile along p
-        const uint32_t tile = (uint32_t)xcd_tile(), nq_tiles = gridDim.x / np_tiles;
-        const uint32_t band = tile / (kBand * np_tiles), in = tile - band * kBand * np_tiles;
-        const uint32_t high = min(kBand, nq_tiles - band * kBand);
-        tp = in / high;
-        tq = band * kBand + in - tp * high;
-    }
-    const Work w = find_work<M, BQ>(a, tq, blockIdx.y);
-    if (w.none) return;
-    const uint32_t p0 = tp * BP, np = min(BP, a.np - p0);
+// outputs [w.q0, + w.nq) x [p0, + BP)
+template <int M, typename Out, typename S>
+__device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t p0, uint8_t* lds) {
+    constexpr int WavesQ = S::WavesQ, F = S::F, Phases = S::Phases, PF = S::PF, QW = S::QW, PW = S::PW;
+    constexpr uint32_t BQ = S::BQ, BP = S::BP, Stages = S::Stages;
+    constexpr int QLoads = BQ / 64, PLoads = BP / 64;  // rows of 128 bytes: 64 by one load of 512 lanes
+    using Stage = typename S::Stage;
+    Stage* stage = reinterpret_cast<Stage*>(lds);
+    const uint32_t np = min(BP, a.np - p0);
     const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const uint32_t group = wave / 4, wq = wave % WavesQ, wp = wave / WavesQ;
@@ -434,7 +436,7 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
 #pragma unroll
                     for (int i = 0; i < Phases * F; ++i) {
                         qs[i] = s.qs[wq * QW + i * 16 + l16];
-                        if constexpr (M == kProduct) qs[i] *= s.ps[wp];
+                        if constexpr (M == kProduct) qs[i] *= s.ps[wp * PW / 64];
                     }
                 }
 #pragma unroll
@@ -522,13 +524,70 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_tiled_kernel(GemmArg
     }
 }
 
-template <int M, typename Out, int WavesQ, int F, int Phases>
-hipError_t launch_tiled(const GemmArgs& a, uint32_t tiles_q, uint32_t z, hipStream_t stream) {
-    constexpr uint32_t BP = kTiledWaves / WavesQ * 64;
-    const uint64_t wgs = (uint64_t)tiles_q * ((a.np + BP - 1) / BP);
+// Tile number t of tiles_q x tiles_p: bands of kBand tiles along q, and in a band tile after tile along p.
+__device__ __forceinline__ uint2 in_bands(uint32_t t, uint32_t tiles_q, uint32_t tiles_p) {
+    const uint32_t band = t / (kBand * tiles_p), in = t - band * kBand * tiles_p;
+    const uint32_t high = min(kBand, tiles_q - band * kBand), tp = in / high;
+    return make_uint2(band * kBand + in - tp * high, tp);
+}
+
+// A workgroup has a CU to itself, and each XCD works through its own run of tiles, 32 at a time.  Where a last round
+// would leave three quarters of the CUs without a tile, or a product has tiles for half of them at most, these tiles
+// are split into parts of 128 x 128, which take about a third of a tile's time.  Product 16,384 x 7168 x 4096 over 8
+// groups, 136 tiles an XCD: 487 us against 524; 512 x 8192 x 8192, 8 tiles an XCD: 44 us against 89.  How many tiles the
+// counts make is known here and not on the host.
+constexpr uint32_t kXcds = 8, kXcdCus = 32, kMostSplit = kXcdCus / 2;
+
+template <typename Out>
+__global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_product_kernel(GemmArgs a) {
+    using L = Large<Out>;
+    constexpr uint32_t PartsQ = L::BQ / Small::BQ, PartsP = L::BP / Small::BP, Parts = PartsQ * PartsP;
+    __shared__ __attribute__((aligned(128))) uint8_t lds[L::kBytes > Small::kBytes ? L::kBytes : Small::kBytes];
+    const uint32_t tiles_q = count_tiles(a.counts, a.groups, a.rows, L::BQ), tiles_p = (a.np + L::BP - 1) / L::BP;
+    const uint32_t x = blockIdx.x % kXcds, k = blockIdx.x / kXcds;
+    const uint32_t all = tiles_q * tiles_p, rest = all % kXcds;
+    const uint32_t first = x * (all / kXcds) + min(x, rest), mine = all / kXcds + (x < rest);
+    const uint32_t last = mine % kXcdCus, split = last <= (mine < kXcdCus ? kMostSplit : kMostSplit / 2) ? last : 0;
+    const uint32_t whole = mine - split;
+    if (k < whole) {
+        const uint2 t = in_bands(first + k, tiles_q, tiles_p);
+        tile<kProduct, Out, L>(a, find_work<kProduct, L::BQ>(a, t.x, 0), t.y * L::BP, lds);
+    } else if (k < whole + split * Parts) {
+        const uint32_t n = (k - whole) / Parts, part = (k - whole) % Parts;
+        const uint2 t = in_bands(first + whole + n, tiles_q, tiles_p);
+        Work w = find_work<kProduct, L::BQ>(a, t.x, 0);
+        const uint32_t q = part / PartsP * Small::BQ, p0 = t.y * L::BP + part % PartsP * Small::BP;
+        if (q >= w.nq || p0 >= a.np) return;
+        w.q0 += q;
+        w.nq = min(w.nq - q, Small::BQ);
+        tile<kProduct, Out, Small>(a, w, p0, lds);
+    }
+}
+
+__global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_wgrad_kernel(GemmArgs a) {
+    using L = Large<float>;
+    __shared__ __attribute__((aligned(128))) uint8_t lds[L::kBytes];
+    const uint32_t tiles_p = (a.np + L::BP - 1) / L::BP;
+    const uint2 t = in_bands((uint32_t)xcd_tile(), gridDim.x / tiles_p, tiles_p);
+    tile<kWgrad, float, L>(a, find_work<kWgrad, L::BQ>(a, t.x, blockIdx.y), t.y * L::BP, lds);
+}
+
+template <typename Out>
+hipError_t launch_tiled_product(const GemmArgs& a, uint32_t most_tiles_q, hipStream_t stream) {
+    using L = Large<Out>;
+    constexpr uint32_t Parts = (L::BQ / Small::BQ) * (L::BP / Small::BP);
+    const uint64_t tiles = (uint64_t)most_tiles_q * ((a.np + L::BP - 1) / L::BP);
+    // fewer tiles than that can make more parts: up to kMostSplit tiles of every XCD are split
+    const uint64_t wgs = kXcds * ((tiles + kXcds - 1) / kXcds + kMostSplit * (Parts - 1));
     if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
-    return enqueue(gemm_tiled_kernel<M, Out, WavesQ, F, Phases>, dim3((uint32_t)wgs, z), dim3(kTiledWaves * 64),
-                   stream, a);
+    return enqueue(gemm_product_kernel<Out>, dim3((uint32_t)wgs), dim3(kTiledWaves * 64), stream, a);
+}
+
+hipError_t launch_tiled_wgrad(const GemmArgs& a, uint32_t z, hipStream_t stream) {
+    using L = Large<float>;
+    const uint64_t wgs = (uint64_t)((a.nq + L::BQ - 1) / L::BQ) * ((a.np + L::BP - 1) / L::BP);
+    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    return enqueue(gemm_wgrad_kernel, dim3((uint32_t)wgs, z), dim3(kTiledWaves * 64), stream, a);
 }
 
 // Tiles of T rows that any counts can make of `rows` rows in `groups` groups and
@@ -543,8 +602,7 @@ bool tiled_offsets(const GemmArgs& a) { return a.ld < (1ull << 23); }
 template <typename Out>
 hipError_t launch_product(const GemmArgs& a, hipStream_t stream) {
     if (a.rows >= 512 && a.np >= 512 && tiled_offsets(a)) {
-        if constexpr (sizeof(Out) == 2) return launch_tiled<kProduct, Out, 2, 4, 2>(a, most_tiles(a, 256), 1, stream);
-        else return launch_tiled<kProduct, Out, 4, 4, 1>(a, most_tiles(a, 256), 1, stream);
+        return launch_tiled_product<Out>(a, most_tiles(a, Large<Out>::BQ), stream);
     }
     return launch_split<kProduct, Out, 4, 4>(a, most_tiles(a, 64), 1, stream);
 }
@@ -562,7 +620,7 @@ hipError_t launch_wgrad(const uint8_t* yt, const float* ys, size_t n, const uint
                         hipStream_t stream) {
     const GemmArgs a{yt, xt, ys, xs, counts, dw, (uint32_t)groups, (uint32_t)rows, (uint32_t)n, (uint32_t)k, padded};
     if (n >= 256 && k >= 256 && tiled_offsets(a))
-        return launch_tiled<kWgrad, float, 4, 4, 1>(a, (uint32_t)((n + 255) / 256), (uint32_t)groups, stream);
+        return launch_tiled_wgrad(a, (uint32_t)groups, stream);
     return launch_split<kWgrad, float, 4, 4>(a, (uint32_t)((n + 63) / 64), (uint32_t)groups, stream);
 }
 

@@ -65,6 +65,18 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t* __restrict__ count
     return {groups, rows, 0u, before, n};
 }
 
+// Tiles of all groups and of the rows past the last one.
+__device__ __forceinline__ uint32_t count_tiles(const int32_t* __restrict__ counts, uint32_t groups, uint32_t rows,
+                                                uint32_t T) {
+    uint32_t row = 0, tiles = 0;
+    for (uint32_t g = 0; g < groups; ++g) {
+        const uint32_t c = group_rows(counts, g, rows - row);
+        row += c;
+        tiles += (c + T - 1) / T;
+    }
+    return tiles + (rows - row + T - 1) / T;
+}
+
 // First tile and number of tiles of group g.
 __device__ __forceinline__ GroupTile find_group(const int32_t* __restrict__ counts, uint32_t rows, uint32_t T,
                                                 uint32_t g) {
