@@ -26,8 +26,8 @@
 //         same data.  Half the rate of the first.
 //
 // Which contraction index a lane's bytes stand for does not matter as long as
-// both operands are loaded alike: lane l holds bytes 32 (l/16) .. + 31 of row
-// l % 16.
+// both operands are loaded alike: lane l holds bytes 16 (l/16) .. + 15 of each
+// half of row l % 16's block.
 #include <stddef.h>
 
 #include "lpc_ops.hpp"
@@ -102,10 +102,10 @@ __device__ __forceinline__ i32x8_t join(i32x4_t a, i32x4_t b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// 32 bytes of one row
+// 16 bytes of each half of a row's block, by lane 16 (l/16) of it: the four lanes of a row read 64 bytes in one run
 __device__ __forceinline__ i32x8_t load_fragment(const uint8_t* __restrict__ p) {
     const i32x4_t* v = reinterpret_cast<const i32x4_t*>(p);
-    return join(v[0], v[1]);
+    return join(v[0], v[4]);
 }
 
 // four neighbouring outputs; `wide`: np is a multiple of 4, so all four exist and are aligned
@@ -193,10 +193,10 @@ __global__ __launch_bounds__(kSplitWaves * 64) void gemm_split_kernel(GemmArgs a
 #pragma unroll
     for (int f = 0; f < QF; ++f) {  // rows past the tile's repeat its last one; their sums are not stored
         qi[f] = w.q0 + min(16 * f + l16, w.nq - 1);
-        qrow[f] = a.q + (size_t)qi[f] * a.ld + 32 * l4;
+        qrow[f] = a.q + (size_t)qi[f] * a.ld + 16 * l4;
     }
 #pragma unroll
-    for (int f = 0; f < PF; ++f) prow[f] = w.p + (size_t)min(p0 + 16 * f + l16, a.np - 1) * a.ld + 32 * l4;
+    for (int f = 0; f < PF; ++f) prow[f] = w.p + (size_t)min(p0 + 16 * f + l16, a.np - 1) * a.ld + 16 * l4;
     const uint32_t blocks = (uint32_t)(a.ld / kBlock);
 
     f32x4_t acc[QF][PF];
@@ -261,6 +261,176 @@ hipError_t launch_split(const GemmArgs& a, uint32_t tiles_q, uint32_t z, hipStre
 }
 
 // ---------------------------------------------------------------------------
+// asynchronous loads to LDS
+//
+// LDS keeps a row's 128 bytes in 8 pieces of 16, piece c of row r at place
+// c ^ (r % 8), and a fragment's lane reads pieces l/16 and l/16 + 4 of row
+// l % 16: the 16 lanes that LDS serves together then use all its banks.  An
+// asynchronous load writes lane after lane, so the permutation is made by the
+// addresses it reads.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// 16 (4) bytes a lane from base + off to LDS at `to` + 16 (4) lane.  The compiler does not count
+// these loads: lds_arrived() waits until at most `Left` of them are on their way.  M0 is read one wait state after it is written.
+__device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base));
+}
+__device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base));
+}
+template <int Left>
+__device__ __forceinline__ void lds_arrived() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Left) : "memory");
+}
+
+// a lane's part of a fragment from its row `r` in LDS; lo: where that row's piece l/16 is
+__device__ __forceinline__ i32x8_t read_fragment(const uint8_t* r, uint32_t lo) {
+    return join(*reinterpret_cast<const i32x4_t*>(r + lo), *reinterpret_cast<const i32x4_t*>(r + (lo ^ 64)));
+}
+
+// ---------------------------------------------------------------------------
+// narrow: 16 QF x 16 PF outputs per workgroup for few rows or few outputs.  Its
+// wavefronts take every kNarrowWaves-th block, each through stages of LDS of its
+// own that asynchronous loads fill Depth - 1 blocks ahead, and never wait for
+// each other; their sums are joined through LDS, in the wavefronts' order.
+//
+// Reading a weight once is all a small product is about.  A load instruction
+// costs about 4 cycles for every line it touches: 8 lines where lanes run along
+// the rows, as here, 16 where a wavefront gathers a fragment and 64 for a column
+// of scales, which is why the scales of 64 blocks are brought in first, along
+// their rows.  32 x 8192 x 8192: 13 us (5 TB/s) against 20 with gathered fragments.
+// ---------------------------------------------------------------------------
+
+constexpr int kNarrowWaves = 4;
+constexpr uint32_t kSpan = 64;  // blocks whose scales are in LDS at a time
+
+template <typename Out, int QF, int PF, int Depth>
+__global__ __launch_bounds__(kNarrowWaves * 64) void gemm_narrow_kernel(GemmArgs a) {
+    constexpr uint32_t BQ = 16 * QF, BP = 16 * PF, kStage = (BQ + BP) * kBlock;
+    constexpr int kLoads = (BQ + BP) / 8, kAhead = (Depth - 1) * kLoads;
+    constexpr uint32_t kRing = kNarrowWaves * Depth * kStage, kSums = kNarrowWaves * QF * PF * 64 * 16;
+    static_assert(BP <= kBlock && kBlock % BP == 0, "one scale of the weight");
+    static_assert(kAhead < 64, "what the wait instruction can count");
+    __shared__ __attribute__((aligned(128))) uint8_t lds[kRing > kSums ? kRing : kSums];
+    __shared__ float qscale[BQ][kSpan + 1], pscale[kSpan];  // 16 rows of a column: 16 banks
+
+    const uint32_t np_tiles = (a.np + BP - 1) / BP, t = (uint32_t)xcd_tile();
+    const Work w = find_work<kProduct, BQ>(a, t / np_tiles, 0);
+    if (w.none) return;
+    const uint32_t p0 = t % np_tiles * BP, np = min(BP, a.np - p0);
+    const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t blocks = (uint32_t)(a.ld / kBlock);
+    uint8_t* ring = lds + wave * Depth * kStage;
+
+    // rows past the tile's repeat its last one; their sums are not stored
+    const uint32_t lr = lane >> 3, piece = ((lane & 7) ^ lr) * 16;
+    uint32_t off[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+        off[i] = (i < (int)BQ / 8 ? min(8 * i + lr, w.nq - 1) : min(8 * i + lr - BQ, np - 1)) * (uint32_t)a.ld + piece;
+    const uint8_t* qbase = a.q + (size_t)w.q0 * a.ld;
+    const uint8_t* pbase = w.p + (size_t)p0 * a.ld;
+    auto load_block = [&](uint32_t b, uint32_t stage) {
+        const uint32_t to = lds_address(ring) + stage * kStage;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            load_lds16((i < (int)BQ / 8 ? qbase : pbase) + (size_t)b * kBlock, off[i], to + i * 1024);
+    };
+
+    f32x4_t acc[QF][PF];
+#pragma unroll
+    for (int i = 0; i < QF; ++i)
+#pragma unroll
+        for (int j = 0; j < PF; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const uint32_t in_row = l16 * kBlock, lo = (l4 ^ (l16 & 7)) * 16;
+    for (uint32_t c0 = w.b0; c0 < w.b1; c0 += kSpan) {
+        const uint32_t span = min(kSpan, w.b1 - c0);
+        const uint32_t mine = wave < span ? (span - wave + kNarrowWaves - 1) / kNarrowWaves : 0;  // blocks
+        if (c0 != w.b0) __syncthreads();  // the last span's scales are read
+        const uint32_t soff = 4 * min(lane, span - 1);
+#pragma unroll
+        for (uint32_t i = 0; i < BQ / kNarrowWaves; ++i) {
+            const uint32_t r = i * kNarrowWaves + wave;
+            load_lds4(a.qs + (size_t)(w.q0 + min(r, w.nq - 1)) * blocks + c0, soff, lds_address(qscale[r]));
+        }
+        load_lds4(w.ps + (size_t)(p0 / kBlock) * blocks + c0, soff, lds_address(pscale));  // the same by every wavefront
+#pragma unroll
+        for (int d = 0; d < Depth - 1; ++d)
+            if (d < (int)mine) load_block(c0 + wave + d * kNarrowWaves, d);
+        if (mine >= Depth - 1) lds_arrived<kAhead>();
+        else lds_arrived<0>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        uint32_t stage = 0;
+        for (uint32_t i = 0; i < mine; ++i) {
+            // the stage that was read last; those reads are in registers
+            if (i + Depth - 1 < mine) {
+                load_block(c0 + wave + (i + Depth - 1) * kNarrowWaves, stage == 0 ? Depth - 1 : stage - 1);
+                lds_arrived<kAhead>();
+            } else {
+                lds_arrived<0>();
+            }
+            const uint8_t* q = ring + stage * kStage + in_row;
+            const uint32_t in = wave + i * kNarrowWaves;
+            i32x8_t qc[QF], pc[PF];
+            float qs[QF];
+            const float ps = pscale[in];
+#pragma unroll
+            for (int f = 0; f < QF; ++f) {
+                qc[f] = read_fragment(q + f * 16 * kBlock, lo);
+                qs[f] = qscale[16 * f + l16][in];
+            }
+#pragma unroll
+            for (int f = 0; f < PF; ++f) pc[f] = read_fragment(q + (BQ + f * 16) * kBlock, lo);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            Fragment<Out> qv[QF];
+#pragma unroll
+            for (int f = 0; f < QF; ++f) qv[f] = Fragment<Out>(qc[f]);
+#pragma unroll
+            for (int j = 0; j < PF; ++j) {
+                const Fragment<Out> pv(pc[j]);
+#pragma unroll
+                for (int f = 0; f < QF; ++f) {
+                    const f32x4_t part = block_sum(pv, qv[f]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[f][j][e] = __builtin_fmaf(part[e], qs[f] * ps, acc[f][j][e]);
+                }
+            }
+            stage = stage + 1 == Depth ? 0 : stage + 1;
+        }
+    }
+
+    __syncthreads();
+    f32x4_t(*sums)[QF * PF][64] = reinterpret_cast<f32x4_t(*)[QF * PF][64]>(lds);
+#pragma unroll
+    for (int i = 0; i < QF; ++i)
+#pragma unroll
+        for (int j = 0; j < PF; ++j) sums[wave][i * PF + j][lane] = acc[i][j];
+    __syncthreads();
+    Out* out = static_cast<Out*>(a.out);
+    for (uint32_t f = wave; f < QF * PF; f += kNarrowWaves) {
+        f32x4_t v = sums[0][f][lane];
+#pragma unroll
+        for (int s = 1; s < kNarrowWaves; ++s) v += sums[s][f][lane];
+        const uint32_t q = f / PF * 16 + l16, p = p0 + f % PF * 16 + 4 * l4;
+        if (q < w.nq && p < a.np) store4(out + (size_t)(w.q0 + q) * a.np + p, v, a.np - p, a.np % 4 == 0);
+    }
+}
+
+template <typename Out, int QF, int PF, int Depth>
+hipError_t launch_narrow(const GemmArgs& a, uint32_t tiles_q, hipStream_t stream) {
+    const uint64_t wgs = (uint64_t)tiles_q * ((a.np + 16 * PF - 1) / (16 * PF));
+    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    return enqueue(gemm_narrow_kernel<Out, QF, PF, Depth>, dim3((uint32_t)wgs), dim3(kNarrowWaves * 64), stream, a);
+}
+
+// ---------------------------------------------------------------------------
 // tiled: one workgroup of 8 wavefronts per BQ x BP outputs.  Blocks of both
 // operands go to LDS by asynchronous loads, two or three stages deep; a
 // wavefront owns 16 F Phases x 64 outputs.
@@ -279,33 +449,10 @@ hipError_t launch_split(const GemmArgs& a, uint32_t tiles_q, uint32_t z, hipStre
 //                   of phase 1 from 4 c - 4 (- 3) to 4 c + 2
 //   Phases == 1, three stages  everything from slot 2 c - 4 (- 3) to 2 c
 // In both a wavefront waits until only one block's worth of loads is on its way.
-//
-// LDS keeps a row's 128 bytes in 8 pieces of 16, piece c of row r at place
-// c ^ (r % 8), and a fragment's lane reads pieces l/16 and l/16 + 4 of row
-// l % 16: the 16 lanes that LDS serves together then use all its banks.  An
-// asynchronous load writes lane after lane, so the permutation is made by the
-// addresses it reads.
 // ---------------------------------------------------------------------------
 
 constexpr int kTiledWaves = 8;
 constexpr uint32_t kBand = 4;  // tiles along q that neighbouring workgroups share P with
-
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
-}
-
-// 16 (4) bytes a lane from base + off to LDS at `to` + 16 (4) lane.  The compiler does not count
-// these loads: lds_arrived() waits until at most `Left` of them are on their way.  M0 is read one wait state after it is written.
-__device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base));
-}
-__device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base));
-}
-template <int Left>
-__device__ __forceinline__ void lds_arrived() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Left) : "memory");
-}
 
 // Ends a slot: this wavefront's reads of LDS are done, and no instruction moves across.
 __device__ __forceinline__ void end_slot() {
@@ -412,7 +559,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
         else lds_arrived<0>();
         end_slot();
         if (group == 1) end_slot();
-        const uint32_t in_row = l16 * kBlock, lo = (l4 ^ (l16 & 7)) * 16, hi = lo ^ 64;
+        const uint32_t in_row = l16 * kBlock, lo = (l4 ^ (l16 & 7)) * 16;
         const uint32_t q_at = wq * QW * kBlock + in_row, p_at = wp * PW * kBlock + in_row;
         uint32_t at = 0;  // stage of block b
         for (uint32_t b = 0; b < nb; ++b) {
@@ -428,8 +575,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
 #pragma unroll
                     for (int j = 0; j < PF; ++j) {
                         const uint8_t* r = s.p + p_at + j * 16 * kBlock;
-                        pv[j] = Fragment<Out>(join(*reinterpret_cast<const i32x4_t*>(r + lo),
-                                                   *reinterpret_cast<const i32x4_t*>(r + hi)));
+                        pv[j] = Fragment<Out>(read_fragment(r, lo));
                         if constexpr (M == kWgrad)
                             ps[j] = *reinterpret_cast<const f32x4_t*>(s.ps + wp * PW + 16 * j + 4 * l4);
                     }
@@ -442,8 +588,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
 #pragma unroll
                 for (int i = 0; i < F; ++i) {
                     const uint8_t* r = s.q + q_at + (ph * F + i) * 16 * kBlock;
-                    qv[i] = Fragment<Out>(join(*reinterpret_cast<const i32x4_t*>(r + lo),
-                                               *reinterpret_cast<const i32x4_t*>(r + hi)));
+                    qv[i] = Fragment<Out>(read_fragment(r, lo));
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 if (Phases == 1 && b + 2 < nb) load_range(0, kLoads, b + 2, last);
@@ -532,10 +677,9 @@ __device__ __forceinline__ uint2 in_bands(uint32_t t, uint32_t tiles_q, uint32_t
 }
 
 // A workgroup has a CU to itself, and each XCD works through its own run of tiles, 32 at a time.  Where a last round
-// would leave three quarters of the CUs without a tile, or a product has tiles for half of them at most, these tiles
-// are split into parts of 128 x 128, which take about a third of a tile's time.  Product 16,384 x 7168 x 4096 over 8
-// groups, 136 tiles an XCD: 487 us against 524; 512 x 8192 x 8192, 8 tiles an XCD: 44 us against 89.  How many tiles the
-// counts make is known here and not on the host.
+// would leave half of the CUs or more without a tile, its tiles are split into parts of 128 x 128, which take about a
+// third of a tile's time.  Product 16,384 x 7168 x 4096 over 8 groups, 136 tiles an XCD: 487 us against 524; 512 x
+// 8192 x 8192, 8 tiles an XCD: 44 us against 89.  How many tiles the counts make is known here and not on the host.
 constexpr uint32_t kXcds = 8, kXcdCus = 32, kMostSplit = kXcdCus / 2;
 
 template <typename Out>
@@ -547,7 +691,7 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_product_kernel(GemmA
     const uint32_t x = blockIdx.x % kXcds, k = blockIdx.x / kXcds;
     const uint32_t all = tiles_q * tiles_p, rest = all % kXcds;
     const uint32_t first = x * (all / kXcds) + min(x, rest), mine = all / kXcds + (x < rest);
-    const uint32_t last = mine % kXcdCus, split = last <= (mine < kXcdCus ? kMostSplit : kMostSplit / 2) ? last : 0;
+    const uint32_t last = mine % kXcdCus, split = last <= kMostSplit ? last : 0;
     const uint32_t whole = mine - split;
     if (k < whole) {
         const uint2 t = in_bands(first + k, tiles_q, tiles_p);
@@ -599,12 +743,25 @@ uint32_t most_tiles(const GemmArgs& a, uint32_t T) {
 // Offsets within a tile of up to 256 rows are held in 32 bits.
 bool tiled_offsets(const GemmArgs& a) { return a.ld < (1ull << 23); }
 
+// By the number of workgroups, one to a CU and 256 CUs (times in us of 64 x 64, 64 x 32 and 32 x 32 outputs and of
+// large tiles):
+//   up to 16 rows            gathered fragments: 1 x 8192 x 8192 12
+//   more than 384 of 64 x 64 large tiles: 256 x 8192 x 8192 46 / 50 / - / 40
+//   more than 128            64 x 64: 128 x 8192 x 8192 24 / 27 / - / 39, 777 x 1152 x 1000 8.2 / 9.1 / - / 9.2
+//   more than 128 of 64 x 32 64 x 32: 64 x 8192 x 8192 20 / 14 / - / 38
+//   otherwise                32 x 32: 32 x 8192 x 8192 - / - / 13 / 38
+// Rows of 8 MiB and more, whose offsets within a tile do not fit 32 bits, are gathered.
 template <typename Out>
 hipError_t launch_product(const GemmArgs& a, hipStream_t stream) {
-    if (a.rows >= 512 && a.np >= 512 && tiled_offsets(a)) {
-        return launch_tiled_product<Out>(a, most_tiles(a, Large<Out>::BQ), stream);
+    if (a.rows <= 16) return launch_split<kProduct, Out, 1, 1>(a, most_tiles(a, 16), 1, stream);
+    if (!tiled_offsets(a)) return launch_split<kProduct, Out, 4, 4>(a, most_tiles(a, 64), 1, stream);
+    if (a.rows > 32) {
+        const uint64_t high = most_tiles(a, 64), wide = (a.np + 63) / 64, narrow = (a.np + 31) / 32;
+        if (high * wide > 384) return launch_tiled_product<Out>(a, most_tiles(a, Large<Out>::BQ), stream);
+        if (high * wide > 128) return launch_narrow<Out, 4, 4, 2>(a, (uint32_t)high, stream);
+        if (high * narrow > 128) return launch_narrow<Out, 4, 2, 2>(a, (uint32_t)high, stream);
     }
-    return launch_split<kProduct, Out, 4, 4>(a, most_tiles(a, 64), 1, stream);
+    return launch_narrow<Out, 2, 2, 4>(a, most_tiles(a, 32), stream);
 }
 
 }  // namespace

@@ -123,6 +123,30 @@ def test_gemm_large_tiles(dev, rows, k, n, counts):
     check_gemm(dev, rows, k, n, counts, torch.bfloat16)
 
 
+@pytest.mark.parametrize("out_t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,k,n,counts", [
+    (20, 16512, 40, None), (40, 8320, 96, None), (70, 8448, 300, [33, 0, 36]), (65, 512, 8192, None),  # 32 x 32
+    (33, 9216, 4160, None), (90, 256, 3300, [40, 20, 5]),                                               # 64 x 32
+    (100, 8320, 4160, None), (512, 384, 1100, [1, 200, 0, 300]),                                        # 64 x 64
+    (256, 896, 6500, None), (3000, 128, 700, None), (2100, 1536, 1700, [700, 0, 3, 1200])])             # large tiles
+def test_gemm_kinds_of_tiles(dev, rows, k, n, counts, out_t):
+    check_gemm(dev, rows, k, n, counts, out_t)
+
+
+def test_gemm_long_rows_are_gathered(dev):
+    """Rows of 8 MiB, more of them than a gathered decode has."""
+    rows, n, k = 40, 33, 1 << 23
+    say("gemm 40 rows of 8 MiB")
+    x = torch.full((rows, k), 0x38, dtype=torch.uint8, device=dev)      # 1.0
+    w = torch.zeros(n, k, dtype=torch.uint8, device=dev)
+    w[n - 1, :] = 0x30                                                  # 0.5
+    out = torch.empty(rows, n, device=dev)
+    lpc.lpc_gemm_fp8(x, torch.ones(rows, k // BLOCK, device=dev), w, torch.ones(1, k // BLOCK, device=dev), out)
+    want = torch.zeros(rows, n)
+    want[:, n - 1] = k / 2
+    assert torch.equal(out.cpu(), want)
+
+
 def test_gemm_many_groups(dev):
     rng = np.random.RandomState(3)
     counts = [int(c) for c in rng.multinomial(400, np.full(130, 1 / 130))]
