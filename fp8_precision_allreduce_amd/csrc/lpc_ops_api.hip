@@ -127,7 +127,8 @@ lpc_status lpc_router_forward(const void* logits, lpc_dtype in, size_t rows, int
                               float* load, float* slope, float* loss, void* workspace, size_t workspace_bytes,
                               hipStream_t stream) {
     if (bad_dtype(in)) return LPC_ERR_DTYPE;
-    if (any_null(load, slope, loss) || !counts || !workspace) return LPC_ERR_NULL;
+    if (any_null(load, slope, loss) || !counts) return LPC_ERR_NULL;
+    if (!workspace && lpc_router_workspace_bytes(rows, experts) != 0) return LPC_ERR_NULL;
     if (rows != 0 && (!logits || !out_experts || !gates)) return LPC_ERR_NULL;
     if (any_misaligned(logits, out_experts, gates, counts, load, slope, workspace) || misaligned4(loss))
         return LPC_ERR_ALIGN;

@@ -138,6 +138,7 @@ __device__ __forceinline__ float largest(const float (&x)[Per]) {
 // launch its valid rows, its counts and its sums of p.
 constexpr size_t kHeader = 512;
 constexpr uint32_t kFinishExperts = 16;  // experts of one workgroup of the finishing launch
+constexpr uint32_t kMostWgs = 256;       // of the rows launch
 
 struct Partials {
     uint32_t* ticket;
@@ -186,28 +187,32 @@ __device__ __forceinline__ float finish_expert(const RouterArgs& a, uint32_t e, 
     return up * load;
 }
 
-// the sum over the workgroup's 256 lanes, in a fixed order, in lane 0
+// the sum over the workgroup's lanes, in a fixed order, in lane 0
+template <int Threads>
 __device__ __forceinline__ float workgroup_sum(float v, float* lds) {
     lds[threadIdx.x] = v;
     __syncthreads();
-    for (int d = kThreads / 2; d > 0; d >>= 1) {
+    for (int d = Threads / 2; d > 0; d >>= 1) {
         if ((int)threadIdx.x < d) lds[threadIdx.x] += lds[threadIdx.x + d];
         __syncthreads();
     }
     return lds[0];
 }
 
-template <typename In, int Lanes, int Per>
-__global__ __launch_bounds__(kThreads) void router_rows_kernel(RouterArgs a) {
+// Bound by its vector instructions and their latency, most of them the k passes: with 16 wavefronts a CU instead of 4,
+// and as many partial sums, 16,384 x 256 takes 14 us against 21.
+template <typename In, int Lanes, int Per, int Threads>
+__global__ __launch_bounds__(Threads) void router_rows_kernel(RouterArgs a) {
     using L = Layout<Lanes, Per>;
-    constexpr uint32_t kGroups = kThreads / Lanes, kWidth = Lanes * Per;
+    constexpr uint32_t kGroups = Threads / Lanes, kWidth = Lanes * Per;
+    constexpr uint32_t kSlices = Threads > (int)kWidth ? Threads / kWidth < kGroups ? Threads / kWidth : kGroups : 1;
     __shared__ float sums[kGroups][kWidth];
     __shared__ uint32_t counts[kWidth];
     __shared__ uint32_t valid_rows;
-    __shared__ float scratch[kThreads];
+    __shared__ float scratch[Threads];
 
     const uint32_t l = threadIdx.x % Lanes, group = threadIdx.x / Lanes;
-    for (uint32_t e = threadIdx.x; e < kWidth; e += kThreads) counts[e] = 0;
+    for (uint32_t e = threadIdx.x; e < kWidth; e += Threads) counts[e] = 0;
     if (threadIdx.x == 0) valid_rows = 0;
     __syncthreads();
 
@@ -269,11 +274,26 @@ __global__ __launch_bounds__(kThreads) void router_rows_kernel(RouterArgs a) {
     if (mine) atomicAdd(&valid_rows, mine);
     __syncthreads();
     const Partials part = partials(a.ws, gridDim.x, a.experts);
-    float loss = 0.0f;
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kThreads) {
-        float s = sums[0][e];
+    if constexpr (kSlices > 1) {  // slice by slice of the groups first, into the slices' first rows
+        const uint32_t e = threadIdx.x % kWidth, slice = threadIdx.x / kWidth;
+        if (slice < kSlices) {
+            float s = sums[slice * (kGroups / kSlices)][e];
 #pragma unroll
-        for (uint32_t g = 1; g < kGroups; ++g) s += sums[g][e];
+            for (uint32_t g = 1; g < kGroups / kSlices; ++g) s += sums[slice * (kGroups / kSlices) + g][e];
+            sums[slice * (kGroups / kSlices)][e] = s;
+        }
+        __syncthreads();
+    }
+    float loss = 0.0f;
+    for (uint32_t e = threadIdx.x; e < a.experts; e += Threads) {
+        float s = sums[0][e];
+        if constexpr (kSlices > 1) {
+#pragma unroll
+            for (uint32_t g = 1; g < kSlices; ++g) s += sums[g * (kGroups / kSlices)][e];
+        } else {
+#pragma unroll
+            for (uint32_t g = 1; g < kGroups; ++g) s += sums[g][e];
+        }
         if (gridDim.x == 1) {
             loss += finish_expert(a, e, valid_rows, counts[e], s);
         } else {
@@ -282,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void router_rows_kernel(RouterArgs a) {
         }
     }
     if (gridDim.x == 1) {  // a single workgroup has all rows: nothing is left for a second launch
-        loss = workgroup_sum(loss, scratch);
+        loss = workgroup_sum<Threads>(loss, scratch);
         if (threadIdx.x == 0) a.loss[0] = loss;
     } else if (threadIdx.x == 0) {
         part.valid[blockIdx.x] = valid_rows;
@@ -290,18 +310,20 @@ __global__ __launch_bounds__(kThreads) void router_rows_kernel(RouterArgs a) {
     }
 }
 
-// 16 experts a workgroup, 16 lanes each over the rows launch's partial sums; the workgroup that
-// takes the last ticket adds up the loss, in the workgroups' order.
-__global__ __launch_bounds__(kThreads) void router_finish_kernel(RouterArgs a, uint32_t wgs) {
-    constexpr uint32_t kSlices = kThreads / kFinishExperts;
+// 16 experts a workgroup, 64 lanes each over the rows launch's partial sums (up to 256, four a lane); the workgroup
+// that takes the last ticket adds up the loss, in the workgroups' order.
+constexpr int kFinishThreads = 1024;
+
+__global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(RouterArgs a, uint32_t wgs) {
+    constexpr uint32_t kSlices = kFinishThreads / kFinishExperts;
     __shared__ float sums[kSlices][kFinishExperts];
     __shared__ uint32_t counts[kSlices][kFinishExperts];
-    __shared__ uint32_t valid[kThreads];
+    __shared__ uint32_t valid[kMostWgs];
     const Partials part = partials(a.ws, wgs, a.experts);
     const uint32_t i = threadIdx.x % kFinishExperts, slice = threadIdx.x / kFinishExperts;
     const uint32_t e = blockIdx.x * kFinishExperts + i;
     float s = 0.0f;
-    uint32_t c = 0, n = 0;
+    uint32_t c = 0;
     if (e < a.experts) {
 #pragma unroll 4
         for (uint32_t w = slice; w < wgs; w += kSlices) {
@@ -309,24 +331,24 @@ __global__ __launch_bounds__(kThreads) void router_finish_kernel(RouterArgs a, u
             c += part.counts[(size_t)w * a.experts + e];
         }
     }
-    for (uint32_t w = threadIdx.x; w < wgs; w += kThreads) n += part.valid[w];
+    if (threadIdx.x < kMostWgs) valid[threadIdx.x] = threadIdx.x < wgs ? part.valid[threadIdx.x] : 0u;
     sums[slice][i] = s;
     counts[slice][i] = c;
-    valid[threadIdx.x] = n;
     __syncthreads();
-    for (int d = kThreads / 2; d > 0; d >>= 1) {
-        if ((int)threadIdx.x < d) valid[threadIdx.x] += valid[threadIdx.x + d];
+    for (uint32_t d = kMostWgs / 2; d > 0; d >>= 1) {
+        if (threadIdx.x < d) {
+            valid[threadIdx.x] += valid[threadIdx.x + d];
+        } else if (const uint32_t t = threadIdx.x - kFinishThreads / 2; d >= 4 && t < d / 4 * kFinishExperts) {
+            // the upper lanes halve the slices meanwhile: 64 -> 1 while 256 -> 4
+            sums[t / kFinishExperts][i] += sums[t / kFinishExperts + d / 4][i];
+            counts[t / kFinishExperts][i] += counts[t / kFinishExperts + d / 4][i];
+        }
         __syncthreads();
     }
     if (threadIdx.x >= 16) return;
     float up = 0.0f;
     if (e < a.experts) {
-#pragma unroll
-        for (uint32_t k = 1; k < kSlices; ++k) {
-            s += sums[k][i];
-            c += counts[k][i];
-        }
-        up = finish_expert(a, e, valid[0], c, s);
+        up = finish_expert(a, e, valid[0], counts[0][i], sums[0][i]);
     }
     up = reduce_sum<16>(up);
     if (threadIdx.x != 0) return;
@@ -366,6 +388,9 @@ struct RouterGradArgs {
     int normalize;
 };
 
+// Reads and writes 32 MiB for 16,384 x 256 in 11 us; streaming stores, which leave nothing to write back at the end,
+// are a tenth of that.
+//
 // The gates' part of the gradient reaches its lane through a row of LDS that is zero but for the
 // chosen experts while it is read.
 template <typename In, int Lanes, int Per>
@@ -450,10 +475,12 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
                 if (e < a.experts) {
                     if constexpr (L::V == 4) {
                         if constexpr (sizeof(In) == 4) {
-                            *reinterpret_cast<f32x4_t*>(out + e) = f32x4_t{dx[j], dx[j + 1], dx[j + 2], dx[j + 3]};
+                            __builtin_nontemporal_store(f32x4_t{dx[j], dx[j + 1], dx[j + 2], dx[j + 3]},
+                                                        reinterpret_cast<f32x4_t*>(out + e));
                         } else {
-                            *reinterpret_cast<u32x2_t*>(out + e) =
-                                u32x2_t{pack_bf16x2(dx[j], dx[j + 1]), pack_bf16x2(dx[j + 2], dx[j + 3])};
+                            __builtin_nontemporal_store(
+                                u32x2_t{pack_bf16x2(dx[j], dx[j + 1]), pack_bf16x2(dx[j + 2], dx[j + 3])},
+                                reinterpret_cast<u32x2_t*>(out + e));
                         }
                     }
                 }
@@ -474,12 +501,17 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
 
 uint32_t row_lanes(uint32_t experts) { return experts <= 256 ? 16u : 64u; }
 
-// Workgroups of the rows launch.  One for up to 64 rows: its result then needs no second launch.
-// Above, at most one per CU: fewer partial sums to read back against more rows in a row.
+// Rows launch: one workgroup for what 64 rows of 16 lanes need at most, as its result then needs no second launch;
+// workgroups of 256 lanes while there are CUs for them all; then at most one of 1,024 lanes per CU, so that there are
+// few partial sums to read back.
+int row_threads(size_t rows, uint32_t experts) {
+    const size_t per = kThreads / row_lanes(experts);
+    return rows <= per || (rows > 4 * per && rows <= kMostWgs * per) ? kThreads : 4 * kThreads;
+}
+
 uint32_t row_wgs(size_t rows, uint32_t experts) {
-    const uint32_t per = kThreads / row_lanes(experts);
-    if (rows <= 64) return 1;
-    return (uint32_t)std::min<size_t>((rows + per - 1) / per, 256);
+    const uint32_t per = (uint32_t)row_threads(rows, experts) / row_lanes(experts);
+    return (uint32_t)std::min<size_t>((rows + per - 1) / per, kMostWgs);
 }
 
 // f(In, Lanes, Per) for the smallest register row that holds the experts
@@ -499,7 +531,9 @@ struct ForwardLaunch {
     hipStream_t stream;
     template <typename In, int Lanes, int Per>
     hipError_t operator()() const {
-        return enqueue(router_rows_kernel<In, Lanes, Per>, dim3(wgs), dim3(kThreads), stream, a);
+        return row_threads(a.rows, a.experts) == kThreads
+                   ? enqueue(router_rows_kernel<In, Lanes, Per, kThreads>, dim3(wgs), dim3(kThreads), stream, a)
+                   : enqueue(router_rows_kernel<In, Lanes, Per, 4 * kThreads>, dim3(wgs), dim3(4 * kThreads), stream, a);
     }
 };
 
@@ -518,6 +552,7 @@ struct BackwardLaunch {
 
 size_t router_workspace_bytes(size_t rows, int experts) {
     const size_t wgs = row_wgs(rows, (uint32_t)experts);
+    if (wgs <= 1) return 0;
     return kHeader + wgs * 4 * (1 + 2 * (size_t)experts);
 }
 
@@ -532,8 +567,8 @@ hipError_t launch_router_forward(const void* logits, int in_bf16, size_t rows, i
     const ForwardLaunch f{a, wgs, stream};
     const hipError_t e = in_bf16 ? with_layout<uint16_t>(a.experts, f) : with_layout<float>(a.experts, f);
     if (e != hipSuccess || wgs == 1) return e;
-    return enqueue(router_finish_kernel, dim3((a.experts + kFinishExperts - 1) / kFinishExperts), dim3(kThreads),
-                   stream, a, wgs);
+    return enqueue(router_finish_kernel, dim3((a.experts + kFinishExperts - 1) / kFinishExperts),
+                   dim3(kFinishThreads), stream, a, wgs);
 }
 
 hipError_t launch_router_backward(const void* logits, int in_bf16, size_t rows, int experts, int topk, int normalize,

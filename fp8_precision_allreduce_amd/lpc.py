@@ -481,12 +481,13 @@ def lpc_router_forward(logits, experts, gates, counts, load, slope, loss, coef: 
             p(gates, "gates", _F32, rows * topk, True), p(counts, "counts", _I32, e, True),
             p(load, "load", _F32, e, True), p(slope, "slope", _F32, e, True), p(loss, "loss", _F32, 1, True)]
     need = lpc_router_workspace_bytes(rows, e)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=logits.device)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
         if stream is not None:  # allocated for the current stream, used on the given one
             workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                                     else torch.cuda.ExternalStream(int(stream), device=logits.device))
-    _run("lpc_router_forward", p.device, stream, *args, p(workspace, "workspace", _U8, 0), workspace.numel())
+    space = (None, 0) if workspace is None else (p(workspace, "workspace", _U8, 0), workspace.numel())
+    _run("lpc_router_forward", p.device, stream, *args, *space)
 
 
 def lpc_router_backward(logits, experts, slope, dgates, dloss, dlogits, normalize: bool = True, mask=None, stream=None):

@@ -109,7 +109,7 @@ lpc_status lpc_gemm_fp8_wgrad(const uint8_t *yt, const float *ys, size_t n,
 /* ---------------------------------------------------------------------- */
 
 /* Device workspace of lpc_router_forward, in bytes, for these sizes (0 where
- * the sizes are refused).  No HIP call.                                      */
+ * none is needed or the sizes are refused).  No HIP call.                    */
 size_t lpc_router_workspace_bytes(size_t rows, int experts);
 
 /* For each row: p = softmax of the logits, the topk experts of the largest
@@ -127,7 +127,8 @@ size_t lpc_router_workspace_bytes(size_t rows, int experts);
  *   logits [rows, experts] of type `in`; mask [rows] uint8 or NULL (keep all)
  *   out_experts [rows, topk] int32, gates [rows, topk]
  *   counts [experts] int32, load [experts], slope [experts], loss [1]
- *   workspace  at least lpc_router_workspace_bytes, no initial contents needed
+ *   workspace  at least lpc_router_workspace_bytes, no initial contents needed;
+ *      NULL where that is 0
  *   experts in 1..LPC_MAX_EXPERTS, topk in 1..min(experts, LPC_MAX_TOPK),
  *   rows < 2^31 (else LPC_ERR_SHAPE).  rows == 0: counts, load, slope and loss
  *   are zero (logits, out_experts and gates may be NULL).                    */

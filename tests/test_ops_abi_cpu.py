@@ -115,6 +115,15 @@ def test_router_errors(L):
         assert g(*replaced(ok, **bad)) == SHAPE, bad
 
 
+def test_router_without_workspace(L):
+    """Few rows need none; more than one workgroup's do."""
+    for rows, experts, none in ((0, 60, True), (1, 64, True), (64, 256, True), (65, 256, False), (16, 1024, True), (17, 1024, False)):
+        need = lpc.lpc_router_workspace_bytes(rows, experts)
+        assert (need == 0) == none, (rows, experts, need)
+        args = [A, F32, rows, experts, 2, 1, 0.01, None, A, A, A, A, A, A, None, 0, None]
+        assert L.lpc_router_forward(*args) == (HIP if none else NULL), (rows, experts)
+
+
 def plan(L, rows, grad=F32, bits=32):
     t = (lpc._AdamwTensor * max(len(rows), 1))(*[lpc._AdamwTensor(*r) for r in rows])
     size = L.lpc_adamw_plan_bytes(t, len(rows))
