@@ -657,6 +657,34 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
     }
 
     Out* out = static_cast<Out*>(a.out) + w.out;
+    constexpr uint32_t kPer = 16 / sizeof(Out), kLanes = PW / kPer;  // outputs of 16 bytes, lanes of a row
+    if (a.np % kPer == 0) {
+        // 64 rows at a time through LDS, which is free, so that a store covers whole lines: it costs by the lines it
+        // touches, like a load, and a fragment's rows would be 16 pieces of 32 (bf16) or 64 bytes.  A wavefront has a
+        // part of its own; rows are 16 bytes further apart than they are long, which spreads them over the banks.
+        constexpr uint32_t kPitch = PW * sizeof(Out) + 16;
+        static_assert(kTiledWaves * 16 * F * kPitch <= S::kBytes, "LDS for the outputs");
+        uint8_t* own = lds + wave * 16 * F * kPitch;
+#pragma unroll
+        for (int ph = 0; ph < Phases; ++ph) {
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+#pragma unroll
+                for (int j = 0; j < PF; ++j)
+                    store4(reinterpret_cast<Out*>(own + (16 * i + l16) * kPitch) + 16 * j + 4 * l4, acc[ph * F + i][j], 4, true);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+            for (uint32_t r = 0; r < 16 * F; r += 64 / kLanes) {
+                const uint32_t row = r + lane / kLanes, col = lane % kLanes;
+                const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + row * kPitch + col * 16);
+                const uint32_t q = wq * QW + ph * 16 * F + row, p = p0 + wp * PW + col * kPer;
+                if (q < w.nq && p < a.np)
+                    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(out + (size_t)(w.q0 + q) * a.np + p));
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < Phases * F; ++i) {
         const uint32_t q = wq * QW + 16 * i + l16;
