@@ -606,7 +606,6 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
                     else if (b + 1 < nb) arrived(b + 1);
                 }
                 end_slot();
-                __builtin_amdgcn_s_setprio(1);
                 // element e of product t of this phase, added to its accumulator here and not where that is next needed
                 f32x4_t part[F * PF];
                 auto take_up = [&](int t, int e) {
@@ -644,7 +643,6 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
                         }
                     }
                 }
-                __builtin_amdgcn_s_setprio(0);
                 if (group == 0) {
                     if (Phases == 2 && ph == 0) arrived(b);
                     else if (b + 1 < nb) arrived(b + 1);
@@ -736,12 +734,26 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_product_kernel(GemmA
     }
 }
 
+// The group with the z-th most rows, for up to 64 groups: their tiles take times that differ as their rows do, and the
+// long ones come first, so that short ones fill the end.
+__device__ __forceinline__ uint32_t by_rows(const GemmArgs& a, uint32_t z) {
+    if (!a.counts || a.groups > 64) return z;
+    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t c = lane < a.groups ? group_rows(a.counts, lane, a.rows) : 0;
+    uint32_t rank = 0;
+    for (uint32_t g = 0; g < a.groups; ++g) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)c, (int)g);
+        rank += o > c || (o == c && g < lane);
+    }
+    return (uint32_t)__builtin_ctzll(__ballot(lane < a.groups && rank == z));
+}
+
 __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_wgrad_kernel(GemmArgs a) {
     using L = Large<float>;
     __shared__ __attribute__((aligned(128))) uint8_t lds[L::kBytes];
     const uint32_t tiles_p = (a.np + L::BP - 1) / L::BP;
     const uint2 t = in_bands((uint32_t)xcd_tile(), gridDim.x / tiles_p, tiles_p);
-    tile<kWgrad, float, L>(a, find_work<kWgrad, L::BQ>(a, t.x, blockIdx.y), t.y * L::BP, lds);
+    tile<kWgrad, float, L>(a, find_work<kWgrad, L::BQ>(a, t.x, by_rows(a, blockIdx.y)), t.y * L::BP, lds);
 }
 
 template <typename Out>
