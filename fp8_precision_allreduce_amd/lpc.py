@@ -16,6 +16,7 @@ import os
 import re
 import threading
 
+import numpy as np
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -365,6 +366,20 @@ class _Args:
             raise ValueError("%s is on cuda:%d, the other tensors on cuda:%d" % (what, d, self.device))
         return t.data_ptr()
 
+    def many(self, ts, what, dtypes, numels):
+        """Pointers of a list's tensors, each of exactly its number of elements."""
+        first = self(ts[0], what + "[0]", dtypes, numels[0], True)
+        dtype, device = ts[0].dtype, ts[0].device
+        out = [first]
+        for i in range(1, len(ts)):
+            t = ts[i]
+            try:
+                alike = t.dtype is dtype and t.device == device and t.numel() == numels[i] and t.is_contiguous()
+            except AttributeError:
+                alike = False
+            out.append(t.data_ptr() if alike else self(t, "%s[%d]" % (what, i), dtypes, numels[i], True))
+        return out
+
     def optional(self, t, what, dtypes, numel):
         return None if t is None else self(t, what, dtypes, numel)
 
@@ -522,19 +537,20 @@ class AdamW:
             if ts is not None and len(ts) != len(params):
                 raise ValueError("%s has %d tensors, params %d" % (what, len(ts), len(params)))
         state = _F32 if self.state_bits == 32 else _U8
-        p, table = _Args(), (_AdamwTensor * max(len(params), 1))()
-        for i, t in enumerate(params):
-            row = table[i]
-            row.param = p(t, "params[%d]" % i, _F32, 0)
-            row.n = n = t.numel()
-            row.grad = p(grads[i], "grads[%d]" % i, (grads[0].dtype,), n, True)
-            row.m = p(m[i], "m[%d]" % i, state, n, True)
-            row.v = p(v[i], "v[%d]" % i, state, n, True)
-            if self.state_bits == 8:
-                row.m_scales = p(m_scales[i], "m_scales[%d]" % i, _F32, _blocks(n), True)
-                row.v_scales = p(v_scales[i], "v_scales[%d]" % i, _F32, _blocks(n), True)
-            if copies is not None:
-                row.copy = p(copies[i], "copies[%d]" % i, (torch.bfloat16,), n, True)
+        p, rows = _Args(), max(len(params), 1)
+        table = (_AdamwTensor * rows)()
+        columns = np.frombuffer(table, dtype=np.uint64).reshape(rows, -1)  # one 8-byte field each, in the order of _fields_
+        sizes = [t.numel() if isinstance(t, torch.Tensor) else 0 for t in params]
+        blocks = [_blocks(n) for n in sizes]
+        states = (m, "m", state, sizes), (v, "v", state, sizes)
+        scales = (m_scales, "m_scales", _F32, blocks), (v_scales, "v_scales", _F32, blocks)
+        fields = ((params, "params", _F32, sizes), (grads, "grads", (grads[0].dtype,) if len(params) else _FB, sizes), *states,
+                  *scales, (copies, "copies", (torch.bfloat16,), sizes))
+        for column, (ts, what, dtypes, ns) in enumerate(fields):
+            if ts is not None and len(ts):
+                columns[:, column] = p.many(ts, what, dtypes, ns)
+        if len(params):
+            columns[:, len(fields)] = sizes
         self.grad_dtype = _dtype(grads[0]) if len(params) else LPC_F32
         self.device = p.device
         self._tensors = (list(params), {k: list(ts) for k, ts in lists.items() if ts is not None})  # kept alive
