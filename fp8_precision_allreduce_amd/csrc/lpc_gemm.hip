@@ -155,7 +155,7 @@ __device__ __forceinline__ Work find_work(const GemmArgs& a, uint32_t tq, uint32
         w.out = 0;
         w.none = t.rows == 0;
     } else {
-        const GroupTile t = find_group(a.counts, a.rows, kBlock, z);
+        const GroupTile t = find_group(a.counts, a.groups, a.rows, kBlock, z);
         w.q0 = tq * BQ;
         w.nq = min(BQ, a.nq - w.q0);
         w.b0 = t.before;
@@ -719,18 +719,23 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_product_kernel(GemmA
     const uint32_t first = x * (all / kXcds) + min(x, rest), mine = all / kXcds + (x < rest);
     const uint32_t last = mine % kXcdCus, split = last <= kMostSplit ? last : 0;
     const uint32_t whole = mine - split;
-    if (k < whole) {
-        const uint2 t = in_bands(first + k, tiles_q, tiles_p);
-        tile<kProduct, Out, L>(a, find_work<kProduct, L::BQ>(a, t.x, 0), t.y * L::BP, lds);
-    } else if (k < whole + split * Parts) {
-        const uint32_t n = (k - whole) / Parts, part = (k - whole) % Parts;
-        const uint2 t = in_bands(first + whole + n, tiles_q, tiles_p);
-        Work w = find_work<kProduct, L::BQ>(a, t.x, 0);
-        const uint32_t q = part / PartsP * Small::BQ, p0 = t.y * L::BP + part % PartsP * Small::BP;
-        if (q >= w.nq || p0 >= a.np) return;
-        w.q0 += q;
-        w.nq = min(w.nq - q, Small::BQ);
-        tile<kProduct, Out, Small>(a, w, p0, lds);
+    if (k >= whole + split * Parts) return;
+    const uint32_t n = k < whole ? k : whole + (k - whole) / Parts;
+    const uint2 t = in_bands(first + n, tiles_q, tiles_p);
+    Work w = find_work<kProduct, L::BQ>(a, t.x, 0);
+    if (k < whole && w.nq > Small::BQ) {
+        tile<kProduct, Out, L>(a, w, t.y * L::BP, lds);
+        return;
+    }
+    // one part, or the upper ones of a tile that has rows for these only: a group's last, or a small group's
+    const uint32_t part = k < whole ? 0 : (k - whole) % Parts, q = part / PartsP * Small::BQ;
+    if (q >= w.nq) return;
+    w.q0 += q;
+    w.nq = min(w.nq - q, Small::BQ);
+    const uint32_t p0 = t.y * L::BP + part % PartsP * Small::BP, end = k < whole ? t.y * L::BP + L::BP : p0 + Small::BP;
+    for (uint32_t p = p0; p < min(end, a.np); p += Small::BP) {
+        tile<kProduct, Out, Small>(a, w, p, lds);
+        __syncthreads();  // LDS may be written again
     }
 }
 

@@ -38,27 +38,65 @@ struct GroupTile {
 };
 
 // Rows of group g: the count on the device, no less than 0 and no more than
-// what the buffer has left.
-__device__ __forceinline__ uint32_t group_rows(const int32_t* __restrict__ counts, uint32_t g, uint32_t left) {
-    if (!counts) return left;
+// `most`.
+__device__ __forceinline__ uint32_t group_rows(const int32_t* __restrict__ counts, uint32_t g, uint32_t most) {
     const int32_t c = counts[g];
-    return c < 0 ? 0u : min((uint32_t)c, left);
+    return c < 0 ? 0u : min((uint32_t)c, most);
 }
 
-// Tile number t.  The counts are read in order by the scalar unit; the loop is
-// uniform over the wavefront.
+// A lane's group among 64: its rows, and its tiles and those before it.  Groups
+// end at `rows`, so their ends are a running sum that stops there.  Every lane
+// of the wavefront has to be active.
+struct GroupScan {
+    uint32_t begin, end;     // rows
+    uint32_t before, tiles;
+
+    // groups first .. + 63, after groups that end at row `row` and have `tile` tiles
+    __device__ __forceinline__ GroupScan(const int32_t* __restrict__ counts, uint32_t groups, uint32_t rows, uint32_t T,
+                                         uint32_t first, uint32_t row, uint32_t tile) {
+        const uint32_t lane = threadIdx.x & 63, g = first + lane;
+        uint32_t sum = g < groups ? group_rows(counts, g, rows) : 0;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const uint32_t o = (uint32_t)__shfl_up((int)sum, d);
+            if (lane >= (uint32_t)d) sum = min(sum + o, rows);
+        }
+        end = min(row + sum, rows);
+        begin = (uint32_t)__shfl_up((int)end, 1);
+        if (lane == 0) begin = row;
+        tiles = (end - begin + T - 1) / T;
+        uint32_t all = tiles;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const uint32_t o = (uint32_t)__shfl_up((int)all, d);
+            if (lane >= (uint32_t)d) all += o;
+        }
+        before = tile + all - tiles;
+    }
+};
+
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, uint32_t lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, (int)lane);
+}
+
+// Tile number t.
 __device__ __forceinline__ GroupTile find_tile(const int32_t* __restrict__ counts, uint32_t groups, uint32_t rows,
                                                uint32_t T, uint32_t t) {
     uint32_t row = 0, before = 0;
-    for (uint32_t g = 0; g < groups; ++g) {
-        const uint32_t c = group_rows(counts, g, rows - row);
-        const uint32_t n = (c + T - 1) / T;
-        if (t - before < n) {
-            const uint32_t off = (t - before) * T;
-            return {g, row + off, min(T, c - off), before, n};
+    if (!counts) {
+        const uint32_t n = (rows + T - 1) / T;
+        if (t < n) return {0, t * T, min(T, rows - t * T), 0, n};
+        return {1, rows, 0, n, 0};
+    }
+    for (uint32_t first = 0; first < groups; first += 64) {
+        const GroupScan s(counts, groups, rows, T, first, row, before);
+        if (const unsigned long long has = __ballot(t - s.before < s.tiles)) {
+            const uint32_t l = (uint32_t)__builtin_ctzll(has);
+            const uint32_t begin = from_lane(s.begin, l), b = from_lane(s.before, l), off = (t - b) * T;
+            return {first + l, begin + off, min(T, from_lane(s.end, l) - begin - off), b, from_lane(s.tiles, l)};
         }
-        row += c;
-        before += n;
+        row = from_lane(s.end, 63);
+        before = from_lane(s.before + s.tiles, 63);
     }
     const uint32_t left = rows - row, n = (left + T - 1) / T, off = (t - before) * T;
     if (t - before < n) return {groups, row + off, min(T, left - off), before, n};
@@ -68,26 +106,27 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t* __restrict__ count
 // Tiles of all groups and of the rows past the last one.
 __device__ __forceinline__ uint32_t count_tiles(const int32_t* __restrict__ counts, uint32_t groups, uint32_t rows,
                                                 uint32_t T) {
-    uint32_t row = 0, tiles = 0;
-    for (uint32_t g = 0; g < groups; ++g) {
-        const uint32_t c = group_rows(counts, g, rows - row);
-        row += c;
-        tiles += (c + T - 1) / T;
+    uint32_t row = 0, before = 0;
+    for (uint32_t first = 0; counts && first < groups; first += 64) {
+        const GroupScan s(counts, groups, rows, T, first, row, before);
+        row = from_lane(s.end, 63);
+        before = from_lane(s.before + s.tiles, 63);
     }
-    return tiles + (rows - row + T - 1) / T;
+    return before + (rows - row + T - 1) / T;
 }
 
 // First tile and number of tiles of group g.
-__device__ __forceinline__ GroupTile find_group(const int32_t* __restrict__ counts, uint32_t rows, uint32_t T,
-                                                uint32_t g) {
+__device__ __forceinline__ GroupTile find_group(const int32_t* __restrict__ counts, uint32_t groups, uint32_t rows,
+                                                uint32_t T, uint32_t g) {
     uint32_t row = 0, before = 0;
-    for (uint32_t i = 0; i < g; ++i) {
-        const uint32_t c = group_rows(counts, i, rows - row);
-        row += c;
-        before += (c + T - 1) / T;
+    if (!counts) return {g, 0, rows, 0, (rows + T - 1) / T};
+    for (uint32_t first = 0;; first += 64) {
+        const GroupScan s(counts, groups, rows, T, first, row, before);
+        if (const uint32_t l = g - first; l < 64)
+            return {g, from_lane(s.begin, l), from_lane(s.end - s.begin, l), from_lane(s.before, l), from_lane(s.tiles, l)};
+        row = from_lane(s.end, 63);
+        before = from_lane(s.before + s.tiles, 63);
     }
-    const uint32_t c = group_rows(counts, g, rows - row);
-    return {g, row, c, before, (c + T - 1) / T};
 }
 
 hipError_t launch_gemm(const uint8_t* x, const float* xs, size_t rows, size_t k, const uint8_t* w, const float* ws,
