@@ -52,9 +52,11 @@ __device__ __forceinline__ uint32_t code_slot(uint32_t c, uint32_t d) {
 
 template <typename In, bool Rows>
 __global__ __launch_bounds__(kThreads) void quantize_cols_kernel(ColArgs a) {
-    __shared__ __attribute__((aligned(16))) float top[32][kBlock];
-    __shared__ __attribute__((aligned(16))) float scale[kBlock];
+    // the row groups' column maxima, and once these are reduced the turned codes
     __shared__ __attribute__((aligned(16))) uint8_t turned[kBlock * kBlock];
+    float(*top)[kBlock] = reinterpret_cast<float(*)[kBlock]>(turned);
+    static_assert(sizeof(float) * 32 * kBlock == sizeof(turned), "shared");
+    __shared__ __attribute__((aligned(16))) float2 scale[kBlock];  // s, and 1 / s where codes go by it
 
     const size_t blocks_n = a.n / kBlock;
     const size_t tile = xcd_tile();
@@ -106,18 +108,23 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_kernel(ColArgs a) {
 #pragma unroll
         for (int k = 1; k < 32; ++k) m = fmaxf(m, top[k][tid]);
         const float s = m / kFp8Max;
-        scale[tid] = s;
+        scale[tid] = make_float2(s, s >= kMinRecipScale ? 1.0f / s : 0.0f);
         a.scales_t[(size_t)tr * a.n + c0 + tid] = s;
     }
     __syncthreads();
 
 #pragma unroll
     for (int j = 0; j < kGranule; ++j) {
-        const float s = scale[cc + j];
+        const float2 s = scale[cc + j];
+        const float x[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
         uint32_t w[1] = {0u};
-        if (s > 0.0f) {
-            const float q[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
-            encode_quotients(q, s, w);
+        if (s.y != 0.0f) {
+            float q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = quotient(x[i], s.x, s.y);
+            w[0] = encode4(q[0], q[1], q[2], q[3]);
+        } else if (s.x > 0.0f) {
+            encode_quotients(x, s.x, w);
         }
         *reinterpret_cast<uint32_t*>(turned + code_slot(cc + j, rr)) = w[0];
     }

@@ -49,27 +49,27 @@ __device__ __forceinline__ uint32_t group_rows(const int32_t* __restrict__ count
 // of the wavefront has to be active.
 struct GroupScan {
     uint32_t begin, end;     // rows
-    uint32_t before, tiles;
+    uint32_t before, tiles;  // no tiles in a lane without a group
+    uint32_t last;           // the last lane with a group
 
     // groups first .. + 63, after groups that end at row `row` and have `tile` tiles
     __device__ __forceinline__ GroupScan(const int32_t* __restrict__ counts, uint32_t groups, uint32_t rows, uint32_t T,
                                          uint32_t first, uint32_t row, uint32_t tile) {
-        const uint32_t lane = threadIdx.x & 63, g = first + lane;
-        uint32_t sum = g < groups ? group_rows(counts, g, rows) : 0;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
+        const uint32_t lane = threadIdx.x & 63, here = min(groups - first, 64u);
+        last = here - 1;
+        uint32_t sum = lane < here ? group_rows(counts, first + lane, rows) : 0;
+        for (uint32_t d = 1; d < here; d *= 2) {
             const uint32_t o = (uint32_t)__shfl_up((int)sum, d);
-            if (lane >= (uint32_t)d) sum = min(sum + o, rows);
+            if (lane >= d) sum = min(sum + o, rows);
         }
         end = min(row + sum, rows);
         begin = (uint32_t)__shfl_up((int)end, 1);
         if (lane == 0) begin = row;
-        tiles = (end - begin + T - 1) / T;
+        tiles = lane < here ? (end - begin + T - 1) / T : 0;
         uint32_t all = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
+        for (uint32_t d = 1; d < here; d *= 2) {
             const uint32_t o = (uint32_t)__shfl_up((int)all, d);
-            if (lane >= (uint32_t)d) all += o;
+            if (lane >= d) all += o;
         }
         before = tile + all - tiles;
     }
@@ -95,8 +95,8 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t* __restrict__ count
             const uint32_t begin = from_lane(s.begin, l), b = from_lane(s.before, l), off = (t - b) * T;
             return {first + l, begin + off, min(T, from_lane(s.end, l) - begin - off), b, from_lane(s.tiles, l)};
         }
-        row = from_lane(s.end, 63);
-        before = from_lane(s.before + s.tiles, 63);
+        row = from_lane(s.end, s.last);
+        before = from_lane(s.before + s.tiles, s.last);
     }
     const uint32_t left = rows - row, n = (left + T - 1) / T, off = (t - before) * T;
     if (t - before < n) return {groups, row + off, min(T, left - off), before, n};
@@ -109,8 +109,8 @@ __device__ __forceinline__ uint32_t count_tiles(const int32_t* __restrict__ coun
     uint32_t row = 0, before = 0;
     for (uint32_t first = 0; counts && first < groups; first += 64) {
         const GroupScan s(counts, groups, rows, T, first, row, before);
-        row = from_lane(s.end, 63);
-        before = from_lane(s.before + s.tiles, 63);
+        row = from_lane(s.end, s.last);
+        before = from_lane(s.before + s.tiles, s.last);
     }
     return before + (rows - row + T - 1) / T;
 }
@@ -124,8 +124,8 @@ __device__ __forceinline__ GroupTile find_group(const int32_t* __restrict__ coun
         const GroupScan s(counts, groups, rows, T, first, row, before);
         if (const uint32_t l = g - first; l < 64)
             return {g, from_lane(s.begin, l), from_lane(s.end - s.begin, l), from_lane(s.before, l), from_lane(s.tiles, l)};
-        row = from_lane(s.end, 63);
-        before = from_lane(s.before + s.tiles, 63);
+        row = from_lane(s.end, s.last);
+        before = from_lane(s.before + s.tiles, s.last);
     }
 }
 
