@@ -449,6 +449,18 @@ hipError_t launch_narrow(const GemmArgs& a, uint32_t tiles_q, hipStream_t stream
 //                   of phase 1 from 4 c - 4 (- 3) to 4 c + 2
 //   Phases == 1, three stages  everything from slot 2 c - 4 (- 3) to 2 c
 // In both a wavefront waits until only one block's worth of loads is on its way.
+//
+// Measured, and what bounds it: 16,384 x 7168 x 4096 to bf16 runs at 2.3 PFLOP/s
+// (2.0 over 8 uneven groups), 4096 x 8192 x 4096 to fp32 at 1.2, weight gradients
+// of 8 groups at 0.95; a library product with one scale reaches 2.86 on these
+// sizes in FP8 and 1.42 in fp16.  The matrix cores are busy for 58% of the cycles
+// (fp32: 52%), and the card's power holds the clock at 1.95 GHz: the same kernel
+// on codes that are all zero runs at 2.9.  A loop of matrix instructions and
+// scalings alone, on random codes in registers, gives 3.5 (fp16: 1.95).  Loads
+// one block later cost a fifth, bank conflicts of a simpler layout as much.
+// Neither one stream per wavefront with everything between its matrix
+// instructions, nor fragments read two rows ahead, nor wavefront priorities, nor
+// 16-byte loads of scales changed the time by more than 2%.
 // ---------------------------------------------------------------------------
 
 constexpr int kTiledWaves = 8;
