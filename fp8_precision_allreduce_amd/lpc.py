@@ -348,23 +348,30 @@ class _Args:
         self.device = None
 
     def __call__(self, t, what, dtypes, numel, exact=False):
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous():
+            n, d = t.numel(), t.get_device()
+            if (n == numel or (n > numel and not exact)) and (d == self.device or self.device is None):
+                self.device = d
+                return t.data_ptr()
+        raise self.fault(t, what, dtypes, numel, exact)
+
+    def fault(self, t, what, dtypes, numel, exact):
+        """What is wrong with an argument that was refused."""
         if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch tensor" % what)
+            return TypeError("%s must be a torch tensor" % what)
         if not t.is_cuda:
-            raise ValueError("%s must be a GPU tensor" % what)
+            return ValueError("%s must be a GPU tensor" % what)
         if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % what)
+            return ValueError("%s must be contiguous" % what)
         if t.dtype not in dtypes:
-            raise TypeError("%s has dtype %s, expected one of %s" % (what, t.dtype, dtypes))
+            return TypeError("%s has dtype %s, expected one of %s" % (what, t.dtype, dtypes))
         n = t.numel()
         if n < numel or (exact and n != numel):
-            raise ValueError("%s holds %d elements, needs %d" % (what, n, numel))
-        d = t.get_device()
-        if self.device is None:
-            self.device = d
-        elif self.device != d:
-            raise ValueError("%s is on cuda:%d, the other tensors on cuda:%d" % (what, d, self.device))
-        return t.data_ptr()
+            return ValueError("%s holds %d elements, needs %d" % (what, n, numel))
+        return ValueError("%s is on cuda:%d, the other tensors on cuda:%d" % (what, t.get_device(), self.device))
+
+    def optional(self, t, what, dtypes, numel):
+        return None if t is None else self(t, what, dtypes, numel)
 
     def many(self, ts, what, dtypes, numels):
         """Pointers of a list's tensors, each of exactly its number of elements."""
@@ -379,9 +386,6 @@ class _Args:
                 alike = False
             out.append(t.data_ptr() if alike else self(t, "%s[%d]" % (what, i), dtypes, numels[i], True))
         return out
-
-    def optional(self, t, what, dtypes, numel):
-        return None if t is None else self(t, what, dtypes, numel)
 
 
 def _run(name, device, stream, *args):
@@ -479,7 +483,7 @@ def lpc_gemm_fp8_wgrad(yt, ys, xt, xs, dw, rows: int, counts=None, stream=None):
 
 def lpc_router_workspace_bytes(rows: int, experts: int) -> int:
     """Device workspace of lpc_router_forward (no GPU call)."""
-    return lib().lpc_router_workspace_bytes(rows, experts)
+    return (_lib or lib()).lpc_router_workspace_bytes(rows, experts)
 
 
 def lpc_router_forward(logits, experts, gates, counts, load, slope, loss, coef: float, normalize: bool = True,
