@@ -19,6 +19,7 @@ namespace lpc {
 template <typename... P, typename... A>
 static hipError_t enqueue(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t stream, A... args) {
     static_assert(sizeof...(P) == sizeof...(A) && sizeof...(P) > 0, "argument count");
+    if (((uint64_t)grid.x * block.x) >> 32) return hipErrorInvalidConfiguration;  // lanes along x are counted in 32 bits
     std::tuple<P...> vals(args...);
     return std::apply(
         [&](auto&... v) {
