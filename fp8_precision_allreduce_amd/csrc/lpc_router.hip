@@ -63,6 +63,19 @@ __device__ __forceinline__ uint32_t reduce_min(uint32_t x) {
     return reduce<Lanes>(x, [](uint32_t a, uint32_t b) { return min(a, b); });
 }
 
+// exp(x) for x <= 0, -infinity among them: 2^t for t = fl(x log2 e), times 1 + (x log2 e - t) ln 2, which the fused
+// operations get from what t leaves of the product and from the constant's next 24 bits.  Within 2 units in the last
+// place where the result is not below 2^-125 (zero or denormal there); half the instructions of a general expf.
+__device__ __forceinline__ float exp_below(float x) {
+    constexpr double kLog2E = 1.4426950408889634074;
+    constexpr float kHigh = (float)kLog2E, kLow = (float)(kLog2E - (double)kHigh), kLn2 = 0.69314718056f;
+    x = fmaxf(x, -200.0f);  // no -infinity in the products
+    const float t = x * kHigh;
+    const float rest = __builtin_fmaf(x, kLow, __builtin_fmaf(x, kHigh, -t));
+    const float p = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(p, rest * kLn2, p);
+}
+
 // ---------------------------------------------------------------------------
 // a row's logits: element j of lane l is expert (j / V) V Lanes + V l + j % V,
 // V = min(Per, 4) neighbouring experts a load
@@ -235,7 +248,7 @@ __global__ __launch_bounds__(Threads) void router_rows_kernel(RouterArgs a) {
             float p[Per], sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < Per; ++j) {
-                p[j] = expf(x[j] - top);  // exp(-infinity) = 0
+                p[j] = exp_below(x[j] - top);  // exp(-infinity) = 0
                 sum += p[j];
             }
             const float inv = 1.0f / reduce_sum<Lanes>(sum);
@@ -256,7 +269,7 @@ __global__ __launch_bounds__(Threads) void router_rows_kernel(RouterArgs a) {
                     logit = best;
                 }
             }
-            gate = index != kNone ? expf(logit - top) * inv : 0.0f;
+            gate = index != kNone ? exp_below(logit - top) * inv : 0.0f;
             if (a.normalize) {
                 const float picked = reduce_sum<Lanes>(gate);
                 gate = picked > 0.0f ? gate / picked : gate;
@@ -425,7 +438,7 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
             float p[Per], sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < Per; ++j) {
-                p[j] = expf(x[j] - top);
+                p[j] = exp_below(x[j] - top);
                 sum += p[j];
             }
             const float inv = 1.0f / reduce_sum<Lanes>(sum);
@@ -437,7 +450,7 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
                     const float y = widen(logits[r * a.experts + e]);
                     if (y > LPC_NEG_INF) {
                         index = e;
-                        gate = expf(y - top) * inv;
+                        gate = exp_below(y - top) * inv;
                         dg = a.dgates[r * a.topk + l];
                     }
                 }
