@@ -767,12 +767,12 @@ __device__ __forceinline__ uint32_t by_rows(const GemmArgs& a, uint32_t z) {
     return (uint32_t)__builtin_ctzll(__ballot(lane < a.groups && rank == z));
 }
 
+template <typename S>
 __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_wgrad_kernel(GemmArgs a) {
-    using L = Large<float>;
-    __shared__ __attribute__((aligned(128))) uint8_t lds[L::kBytes];
-    const uint32_t tiles_p = (a.np + L::BP - 1) / L::BP;
+    __shared__ __attribute__((aligned(128))) uint8_t lds[S::kBytes];
+    const uint32_t tiles_p = (a.np + S::BP - 1) / S::BP;
     const uint2 t = in_bands((uint32_t)xcd_tile(), gridDim.x / tiles_p, tiles_p);
-    tile<kWgrad, float, L>(a, find_work<kWgrad, L::BQ>(a, t.x, by_rows(a, blockIdx.y)), t.y * L::BP, lds);
+    tile<kWgrad, float, S>(a, find_work<kWgrad, S::BQ>(a, t.x, by_rows(a, blockIdx.y)), t.y * S::BP, lds);
 }
 
 template <typename Out>
@@ -786,11 +786,16 @@ hipError_t launch_tiled_product(const GemmArgs& a, uint32_t most_tiles_q, hipStr
     return enqueue(gemm_product_kernel<Out>, dim3((uint32_t)wgs), dim3(kTiledWaves * 64), stream, a);
 }
 
+template <typename S>
+uint64_t wgrad_tiles(const GemmArgs& a) {
+    return (uint64_t)((a.nq + S::BQ - 1) / S::BQ) * ((a.np + S::BP - 1) / S::BP);
+}
+
+template <typename S>
 hipError_t launch_tiled_wgrad(const GemmArgs& a, uint32_t z, hipStream_t stream) {
-    using L = Large<float>;
-    const uint64_t wgs = (uint64_t)((a.nq + L::BQ - 1) / L::BQ) * ((a.np + L::BP - 1) / L::BP);
+    const uint64_t wgs = wgrad_tiles<S>(a);
     if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
-    return enqueue(gemm_wgrad_kernel, dim3((uint32_t)wgs, z), dim3(kTiledWaves * 64), stream, a);
+    return enqueue(gemm_wgrad_kernel<S>, dim3((uint32_t)wgs, z), dim3(kTiledWaves * 64), stream, a);
 }
 
 // Tiles of T rows that any counts can make of `rows` rows in `groups` groups and
@@ -835,8 +840,14 @@ hipError_t launch_wgrad(const uint8_t* yt, const float* ys, size_t n, const uint
                         size_t rows, size_t padded, int groups, const int32_t* counts, float* dw,
                         hipStream_t stream) {
     const GemmArgs a{yt, xt, ys, xs, counts, dw, (uint32_t)groups, (uint32_t)rows, (uint32_t)n, (uint32_t)k, padded};
-    if (n >= 256 && k >= 256 && tiled_offsets(a))
-        return launch_tiled_wgrad(a, (uint32_t)groups, stream);
+    // By the number of workgroups, one to a CU (times in us of 64 x 64, 128 x 128 and 256 x 128 outputs):
+    //   up to 256 of 64 x 64     gathered: 2048 x 1024 x 1024 14.5 / 21 / 32
+    //   up to 128 of 256 x 128   2048 x 2048 x 2048 51 / 23 / 33
+    //   more                     2048 x 4096 x 2048 99 / 44 / 37
+    const uint64_t g = (uint64_t)groups, small = ((n + 63) / 64) * ((k + 63) / 64) * g;
+    if (small > 256 && tiled_offsets(a))
+        return wgrad_tiles<Large<float>>(a) * g <= 128 ? launch_tiled_wgrad<Small>(a, (uint32_t)groups, stream)
+                                                       : launch_tiled_wgrad<Large<float>>(a, (uint32_t)groups, stream);
     return launch_split<kWgrad, float, 4, 4>(a, (uint32_t)((n + 63) / 64), (uint32_t)groups, stream);
 }
 

@@ -285,6 +285,13 @@ def test_wgrad(dev, rows, n, k, counts):
         assert not bad.any() and not dw[g].isnan().any(), (g, int(bad.sum()))
 
 
+@pytest.mark.parametrize("rows,n,k,counts", [
+    (130, 1030, 1100, None), (390, 700, 900, [1, 0, 260, 100]),        # 128 x 128
+    (300, 2300, 2050, None), (260, 1300, 900, [128, 3, 0, 120])])      # 256 x 128
+def test_wgrad_kinds_of_tiles(dev, rows, n, k, counts):
+    test_wgrad(dev, rows, n, k, counts)
+
+
 def test_wgrad_without_rows(dev):
     dw = torch.full((2, 64, 128), 7.0, device=dev)
     e8, ef = torch.empty(0, dtype=torch.uint8, device=dev), torch.empty(0, device=dev)
