@@ -339,6 +339,9 @@ def lpc_e4m3_encode(x: torch.Tensor, codes: torch.Tensor, stream=None):
 # unless another is given.
 # ---------------------------------------------------------------------------
 
+_u8, _f4, _i4, _MASK = torch.uint8, torch.float32, torch.int32, (torch.uint8, torch.bool)
+
+
 class _Args:
     """Pointers of one call's tensors, checked as _dev checks them and to be on one GPU."""
 
@@ -421,6 +424,23 @@ def _blocks(n):
 def lpc_gemm_fp8(x, xs, w, ws, out, counts=None, stream=None):
     """out [rows, n] = x [rows, k] times w [groups, n, k] (or [n, k]) transposed, E4M3 codes with scales
     xs [rows, k/128] and ws [groups, ceil(n/128), k/128]; counts [groups] int32: rows of each group."""
+    # A small product takes less time on the GPU than its call does here, so what is usual is looked at in one expression
+    # (5.9 us a call against 7.5); anything else goes through the checks below, which say what is wrong.
+    try:
+        (rows, k), (n, kw), device = x.shape, w.shape[-2:], x.get_device()
+        groups, blocks = 1 if counts is None else counts.numel(), k // BLOCK
+        usual = (stream is None and device >= 0 and kw == k and out.shape == (rows, n) and w.numel() == groups * n * k
+                 and xs.numel() == rows * blocks and ws.numel() == groups * -(-n // BLOCK) * blocks
+                 and x.dtype is _u8 and w.dtype is _u8 and xs.dtype is _f4 and ws.dtype is _f4
+                 and x.is_contiguous() and w.is_contiguous() and xs.is_contiguous() and ws.is_contiguous()
+                 and out.is_contiguous() and w.get_device() == device and xs.get_device() == device
+                 and ws.get_device() == device and out.get_device() == device and w.dim() < 4
+                 and (counts is None or (counts.dtype is _i4 and counts.is_contiguous() and counts.get_device() == device)))
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if usual:
+        return _run("lpc_gemm_fp8", device, None, x.data_ptr(), xs.data_ptr(), rows, k, w.data_ptr(), ws.data_ptr(), n, groups,
+                    None if counts is None else counts.data_ptr(), out.data_ptr(), _dtype(out))
     rows, k = _shape2(x, "x")
     n, kw = w.shape[-2:]
     groups = _groups(counts)
@@ -490,13 +510,34 @@ def lpc_router_forward(logits, experts, gates, counts, load, slope, loss, coef: 
                        mask=None, workspace=None, stream=None):
     """Routing of logits [rows, E]: experts (int32) and gates [rows, topk], counts (int32), load and slope [E],
     loss [1].  Without a workspace (uint8, lpc_router_workspace_bytes) one is taken from torch's allocator."""
+    try:  # the usual call in one expression, as in lpc_gemm_fp8
+        (rows, e), (r2, topk), device = logits.shape, experts.shape, logits.get_device()
+        usual = (stream is None and workspace is None and device >= 0 and r2 == rows
+                 and gates.numel() == rows * topk and counts.numel() == e and load.numel() == e and slope.numel() == e
+                 and loss.numel() == 1 and (logits.dtype is _f4 or logits.dtype is torch.bfloat16)
+                 and experts.dtype is _i4 and counts.dtype is _i4 and gates.dtype is _f4 and load.dtype is _f4
+                 and slope.dtype is _f4 and loss.dtype is _f4 and logits.is_contiguous() and experts.is_contiguous()
+                 and gates.is_contiguous() and counts.is_contiguous() and load.is_contiguous() and slope.is_contiguous()
+                 and experts.get_device() == device and gates.get_device() == device and counts.get_device() == device
+                 and load.get_device() == device and slope.get_device() == device and loss.get_device() == device
+                 and (mask is None or (mask.dtype in _MASK and mask.numel() == rows and mask.is_contiguous()
+                                       and mask.get_device() == device)))
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if usual:
+        need = lpc_router_workspace_bytes(rows, e)
+        space = torch.empty(need, dtype=_u8, device=logits.device) if need else None
+        return _run("lpc_router_forward", device, None, logits.data_ptr(), LPC_F32 if logits.dtype is _f4 else LPC_BF16, rows, e,
+                    topk, 1 if normalize else 0, coef, None if mask is None else mask.data_ptr(), experts.data_ptr(),
+                    gates.data_ptr(), counts.data_ptr(), load.data_ptr(), slope.data_ptr(), loss.data_ptr(),
+                    None if space is None else space.data_ptr(), need)
     rows, e = _shape2(logits, "logits")
     r2, topk = _shape2(experts, "experts")
     if r2 != rows:
         raise ValueError("experts has %d rows, expected %d" % (r2, rows))
     p = _Args()
     args = [p(logits, "logits", _FB, 0), _dtype(logits), rows, e, topk, 1 if normalize else 0, coef,
-            p.optional(mask, "mask", (torch.uint8, torch.bool), rows), p(experts, "experts", _I32, 0),
+            p.optional(mask, "mask", _MASK, rows), p(experts, "experts", _I32, 0),
             p(gates, "gates", _F32, rows * topk, True), p(counts, "counts", _I32, e, True),
             p(load, "load", _F32, e, True), p(slope, "slope", _F32, e, True), p(loss, "loss", _F32, 1, True)]
     need = lpc_router_workspace_bytes(rows, e)
@@ -517,7 +558,7 @@ def lpc_router_backward(logits, experts, slope, dgates, dloss, dlogits, normaliz
         raise ValueError("experts and dlogits do not match logits")
     p = _Args()
     args = (p(logits, "logits", _FB, 0), _dtype(logits), rows, e, topk, 1 if normalize else 0,
-            p.optional(mask, "mask", (torch.uint8, torch.bool), rows), p(experts, "experts", _I32, 0),
+            p.optional(mask, "mask", _MASK, rows), p(experts, "experts", _I32, 0),
             p(slope, "slope", _F32, e, True), p(dgates, "dgates", _F32, rows * topk, True),
             p(dloss, "dloss", _F32, 1, True), p(dlogits, "dlogits", _FB, rows * e, True))
     _run("lpc_router_backward", p.device, stream, *args)
