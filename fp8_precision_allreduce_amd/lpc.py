@@ -552,6 +552,23 @@ def lpc_router_forward(logits, experts, gates, counts, load, slope, loss, coef: 
 
 def lpc_router_backward(logits, experts, slope, dgates, dloss, dlogits, normalize: bool = True, mask=None, stream=None):
     """dlogits [rows, E] from dgates [rows, topk] and dloss [1], with the forward call's experts and slope."""
+    try:  # the usual call in one expression, as in lpc_gemm_fp8
+        (rows, e), (r2, topk), device = logits.shape, experts.shape, logits.get_device()
+        usual = (stream is None and device >= 0 and r2 == rows and slope.numel() == e and dgates.numel() == rows * topk
+                 and dloss.numel() == 1 and dlogits.numel() == rows * e and dlogits.dtype is logits.dtype
+                 and (logits.dtype is _f4 or logits.dtype is torch.bfloat16) and experts.dtype is _i4 and slope.dtype is _f4
+                 and dgates.dtype is _f4 and dloss.dtype is _f4 and logits.is_contiguous() and experts.is_contiguous()
+                 and slope.is_contiguous() and dgates.is_contiguous() and dlogits.is_contiguous()
+                 and experts.get_device() == device and slope.get_device() == device and dgates.get_device() == device
+                 and dloss.get_device() == device and dlogits.get_device() == device
+                 and (mask is None or (mask.dtype in _MASK and mask.numel() == rows and mask.is_contiguous()
+                                       and mask.get_device() == device)))
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if usual:
+        return _run("lpc_router_backward", device, None, logits.data_ptr(), LPC_F32 if logits.dtype is _f4 else LPC_BF16, rows, e,
+                    topk, 1 if normalize else 0, None if mask is None else mask.data_ptr(), experts.data_ptr(),
+                    slope.data_ptr(), dgates.data_ptr(), dloss.data_ptr(), dlogits.data_ptr())
     rows, e = _shape2(logits, "logits")
     r2, topk = _shape2(experts, "experts")
     if r2 != rows or dlogits.dtype != logits.dtype:

@@ -687,3 +687,26 @@ def test_binding_refusals(dev):
     assert e.value.status_name == "LPC_ERR_SHAPE"
     with pytest.raises(ValueError, match="holds"):
         lpc.AdamW([f32], [f32[:2]], [f32], [f32])
+
+
+def test_binding_usual_and_other_calls_agree(dev):
+    """A call that the binding checks in one expression and the same call by way of every single check (a stream given)."""
+    rng = np.random.RandomState(21)
+    x, xs = [t.to(dev) for t in quantize(torch.from_numpy(rng.standard_normal((70, 384)).astype(np.float32)))]
+    w, ws = [t.to(dev) for t in weights(2, 200, 384, rng)]
+    counts = torch.tensor([30, 35], dtype=torch.int32, device=dev)
+    lg, mask = logits(70, 24, torch.bfloat16, holes=True).to(dev), (torch.rand(70, device=dev) < 0.7)
+    dg, dl = torch.randn(70, 3, device=dev), torch.ones(1, device=dev)
+    results = []
+    for stream in (None, torch.cuda.current_stream()):
+        out = torch.empty(70, 200, device=dev)
+        lpc.lpc_gemm_fp8(x, xs, w, ws, out, counts=counts, stream=stream)
+        o = [torch.empty(70, 3, dtype=torch.int32, device=dev), torch.empty(70, 3, device=dev),
+             torch.empty(24, dtype=torch.int32, device=dev), torch.empty(24, device=dev), torch.empty(24, device=dev),
+             torch.empty(1, device=dev)]
+        lpc.lpc_router_forward(lg, *o, coef=0.1, mask=mask, stream=stream)
+        dx = torch.empty_like(lg)
+        lpc.lpc_router_backward(lg, o[0], o[4], dg, dl, dx, mask=mask, stream=stream)
+        torch.cuda.synchronize()
+        results.append([out, *o, dx])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
