@@ -139,33 +139,39 @@ struct Work {
     bool none;         // nothing at all to do
 };
 
+__device__ __forceinline__ Work product_work(const GemmArgs& a, const GroupTile& t) {
+    const uint32_t blocks = (uint32_t)(a.ld / kBlock);
+    const size_t g = t.group < a.groups ? t.group : 0;
+    Work w;
+    w.q0 = t.row;
+    w.nq = t.rows;
+    w.b0 = 0;
+    w.b1 = t.group < a.groups ? blocks : 0;  // rows past the last group: an empty sum
+    w.p = a.p + g * a.np * a.ld;
+    w.ps = a.ps + g * ((a.np + kBlock - 1) / kBlock) * blocks;
+    w.out = 0;
+    w.none = t.rows == 0;
+    return w;
+}
+
+// t: the group's blocks of 128 rows
+__device__ __forceinline__ Work wgrad_work(const GemmArgs& a, const GroupTile& t, uint32_t q0, uint32_t BQ) {
+    Work w;
+    w.q0 = q0;
+    w.nq = min(BQ, a.nq - q0);
+    w.b0 = t.before;
+    w.b1 = t.before + t.tiles;
+    w.p = a.p;
+    w.ps = a.ps;
+    w.out = (size_t)t.group * a.nq * a.np;
+    w.none = false;
+    return w;
+}
+
 template <int M, uint32_t BQ>
 __device__ __forceinline__ Work find_work(const GemmArgs& a, uint32_t tq, uint32_t z) {
-    Work w;
-    if constexpr (M == kProduct) {
-        const GroupTile t = find_tile(a.counts, a.groups, a.rows, BQ, tq);
-        const uint32_t blocks = (uint32_t)(a.ld / kBlock);
-        const size_t g = t.group < a.groups ? t.group : 0;
-        w.q0 = t.row;
-        w.nq = t.rows;
-        w.b0 = 0;
-        w.b1 = t.group < a.groups ? blocks : 0;  // rows past the last group: an empty sum
-        w.p = a.p + g * a.np * a.ld;
-        w.ps = a.ps + g * ((a.np + kBlock - 1) / kBlock) * blocks;
-        w.out = 0;
-        w.none = t.rows == 0;
-    } else {
-        const GroupTile t = find_group(a.counts, a.groups, a.rows, kBlock, z);
-        w.q0 = tq * BQ;
-        w.nq = min(BQ, a.nq - w.q0);
-        w.b0 = t.before;
-        w.b1 = t.before + t.tiles;
-        w.p = a.p;
-        w.ps = a.ps;
-        w.out = (size_t)z * a.nq * a.np;
-        w.none = false;
-    }
-    return w;
+    if constexpr (M == kProduct) return product_work(a, find_tile(a.counts, a.groups, a.rows, BQ, tq));
+    else return wgrad_work(a, find_group(a.counts, a.groups, a.rows, kBlock, z), tq * BQ, BQ);
 }
 
 // ---------------------------------------------------------------------------
@@ -727,7 +733,8 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_product_kernel(GemmA
     using L = Large<Out>;
     constexpr uint32_t PartsQ = L::BQ / Small::BQ, PartsP = L::BP / Small::BP, Parts = PartsQ * PartsP;
     __shared__ __attribute__((aligned(128))) uint8_t lds[L::kBytes > Small::kBytes ? L::kBytes : Small::kBytes];
-    const uint32_t tiles_q = count_tiles(a.counts, a.groups, a.rows, L::BQ), tiles_p = (a.np + L::BP - 1) / L::BP;
+    const TileScan tiles(a.counts, a.groups, a.rows, L::BQ);
+    const uint32_t tiles_q = tiles.all, tiles_p = (a.np + L::BP - 1) / L::BP;
     const uint32_t x = blockIdx.x % kXcds, k = blockIdx.x / kXcds;
     const uint32_t all = tiles_q * tiles_p, rest = all % kXcds;
     const uint32_t first = x * (all / kXcds) + min(x, rest), mine = all / kXcds + (x < rest);
@@ -736,7 +743,7 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_product_kernel(GemmA
     if (k >= whole + split * Parts) return;
     const uint32_t n = k < whole ? k : whole + (k - whole) / Parts;
     const uint2 t = in_bands(first + n, tiles_q, tiles_p);
-    Work w = find_work<kProduct, L::BQ>(a, t.x, 0);
+    Work w = product_work(a, tiles.find(t.x));
     if (k < whole && w.nq > Small::BQ) {
         tile<kProduct, Out, L>(a, w, t.y * L::BP, lds);
         return;
@@ -755,16 +762,16 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_product_kernel(GemmA
 
 // The group with the z-th most rows, for up to 64 groups: their tiles take times that differ as their rows do, and the
 // long ones come first, so that short ones fill the end.
-__device__ __forceinline__ uint32_t by_rows(const GemmArgs& a, uint32_t z) {
-    if (!a.counts || a.groups > 64) return z;
-    const uint32_t lane = threadIdx.x & 63;
-    const uint32_t c = lane < a.groups ? group_rows(a.counts, lane, a.rows) : 0;
+__device__ __forceinline__ GroupTile group_by_rows(const GemmArgs& a, uint32_t z) {
+    if (a.groups > 64) return find_group(a.counts, a.groups, a.rows, kBlock, z);
+    const GroupScan s(a.counts, a.groups, a.rows, kBlock, 0, 0, 0);
+    const uint32_t lane = threadIdx.x & 63, mine = s.end - s.begin;
     uint32_t rank = 0;
     for (uint32_t g = 0; g < a.groups; ++g) {
-        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)c, (int)g);
-        rank += o > c || (o == c && g < lane);
+        const uint32_t other = from_lane(mine, g);
+        rank += other > mine || (other == mine && g < lane);
     }
-    return (uint32_t)__builtin_ctzll(__ballot(lane < a.groups && rank == z));
+    return group_of_lane(s, 0, (uint32_t)__builtin_ctzll(__ballot(lane < a.groups && rank == z)));
 }
 
 template <typename S>
@@ -772,7 +779,7 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_wgrad_kernel(GemmArg
     __shared__ __attribute__((aligned(128))) uint8_t lds[S::kBytes];
     const uint32_t tiles_p = (a.np + S::BP - 1) / S::BP;
     const uint2 t = in_bands((uint32_t)xcd_tile(), gridDim.x / tiles_p, tiles_p);
-    tile<kWgrad, float, S>(a, find_work<kWgrad, S::BQ>(a, t.x, by_rows(a, blockIdx.y)), t.y * S::BP, lds);
+    tile<kWgrad, float, S>(a, wgrad_work(a, group_by_rows(a, blockIdx.y), t.x * S::BQ, S::BQ), t.y * S::BP, lds);
 }
 
 template <typename Out>

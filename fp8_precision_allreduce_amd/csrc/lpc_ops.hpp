@@ -45,7 +45,7 @@ __device__ __forceinline__ uint32_t group_rows(const int32_t* __restrict__ count
     return c < 0 ? 0u : min((uint32_t)c, most);
 }
 
-// A lane's group among 64: its rows, and its tiles and those before it.  Groups
+// A lane's group among 64 (a single one of all rows where there are no counts): its rows, and its tiles and those before it.  Groups
 // end at `rows`, so their ends are a running sum that stops there.  Every lane
 // of the wavefront has to be active.
 struct GroupScan {
@@ -58,7 +58,7 @@ struct GroupScan {
                                          uint32_t first, uint32_t row, uint32_t tile) {
         const uint32_t lane = threadIdx.x & 63, here = min(groups - first, 64u);
         last = here - 1;
-        uint32_t sum = lane < here ? group_rows(counts, first + lane, rows) : 0;
+        uint32_t sum = lane >= here ? 0 : counts ? group_rows(counts, first + lane, rows) : rows;
         for (uint32_t d = 1; d < here; d *= 2) {
             const uint32_t o = (uint32_t)__shfl_up((int)sum, d);
             if (lane >= d) sum = min(sum + o, rows);
@@ -80,22 +80,30 @@ __device__ __forceinline__ uint32_t from_lane(uint32_t v, uint32_t lane) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, (int)lane);
 }
 
+// lane l's group, l + first
+__device__ __forceinline__ GroupTile group_of_lane(const GroupScan& s, uint32_t first, uint32_t l) {
+    return {first + l, from_lane(s.begin, l), from_lane(s.end - s.begin, l), from_lane(s.before, l), from_lane(s.tiles, l)};
+}
+
+// tile t of a lane's group, if it is one of these
+__device__ __forceinline__ bool tile_of_lanes(const GroupScan& s, uint32_t first, uint32_t T, uint32_t t, GroupTile* out) {
+    const unsigned long long has = __ballot(t - s.before < s.tiles);
+    if (!has) return false;
+    *out = group_of_lane(s, first, (uint32_t)__builtin_ctzll(has));
+    const uint32_t off = (t - out->before) * T;
+    out->row += off;
+    out->rows = min(T, out->rows - off);
+    return true;
+}
+
 // Tile number t.
 __device__ __forceinline__ GroupTile find_tile(const int32_t* __restrict__ counts, uint32_t groups, uint32_t rows,
                                                uint32_t T, uint32_t t) {
     uint32_t row = 0, before = 0;
-    if (!counts) {
-        const uint32_t n = (rows + T - 1) / T;
-        if (t < n) return {0, t * T, min(T, rows - t * T), 0, n};
-        return {1, rows, 0, n, 0};
-    }
     for (uint32_t first = 0; first < groups; first += 64) {
         const GroupScan s(counts, groups, rows, T, first, row, before);
-        if (const unsigned long long has = __ballot(t - s.before < s.tiles)) {
-            const uint32_t l = (uint32_t)__builtin_ctzll(has);
-            const uint32_t begin = from_lane(s.begin, l), b = from_lane(s.before, l), off = (t - b) * T;
-            return {first + l, begin + off, min(T, from_lane(s.end, l) - begin - off), b, from_lane(s.tiles, l)};
-        }
+        GroupTile found;
+        if (tile_of_lanes(s, first, T, t, &found)) return found;
         row = from_lane(s.end, s.last);
         before = from_lane(s.before + s.tiles, s.last);
     }
@@ -104,27 +112,38 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t* __restrict__ count
     return {groups, rows, 0u, before, n};
 }
 
-// Tiles of all groups and of the rows past the last one.
-__device__ __forceinline__ uint32_t count_tiles(const int32_t* __restrict__ counts, uint32_t groups, uint32_t rows,
-                                                uint32_t T) {
-    uint32_t row = 0, before = 0;
-    for (uint32_t first = 0; counts && first < groups; first += 64) {
-        const GroupScan s(counts, groups, rows, T, first, row, before);
-        row = from_lane(s.end, s.last);
-        before = from_lane(s.before + s.tiles, s.last);
+// All tiles: how many there are, those of the rows past the last group among them, and a tile by its number.  The counts
+// of up to 64 groups are read once for both.
+struct TileScan {
+    const int32_t* counts;
+    uint32_t groups, rows, T, all;
+    GroupScan scan;
+
+    __device__ __forceinline__ TileScan(const int32_t* __restrict__ c, uint32_t g, uint32_t r, uint32_t t)
+        : counts(c), groups(g), rows(r), T(t), scan(c, g, r, t, 0, 0, 0) {
+        uint32_t row = from_lane(scan.end, scan.last), before = from_lane(scan.before + scan.tiles, scan.last);
+        for (uint32_t first = 64; first < groups; first += 64) {
+            const GroupScan s(counts, groups, rows, T, first, row, before);
+            row = from_lane(s.end, s.last);
+            before = from_lane(s.before + s.tiles, s.last);
+        }
+        all = before + (rows - row + T - 1) / T;
     }
-    return before + (rows - row + T - 1) / T;
-}
+
+    __device__ __forceinline__ GroupTile find(uint32_t t) const {
+        GroupTile found;
+        if (tile_of_lanes(scan, 0, T, t, &found)) return found;
+        return find_tile(counts, groups, rows, T, t);
+    }
+};
 
 // First tile and number of tiles of group g.
 __device__ __forceinline__ GroupTile find_group(const int32_t* __restrict__ counts, uint32_t groups, uint32_t rows,
                                                 uint32_t T, uint32_t g) {
     uint32_t row = 0, before = 0;
-    if (!counts) return {g, 0, rows, 0, (rows + T - 1) / T};
     for (uint32_t first = 0;; first += 64) {
         const GroupScan s(counts, groups, rows, T, first, row, before);
-        if (const uint32_t l = g - first; l < 64)
-            return {g, from_lane(s.begin, l), from_lane(s.end - s.begin, l), from_lane(s.before, l), from_lane(s.tiles, l)};
+        if (g - first < 64) return group_of_lane(s, first, g - first);
         row = from_lane(s.end, s.last);
         before = from_lane(s.before + s.tiles, s.last);
     }
