@@ -581,6 +581,19 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
         if (group == 1) end_slot();
         const uint32_t in_row = l16 * kBlock, lo = (l4 ^ (l16 & 7)) * 16;
         const uint32_t q_at = wq * QW * kBlock + in_row, p_at = wp * PW * kBlock + in_row;
+        // fp32 out: the last two products of a slot are taken up in the wavefront's next one, when the matrix core is
+        // done with them (weight gradient of 8 groups 498 us against 514; to bf16 it gained nothing).
+        f32x4_t late[2] = {}, late_scale[2] = {};
+        auto take_up_late = [&]() {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                f32x4_t& to = acc[Phases * F - 1][PF - 2 + n / 4];
+                float c = __builtin_fmaf(late[n / 4][n % 4], late_scale[n / 4][n % 4], to[n % 4]);
+                asm volatile("" : "+v"(c));
+                to[n % 4] = c;
+            }
+        };
+        static_assert(sizeof(Out) == 2 || Phases == 1, "the late products' accumulators");
         uint32_t at = 0;  // stage of block b
         for (uint32_t b = 0; b < nb; ++b) {
             const Stage& s = stage[at];
@@ -614,6 +627,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
                 if (Phases == 1 && b + 2 < nb) load_range(0, kLoads, b + 2, last);
                 if (Phases == 2 && ph == 0 && b + 1 < nb) load_range(kEarly, kLoads, b + 1, after);
                 if (Phases == 2 && ph == 1 && b + 2 < nb) load_range(0, kEarly, b + 2, at);
+                if constexpr (sizeof(Out) == 4) take_up_late();
                 // widened here, while the other group multiplies
                 if (ph == 0) {
 #pragma unroll
@@ -648,19 +662,23 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
                     }
                 } else {
 #pragma unroll
-                    for (int t = 0; t < F * PF + 2; t += 2) {
+                    for (int t = 0; t < F * PF; t += 2) {
 #pragma unroll
                         for (int n = 0; n < 8; ++n) {  // two products' chains of four instructions in turn
                             const int u = t + n % 2;
-                            if (t < F * PF) {
-                                if (n < 2) part[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-                                part[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pv[u % PF].h[n / 2],
-                                                                                 qv[u / PF].h[n / 2], part[u], 0, 0, 0);
-                            }
+                            if (n < 2) part[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                            part[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pv[u % PF].h[n / 2], qv[u / PF].h[n / 2],
+                                                                             part[u], 0, 0, 0);
                             __builtin_amdgcn_sched_barrier(0);
                             if (t >= 2) take_up(t - 2 + n / 4, n % 4);
                             __builtin_amdgcn_sched_barrier(0);
                         }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float q = qs[F - 1];
+                        late[h] = part[F * PF - 2 + h];
+                        late_scale[h] = M == kProduct ? f32x4_t{q, q, q, q} : q * ps[PF - 2 + h];
                     }
                 }
                 if (group == 0) {
@@ -671,6 +689,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
             }
             at = after;
         }
+        if constexpr (sizeof(Out) == 4) take_up_late();
         if (group == 0) end_slot();
     }
 
