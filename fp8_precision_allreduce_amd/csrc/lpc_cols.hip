@@ -8,6 +8,10 @@
 // the four rows of a column make one dword of the transposed codes, which LDS
 // turns into runs of 128 bytes.  The padded rows of a group's last block are
 // zeros in every lane, so no lane leaves before the reductions.
+//
+// Bound by the vector unit, about 12 instructions an element, six of them the
+// correctly rounded quotient, and close behind by HBM: 16,384 x 7168 rows held as
+// codes take 61 us (235 MB, 3.9 TB/s), 16,384 x 2048 bf16 with both forms 35 us.
 #include "lpc_ops.hpp"
 
 namespace lpc {

@@ -177,7 +177,9 @@ __device__ __forceinline__ Work find_work(const GemmArgs& a, uint32_t tq, uint32
 // ---------------------------------------------------------------------------
 // split: 16 QF x 16 PF outputs per workgroup, its 8 wavefronts take every
 // eighth block and their sums are joined through LDS, in the wavefronts' order.
-// Operands go straight to registers.
+// Operands go straight to registers.  For up to 16 rows, where the weight is all
+// there is to read: 1 x 8192 x 8192 takes 11.8 us, 5.7 TB/s.  Loads further ahead
+// of their use, 2 to 4 blocks, took longer (15.7): 16 wavefronts a CU cover it.
 // ---------------------------------------------------------------------------
 
 constexpr int kSplitWaves = 8;
