@@ -407,6 +407,20 @@ def _run(name, device, stream, *args):
         raise LpcError(name, st, lpc_status_string(st))
 
 
+def _torch_stream(stream, device):
+    return stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+
+
+def _scratch(size, device, stream):
+    """Device memory for one call.  It comes from the pool of the stream that the call runs on: a block of another
+    stream's pool may still be in use there, and nothing would order the call after that."""
+    if stream is None:
+        return torch.empty(size, dtype=_u8, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        return torch.empty(size, dtype=_u8, device=device)
+
+
 def _shape2(t, what):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError("%s must be a 2-D tensor" % what)
@@ -542,10 +556,7 @@ def lpc_router_forward(logits, experts, gates, counts, load, slope, loss, coef: 
             p(load, "load", _F32, e, True), p(slope, "slope", _F32, e, True), p(loss, "loss", _F32, 1, True)]
     need = lpc_router_workspace_bytes(rows, e)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
-        if stream is not None:  # allocated for the current stream, used on the given one
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(int(stream), device=logits.device))
+        workspace = _scratch(need, logits.device, stream)
     space = (None, 0) if workspace is None else (p(workspace, "workspace", _U8, 0), workspace.numel())
     _run("lpc_router_forward", p.device, stream, *args, *space)
 
