@@ -599,7 +599,8 @@ class AdamW:
     and updated in place; the tensors must stay where they are.  With m_scales and v_scales the moments are E4M3
     codes (uint8) with one fp32 scale per 128 elements, v holding the root of the second moment.  copies: bf16
     tensors that get the updated params.  A step reads no tensor's address again, so it can be captured in a graph
-    (its hyperparameters are then the captured ones)."""
+    (its hyperparameters are then the captured ones; the object has to live as long as the graph is replayed), and a
+    gradient that a program replaces by another tensor needs a new AdamW."""
 
     def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, copies=None):
         if (m_scales is None) != (v_scales is None):
@@ -634,6 +635,8 @@ class AdamW:
               ctypes.byref(chunks))
         self._chunks = chunks.value
         self._plan = host.to("cuda:%d" % self.device) if self._chunks else None
+        # streams after whose work the plan may be handed out again when this object goes: that of its pool, and those of steps
+        self._streams = {torch._C._cuda_getCurrentRawStream(self.device)} if self._chunks else set()
 
     def step(self, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
              weight_decay: float = 0.01, grad_scale=None, stream=None):
@@ -642,5 +645,9 @@ class AdamW:
             return
         p = _Args()
         p.device = self.device
-        _run("lpc_adamw_step", self.device, stream, self._plan.data_ptr(), self._chunks, self.grad_dtype,
+        handle = torch._C._cuda_getCurrentRawStream(self.device) if stream is None else getattr(stream, "cuda_stream", stream)
+        if handle not in self._streams:
+            self._plan.record_stream(_torch_stream(handle, self._plan.device))
+            self._streams.add(handle)
+        _run("lpc_adamw_step", self.device, handle, self._plan.data_ptr(), self._chunks, self.grad_dtype,
              self.state_bits, step, lr, beta1, beta2, eps, weight_decay, p.optional(grad_scale, "grad_scale", _F32, 1))
