@@ -39,7 +39,7 @@ bool bad_groups(int groups) { return groups < 1 || groups > LPC_MAX_GROUPS; }
 bool missing_counts(int groups, const int32_t* counts) { return groups > 1 && !counts; }
 
 size_t padded_rows(size_t rows, int groups) {
-    if (rows == 0 || groups < 1) return 0;
+    if (rows == 0 || rows >= kMaxDim || groups < 1) return 0;
     return LPC_BLOCK * ((rows + LPC_BLOCK - 1) / LPC_BLOCK + (size_t)groups - 1);
 }
 
@@ -88,7 +88,8 @@ lpc_status lpc_quantize_fp8_cols(const void* y, lpc_dtype in, size_t rows, size_
     if (rows == 0 || n == 0) return LPC_OK;
     if (!y || !codes_t || !scales_t || !codes != !scales || missing_counts(groups, counts)) return LPC_ERR_NULL;
     if (any_misaligned(y, codes_t, scales_t, codes, scales) || misaligned4(counts)) return LPC_ERR_ALIGN;
-    if (bad_groups(groups) || n % LPC_BLOCK || too_many(padded_rows(rows, groups), n)) return LPC_ERR_SHAPE;
+    if (bad_groups(groups) || n % LPC_BLOCK || rows >= kMaxDim || too_many(padded_rows(rows, groups), n))
+        return LPC_ERR_SHAPE;
     return hip_status(lpc::launch_quantize_cols(y, in == LPC_BF16, rows, n, padded_rows(rows, groups), groups, counts,
                                                 codes_t, scales_t, codes, scales, stream));
 }
@@ -98,7 +99,8 @@ lpc_status lpc_requantize_fp8_cols(const uint8_t* x, const float* xs, size_t row
     if (rows == 0 || k == 0) return LPC_OK;
     if (!x || !xs || !codes_t || !scales_t || missing_counts(groups, counts)) return LPC_ERR_NULL;
     if (any_misaligned(x, xs, codes_t, scales_t) || misaligned4(counts)) return LPC_ERR_ALIGN;
-    if (bad_groups(groups) || k % LPC_BLOCK || too_many(padded_rows(rows, groups), k)) return LPC_ERR_SHAPE;
+    if (bad_groups(groups) || k % LPC_BLOCK || rows >= kMaxDim || too_many(padded_rows(rows, groups), k))
+        return LPC_ERR_SHAPE;
     return hip_status(lpc::launch_requantize_cols(x, xs, rows, k, padded_rows(rows, groups), groups, counts, codes_t,
                                                   scales_t, stream));
 }
@@ -111,7 +113,7 @@ lpc_status lpc_gemm_fp8_wgrad(const uint8_t* yt, const float* ys, size_t n, cons
     if (rows != 0 && any_null(ys, xs)) return LPC_ERR_NULL;
     if (any_misaligned(yt, ys, xt, xs, dw) || misaligned4(counts)) return LPC_ERR_ALIGN;
     const size_t padded = padded_rows(rows, groups);
-    if (bad_groups(groups) || too_many(padded, n) || too_many(padded, k) || too_many(n, k) ||
+    if (bad_groups(groups) || rows >= kMaxDim || too_many(padded, n) || too_many(padded, k) || too_many(n, k) ||
         n * k > LPC_MAX_MATRIX / (size_t)groups)
         return LPC_ERR_SHAPE;
     return hip_status(lpc::launch_wgrad(yt, ys, n, xt, xs, k, rows, padded, groups, counts, dw, stream));

@@ -67,7 +67,8 @@ lpc_status lpc_gemm_fp8(const uint8_t *x, const float *xs, size_t rows, size_t k
  * lpc_gemm_fp8_wgrad reads: each group starts at a multiple of 128, after the
  * groups before it rounded up to 128.  The result depends on the sizes alone
  * and is enough for any counts: 128 * (ceil(rows/128) + groups - 1), or 0 when
- * rows == 0 or groups < 1.  No HIP call.                                     */
+ * rows == 0, rows >= 2^31 (which every call refuses) or groups < 1.  No HIP
+ * call.                                                                      */
 size_t lpc_padded_rows(size_t rows, int groups);
 
 /* Quantize a matrix along its columns, and in the same pass along its rows:

@@ -89,6 +89,21 @@ def test_wgrad_errors(L):
         assert f(*replaced(ok, **bad)) == SHAPE, bad
 
 
+def test_row_counts_that_wrap_are_refused(L):
+    """Rounding such a count up to whole blocks passes SIZE_MAX; a negative Python int becomes one."""
+    for rows in ((1 << 64) - 1, (1 << 64) - 99, (1 << 64) - 127, (1 << 64) - 128, 1 << 63, 1 << 32, 1 << 31):
+        for groups in (1, 2, 1024):
+            assert L.lpc_padded_rows(rows, groups) == 0, (rows, groups)
+            assert L.lpc_quantize_fp8_cols(A, BF16, rows, 256, groups, A, A, A, A, A, None) == SHAPE, (rows, groups)
+            assert L.lpc_requantize_fp8_cols(A, A, rows, 256, groups, A, A, A, None) == SHAPE, (rows, groups)
+            assert L.lpc_gemm_fp8_wgrad(A, A, 7, A, A, 9, rows, groups, A, A, None) == SHAPE, (rows, groups)
+            assert L.lpc_gemm_fp8(A, A, rows, 256, A, A, 100, groups, A, A, BF16, None) == SHAPE, (rows, groups)
+        assert L.lpc_router_workspace_bytes(rows, 60) == 0
+        assert L.lpc_router_forward(A, BF16, rows, 60, 4, 1, 0.01, None, A, A, A, A, A, A, A, 1 << 30, None) == SHAPE
+        assert L.lpc_router_backward(A, F32, rows, 60, 4, 1, None, A, A, A, A, A, None) == SHAPE
+    assert lpc.lpc_padded_rows(-1, 2) == 0
+
+
 def test_router_errors(L):
     f, g = L.lpc_router_forward, L.lpc_router_backward
     need = lpc.lpc_router_workspace_bytes(1000, 60)
