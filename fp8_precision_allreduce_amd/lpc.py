@@ -437,7 +437,9 @@ def _blocks(n):
 
 def lpc_gemm_fp8(x, xs, w, ws, out, counts=None, stream=None):
     """out [rows, n] = x [rows, k] times w [groups, n, k] (or [n, k]) transposed, E4M3 codes with scales
-    xs [rows, k/128] and ws [groups, ceil(n/128), k/128]; counts [groups] int32: rows of each group."""
+    xs [rows, k/128] and ws [groups, ceil(n/128), k/128]; counts [groups] int32: rows of each group.  Sums are FP32 where
+    out is; for a bf16 out the matrix instruction drops what is small beside the largest of 8 neighbouring products
+    (include/lpc_ops.h gives the bound)."""
     # A small product takes less time on the GPU than its call does here, so what is usual is looked at in one expression
     # (5.9 us a call against 7.5); anything else goes through the checks below, which say what is wrong.
     try:
