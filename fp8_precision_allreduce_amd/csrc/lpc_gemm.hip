@@ -286,13 +286,17 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 // 16 (4) bytes a lane from base + off to LDS at `to` + 16 (4) lane.  The compiler does not count
-// these loads: lds_arrived() waits until at most `Left` of them are on their way.  M0 is read one wait state after it is written.
+// these loads: lds_arrived() waits until at most `Left` of them are on their way.  M0 is read one wait state after it is written,
+// and is named as overwritten, so that no use of it by the compiler is carried across (the warning says that it is not saved either).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "m0");
 }
 __device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base) : "m0");
 }
+#pragma clang diagnostic pop
 template <int Left>
 __device__ __forceinline__ void lds_arrived() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Left) : "memory");
