@@ -401,6 +401,14 @@ struct RouterGradArgs {
     int normalize;
 };
 
+// A row's LDS belongs to one wavefront, whose LDS operations take effect in the order of its instructions; the compiler has
+// to keep that order between lanes too, which it sees no reason for (the barrier alone is no statement about memory).
+__device__ __forceinline__ void row_in_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // Reads and writes 32 MiB for 16,384 x 256 in 11 us; streaming stores, which leave nothing to write back at the end,
 // are a tenth of that.
 //
@@ -423,7 +431,7 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
         up[j] = e < a.experts ? dloss * a.slope[e] : 0.0f;
         direct[group][e] = 0.0f;
     }
-    __builtin_amdgcn_wave_barrier();  // a row's LDS belongs to one wavefront, whose operations stay in order
+    row_in_order();
 
     for (size_t r = (size_t)blockIdx.x * kGroups + group; r < a.rows; r += (size_t)gridDim.x * kGroups) {
         float x[Per];
@@ -464,7 +472,7 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
                 slot = dg;
             }
             if (index != kNone) direct[group][index] = slot;
-            __builtin_amdgcn_wave_barrier();
+            row_in_order();
             float dot = 0.0f;
 #pragma unroll
             for (int j = 0; j < Per; ++j) {
@@ -476,9 +484,9 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterGradArg
 #pragma unroll
             for (int j = 0; j < Per; ++j)
                 dx[j] = a.normalize ? p[j] * (up[j] - dot) + dx[j] : p[j] * ((up[j] + dx[j]) - dot);
-            __builtin_amdgcn_wave_barrier();
+            row_in_order();
             if (index != kNone) direct[group][index] = 0.0f;
-            __builtin_amdgcn_wave_barrier();
+            row_in_order();
         }
         In* out = dlogits + r * a.experts;
         if (L::V == 4 && whole) {

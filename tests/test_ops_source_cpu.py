@@ -1,4 +1,4 @@
-"""What the compiler has to be told about the operators' inline assembly, read from the sources."""
+"""What the compiler has to be told about inline assembly and the order of memory, read from the sources."""
 import glob
 import os
 import re
@@ -26,3 +26,12 @@ def test_statements_are_found():
     text = 'asm volatile("s_mov_b32 m0, %0\\n\\tx" ::"s"(a) : "m0"); asm volatile("" ::: "memory");'
     assert [i for i, _ in statements(text)] == ["s_mov_b32 m0, %0\\n\\tx", ""]
     assert sum("m0" in i for i, _ in statements(open(os.path.join(CSRC, "lpc_gemm.hip")).read())) == 2
+
+
+@pytest.mark.parametrize("name", ["lpc_gemm.hip", "lpc_cols.hip", "lpc_router.hip", "lpc_adamw.hip", "lpc_ops.hpp"])
+def test_wave_barriers_order_memory(name):
+    """A wave barrier keeps no load or store where it is; where lanes exchange values through LDS a fence has to."""
+    fence = r'__builtin_amdgcn_fence\(__ATOMIC_ACQ_REL, "wavefront"\);\s*'
+    text = open(os.path.join(CSRC, name)).read()
+    assert len(re.findall(r"__builtin_amdgcn_wave_barrier\(\);", text)) == \
+        len(re.findall(fence + r"__builtin_amdgcn_wave_barrier\(\);\s*" + fence, text))
