@@ -22,7 +22,10 @@
  * call to call: no sum depends on the order in which workgroups run.
  *
  * Inputs must be finite (router logits may also be -infinity), and so must the
- * sums; otherwise the affected results are unspecified.
+ * sums; otherwise the affected results are unspecified.  The products multiply
+ * a block's two scales first, rounded to FP32: that must be finite too, also
+ * where the block's sum is small or zero, and where it is below 2^-126 it has a
+ * denormal's precision, which changes a result by at most 2^-125 a block.
  */
 #ifndef LPC_OPS_H
 #define LPC_OPS_H

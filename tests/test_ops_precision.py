@@ -110,12 +110,12 @@ def codes(v):
     return v.to(torch.float8_e4m3fn).view(torch.uint8)
 
 
-def product(x, w, out_t, counts=None):
-    """x [rows, k] times w [groups, n, k], all scales one."""
+def product(x, w, out_t, counts=None, xs=1.0, ws=1.0):
+    """x [rows, k] times w [groups, n, k], all scales xs and ws."""
     dev, (g, n, k) = x.device, w.shape
     out = torch.full((x.shape[0], n), float("nan"), dtype=out_t, device=dev)
-    lpc.lpc_gemm_fp8(codes(x), torch.ones(x.shape[0], k // BLOCK, device=dev), codes(w),
-                     torch.ones(g, -(-n // BLOCK), k // BLOCK, device=dev), out,
+    lpc.lpc_gemm_fp8(codes(x), torch.full((x.shape[0], k // BLOCK), xs, device=dev), codes(w),
+                     torch.full((g, -(-n // BLOCK), k // BLOCK), ws, device=dev), out,
                      counts=None if counts is None else torch.tensor(counts, dtype=torch.int32, device=dev))
     return out
 
@@ -199,3 +199,41 @@ def test_weight_gradients_are_exact(dev, rows, n, k, counts):
         part = slice(at, at + b * BLOCK)
         assert torch.equal(dw[i].cpu().double(), yt[:, part] @ xt[:, part].t()), i
         at += b * BLOCK
+
+
+SCALES = [(1.25 * 2.0 ** -80, 1.75 * 2.0 ** -69),             # multiply to 2.1875 2^-149: rounded to 2 of a denormal's steps
+          (1.25 * 2.0 ** -60, 1.75 * 2.0 ** -72),
+          (1.25 * 2.0 ** -100, 1.75 * 2.0 ** -20),
+          (1.25 * 2.0 ** 60, 1.5 * 2.0 ** 43),                # sums near FP32's largest
+          (1.25 * 2.0 ** 120, 1.5 * 2.0 ** -120)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out_t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("xs,ws", SCALES)
+def test_products_of_extreme_scales(dev, xs, ws, out_t):
+    for rows, k, n in ((3, 128, 200), (30, 256, 200), (512, 384, 1100), (2100, 128, 1700)):
+        say("scales rows=%d k=%d n=%d %g %g" % (rows, k, n, xs, ws))
+        g = generator(rows, dev)
+        x, w = (whole_numbers(m, k, g, dev).abs() for m in (rows, n))
+        sums = x.double() @ w.double().t() if out_t == torch.float32 else cut_sums(x, w)
+        want = sums * (xs * ws)
+        assert want.abs().max() < 3e38
+        off = (product(x, w[None], out_t, xs=xs, ws=ws).double() - want).abs()
+        # the scales' product, each block's product with it and its addition; below 2^-126 half a denormal's step of each
+        tol = want * (k // BLOCK + 2) * 2.0 ** -24 + k // BLOCK * 2.0 ** -125
+        assert (off <= tol + (want + tol) * (2.0 ** -8 if out_t == torch.bfloat16 else 0)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ys,xs", SCALES)
+def test_weight_gradients_of_extreme_scales(dev, ys, xs):
+    for rows, n, k in ((128, 100, 37), (128, 1030, 1100), (256, 2300, 2050)):
+        say("scales wgrad rows=%d n=%d k=%d %g %g" % (rows, n, k, ys, xs))
+        g, blocks = generator(rows, dev), rows // BLOCK
+        yt, xt = (whole_numbers(m, rows, g, dev).abs() for m in (n, k))
+        dw = torch.full((n, k), float("nan"), device=dev)
+        lpc.lpc_gemm_fp8_wgrad(codes(yt), torch.full((blocks, n), ys, device=dev), codes(xt),
+                               torch.full((blocks, k), xs, device=dev), dw, rows)
+        want = (yt.double() @ xt.double().t()) * (ys * xs)
+        assert ((dw.double() - want).abs() <= want * (blocks + 2) * 2.0 ** -24 + blocks * 2.0 ** -125).all()
