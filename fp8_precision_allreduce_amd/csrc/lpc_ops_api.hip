@@ -213,7 +213,9 @@ lpc_status lpc_adamw_step(const void* plan, size_t chunks, lpc_dtype grad_t, int
     if (chunks == 0) return LPC_OK;
     if (!plan) return LPC_ERR_NULL;
     if (misaligned(plan) || misaligned4(grad_scale)) return LPC_ERR_ALIGN;
-    if (chunks >= kMaxDim || step < 1) return LPC_ERR_SHAPE;
+    // a beta of one divides by zero, any other outside of [0, 1), NaN among them, is no mean
+    const bool means = beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0;
+    if (chunks >= kMaxDim || step < 1 || !means) return LPC_ERR_SHAPE;
     lpc::AdamwScalars s;
     s.beta1 = (float)beta1;
     s.rest1 = (float)(1.0 - beta1);

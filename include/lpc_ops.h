@@ -212,7 +212,7 @@ lpc_status lpc_adamw_plan(const lpc_adamw_tensor *tensors, int count, lpc_dtype 
  * in FP32, every operation rounded on its own; the scalars in front are
  * computed in double and rounded once.
  *   plan      DEVICE copy of the plan;  chunks, grad_t, state_bits as planned
- *   step >= 1 (else LPC_ERR_SHAPE)                                           */
+ *   step >= 1, beta1 and beta2 in [0, 1) (else LPC_ERR_SHAPE)                */
 lpc_status lpc_adamw_step(const void *plan, size_t chunks, lpc_dtype grad_t, int state_bits,
                           int64_t step, double lr, double beta1, double beta2, double eps,
                           double weight_decay, const float *grad_scale, hipStream_t stream);

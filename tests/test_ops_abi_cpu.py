@@ -190,6 +190,15 @@ def test_adamw_step_errors(L):
     assert f(*replaced(ok, _4=0)) == SHAPE and f(*replaced(ok, _1=1 << 31)) == SHAPE
 
 
+def test_adamw_step_refuses_betas_that_are_no_means(L):
+    ok = [A, 3, F32, 32, 1, 1e-3, 0.9, 0.99, 1e-8, 0.1, None, None]
+    for i in (6, 7):
+        for beta in (1.0, 1.5, -0.1, float("nan"), float("inf"), -float("inf")):
+            assert L.lpc_adamw_step(*replaced(ok, **{"_%d" % i: beta})) == SHAPE, (i, beta)
+        for beta in (0.0, 0.5, 1.0 - 2.0 ** -53):
+            assert L.lpc_adamw_step(*replaced(ok, **{"_%d" % i: beta})) == HIP, (i, beta)
+
+
 def test_binding_refuses_host_tensors(L):
     u8, f32 = torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(4, 1)
     with pytest.raises(ValueError, match="GPU tensor"):
