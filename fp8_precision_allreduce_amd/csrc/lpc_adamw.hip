@@ -6,9 +6,13 @@
 // first use.  With 8-bit moments 32 neighbouring lanes own a scale block and
 // its maximum is reduced across them (group32_max), both moments in registers.
 //
-// Bound by HBM: 134 M elements with 8-bit moments, bf16 gradients and copies
-// (16 bytes each) take 380 us, 5.7 TB/s; 34 M with fp32 moments and gradients
-// (28 bytes) 157 us, 6.0 TB/s.  A plain copy of 4 GiB reaches 4.8.
+// fp32 moments are bound by HBM: 34 M elements with fp32 gradients (28 bytes each)
+// take 157 us, 6.0 TB/s, as much as a plain stream of the same reads and writes.
+// 8-bit moments are bound by the vector unit as much: about 100 instructions an
+// element (quotients, roots and the maxima of two scale blocks) at a clock that the
+// card's power holds low.  134 M elements with bf16 gradients and copies (16 bytes)
+// take 388 us, 5.6 TB/s against the stream's 6.3; the first passes after a pause
+// take 370, the next dozen up to 550 until the clock has settled.
 //
 // Every operation is rounded on its own, in the order of the formulas in
 // lpc_ops.h, so the result does not depend on how a tensor is split up.

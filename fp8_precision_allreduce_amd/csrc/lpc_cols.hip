@@ -9,9 +9,13 @@
 // turns into runs of 128 bytes.  The padded rows of a group's last block are
 // zeros in every lane, so no lane leaves before the reductions.
 //
-// Bound by the vector unit, about 12 instructions an element, six of them the
-// correctly rounded quotient, and close behind by HBM: 16,384 x 7168 rows held as
-// codes take 61 us (235 MB, 3.9 TB/s), 16,384 x 2048 bf16 with both forms 35 us.
+// 16,384 x 7168 rows held as codes take 70 us between the other launches of a
+// backward pass (235 MB, 3.4 TB/s; 56 us again and again on operands that the
+// last-level cache holds), 16,384 x 2048 bf16 with both forms 37 us.  Neither bound
+// is near: the vector instructions, about 16 an element (both forms: 26), six of
+// them a correctly rounded quotient, fill 64% (50%) of the cycles, the bytes at a
+// plain stream's 6.5 TB/s half of the time; a workgroup's loads, reductions and
+// stores come one after the other.  2048 rows of 8192 or of 2048: 13 us either way.
 #include "lpc_ops.hpp"
 
 namespace lpc {

@@ -181,8 +181,10 @@ __device__ __forceinline__ Work find_work(const GemmArgs& a, uint32_t tq, uint32
 // split: 16 QF x 16 PF outputs per workgroup, its 8 wavefronts take every
 // eighth block and their sums are joined through LDS, in the wavefronts' order.
 // Operands go straight to registers.  For up to 16 rows, where the weight is all
-// there is to read: 1 x 8192 x 8192 takes 11.8 us, 5.7 TB/s.  Loads further ahead
-// of their use, 2 to 4 blocks, took longer (15.7): 16 wavefronts a CU cover it.
+// there is to read: 1 x 8192 x 8192 takes 15.0 us from HBM (4.5 TB/s; a plain
+// stream of 64 MiB reaches 6.5) and 11.8 where the last-level cache still holds
+// the weight.  Loads further ahead of their use, 2 to 4 blocks, took longer (from
+// that cache 15.7): 16 wavefronts a CU cover it.
 // ---------------------------------------------------------------------------
 
 constexpr int kSplitWaves = 8;
@@ -317,7 +319,8 @@ __device__ __forceinline__ i32x8_t read_fragment(const uint8_t* r, uint32_t lo) 
 // costs about 4 cycles for every line it touches: 8 lines where lanes run along
 // the rows, as here, 16 where a wavefront gathers a fragment and 64 for a column
 // of scales, which is why the scales of 64 blocks are brought in first, along
-// their rows.  32 x 8192 x 8192: 13 us (5 TB/s) against 20 with gathered fragments.
+// their rows.  32 x 8192 x 8192: 15.6 us from HBM (4.3 TB/s), 13.2 with the weight
+// in the last-level cache, where gathered fragments took 20.
 // ---------------------------------------------------------------------------
 
 constexpr int kNarrowWaves = 4;
@@ -465,14 +468,22 @@ hipError_t launch_narrow(const GemmArgs& a, uint32_t tiles_q, hipStream_t stream
 //   Phases == 1, three stages  everything from slot 2 c - 4 (- 3) to 2 c
 // In both a wavefront waits until only one block's worth of loads is on its way.
 //
-// Measured, and what bounds it: 16,384 x 7168 x 4096 to bf16 runs at 2.3 PFLOP/s
-// (2.0 over 8 uneven groups), 4096 x 8192 x 4096 to fp32 at 1.2, weight gradients
-// of 8 groups at 0.95; a library product with one scale reaches 2.86 on these
-// sizes in FP8 and 1.42 in fp16.  The matrix cores are busy for 58% of the cycles
-// (fp32: 52%), and the card's power holds the clock at 1.95 GHz: the same kernel
-// on codes that are all zero runs at 2.9.  A loop of matrix instructions and
-// scalings alone, on random codes in registers, gives 3.5 (fp16: 1.95).  Loads
-// one block later cost a fifth, bank conflicts of a simpler layout as much.
+// Measured, and what bounds it (PFLOP/s): 16,384 x 7168 x 4096 to bf16 runs at 2.4,
+// over 8 groups at 2.2 (equal rows) and 1.9 to 2.1 (Zipf-distributed rows), 4096 x
+// 8192 x 4096 to fp32 at 1.2; 16,384 rows of 2048 over 8 such groups to 7168 outputs
+// at 1.9, the weight gradients of 7168 x 2048 of these at 0.98.  A library product
+// with one scale reaches 2.85 to 2.99 in FP8 and 1.45 to 1.50 in fp16.
+//   bf16   the card's power: the matrix cores are busy for 61% of the cycles (52%
+//          over 8 groups) at a clock that falls to 1.7 to 1.85 GHz; on codes that
+//          are all zero the same kernel runs at 3.15.
+//   short contractions (2048: 16 blocks)  filling, draining and stores: busy 44%
+//          at 2.1 GHz, where power is no limit.
+//   fp32   the vector unit: 3.3 vector instructions beside each matrix instruction,
+//          in weight gradients 4.5, mostly widening that two to four wavefronts
+//          repeat; busy 52% and 43% at 2.1 GHz.
+// A loop of matrix instructions and scalings alone, on random codes in registers,
+// gives 3.5 (fp16: 1.95).  Loads one block later cost a fifth, bank conflicts of a
+// simpler layout as much.
 // Neither one stream per wavefront with everything between its matrix
 // instructions, nor fragments read two rows ahead, nor wavefront priorities, nor
 // 16-byte loads of scales changed the time by more than 2%, and workgroups that
@@ -481,7 +492,8 @@ hipError_t launch_narrow(const GemmArgs& a, uint32_t tiles_q, hipStream_t stream
 
 constexpr int kTiledWaves = 8;
 // Tiles along q that neighbouring workgroups share P with: an XCD's 32 CUs then work on about 6 x 5 tiles, whose
-// operands its L2 serves.  16,384 x 7168 x 4096 over 8 groups took 440 us with 6, 443 with 8 and 466 with 2 or 4.
+// operands its L2 serves.  16,384 x 7168 x 4096 over 8 groups of Zipf-distributed rows took 454 us with 6, 453 with 8 and
+// 471 with 2 or 4 (equal rows 424, 419, 425 and 435).
 constexpr uint32_t kBand = 6;
 
 // Ends a slot: this wavefront's reads of LDS are done, and no instruction moves across.
@@ -753,8 +765,8 @@ __device__ __forceinline__ uint2 in_bands(uint32_t t, uint32_t tiles_q, uint32_t
 
 // A workgroup has a CU to itself, and each XCD works through its own run of tiles, 32 at a time.  Where a last round
 // would leave half of the CUs or more without a tile, its tiles are split into parts of 128 x 128, which take about a
-// third of a tile's time.  Product 16,384 x 7168 x 4096 over 8 groups, 136 tiles an XCD: 487 us against 524; 512 x
-// 8192 x 8192, 8 tiles an XCD: 44 us against 89.  How many tiles the counts make is known here and not on the host.
+// third of a tile's time.  Product 16,384 x 7168 x 4096 over 8 groups of Zipf-distributed rows: 454 us against 482; 512 x
+// 8192 x 8192, 8 tiles an XCD: 52 us against 99.  How many tiles the counts make is known here and not on the host.
 constexpr uint32_t kXcds = 8, kXcdCus = 32, kMostSplit = kXcdCus / 2;
 
 template <typename Out>
@@ -843,13 +855,19 @@ uint32_t most_tiles(const GemmArgs& a, uint32_t T) {
 // Offsets within a tile of up to 256 rows are held in 32 bits.
 bool tiled_offsets(const GemmArgs& a) { return a.ld < (1ull << 23); }
 
-// By the number of workgroups, one to a CU and 256 CUs (times in us of 64 x 64, 64 x 32 and 32 x 32 outputs and of
-// large tiles):
-//   up to 16 rows            gathered fragments: 1 x 8192 x 8192 12
-//   more than 384 of 64 x 64 large tiles: 256 x 8192 x 8192 46 / 50 / - / 40
-//   more than 128            64 x 64: 128 x 8192 x 8192 24 / 27 / - / 39, 777 x 1152 x 1000 8.2 / 9.1 / - / 9.2
-//   more than 128 of 64 x 32 64 x 32: 64 x 8192 x 8192 20 / 14 / - / 38
-//   otherwise                32 x 32: 32 x 8192 x 8192 - / - / 13 / 38
+// By the number of workgroups, one to a CU and 256 CUs.  Times in us with the weight in HBM: gathered / 32 x 32 / 64 x 32
+// / 64 x 64 outputs / large tiles, of dense products of 8192 x 8192 weights:
+//   up to 16 rows            gathered: 1 row 15.4 / 15.1 / 15.8 / 20.3 / 41 (16 rows 22.5 / 15.3 / 15.9 / 20.7 / 41)
+//   more than 384 of 64 x 64 large tiles: 256 rows 283 / 94 / 61 / 47 / 53 (4096 rows over 8 groups of the experts
+//                            below 1010 / 327 / 206 / 174 / 79)
+//   more than 128            64 x 64: 128 rows 142 / 49 / 34 / 27 / 55, 777 x 1152 x 1000 17 / 15 / 11 / 8.2 / 14.5
+//   more than 128 of 64 x 32 64 x 32: 64 rows 73 / 28 / 20 / 26 / 44
+//   otherwise                32 x 32: 32 rows 38 / 16 / 17 / 22 / 42
+// At 16 and at 256 rows another form takes less than the one chosen.  So it is with few rows over many groups, whose empty
+// tiles the bound counts: experts of 7168 x 2048, rows spread evenly at random,
+//   32 rows over 8 groups    30 / 29 / 34 / 35 / 35       256 rows  92 / 41 / 35 / 36 / 37
+//   32 rows over 64          149 / 154 / 198 / 152 / 91   256 rows  216 / 191 / 218 / 183 / 190
+//   32 rows over 256         527 / 647 / 811 / 563 / 129  256 rows  633 / 762 / 923 / 642 / 507
 // Rows of 8 MiB and more, whose offsets within a tile do not fit 32 bits, are gathered.
 template <typename Out>
 hipError_t launch_product(const GemmArgs& a, hipStream_t stream) {
@@ -877,9 +895,9 @@ hipError_t launch_wgrad(const uint8_t* yt, const float* ys, size_t n, const uint
                         hipStream_t stream) {
     const GemmArgs a{yt, xt, ys, xs, counts, dw, (uint32_t)groups, (uint32_t)rows, (uint32_t)n, (uint32_t)k, padded};
     // By the number of workgroups, one to a CU (times in us of 64 x 64, 128 x 128 and 256 x 128 outputs):
-    //   up to 256 of 64 x 64     gathered: 2048 x 1024 x 1024 14.5 / 21 / 32
-    //   up to 128 of 256 x 128   2048 x 2048 x 2048 51 / 23 / 33
-    //   more                     2048 x 4096 x 2048 99 / 44 / 37
+    //   up to 256 of 64 x 64     gathered: 2048 x 1024 x 1024 14.9 / 21.5 / 30.7
+    //   up to 128 of 256 x 128   2048 x 2048 x 2048 52.5 / 24.3 / 32.1
+    //   more                     2048 x 4096 x 2048 101 / 45 / 37.4
     const uint64_t g = (uint64_t)groups, small = ((n + 63) / 64) * ((k + 63) / 64) * g;
     if (small > 256 && tiled_offsets(a))
         return wgrad_tiles<Large<float>>(a) * g <= 128 ? launch_tiled_wgrad<Small>(a, (uint32_t)groups, stream)

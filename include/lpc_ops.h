@@ -15,8 +15,9 @@
  * enqueued (dtype LPC_ERR_DTYPE, then nothing to do LPC_OK, null pointers
  * LPC_ERR_NULL, alignment LPC_ERR_ALIGN, shape LPC_ERR_SHAPE; 16-byte alignment
  * of every pointer but a mask's, any, and those to row counts and to single
- * numbers (loss, dloss, grad_scale), 4 bytes), a refused launch is LPC_ERR_HIP.  Values that a call reads
- * from device memory (row counts, expert indices) are checked by the kernels:
+ * numbers (loss, dloss, grad_scale), 4 bytes), a refused launch, one of 2^32
+ * lanes or more among them, is LPC_ERR_HIP.  Values that a call reads from
+ * device memory (row counts, expert indices) are checked by the kernels:
  * one out of range reads and writes nothing out of bounds.  Outputs must not
  * overlap inputs unless a call says otherwise.  Every result is the same from
  * call to call: no sum depends on the order in which workgroups run.
@@ -140,7 +141,8 @@ size_t lpc_router_workspace_bytes(size_t rows, int experts);
  *   loss[0]   sum over e of coef * E * load[e] * counts[e] / (max(valid, 1) * topk)
  * A logit of -infinity (or NaN) is an expert the row may not use: p = 0, never
  * chosen.  A row that is not valid chooses nothing and counts nowhere.  Slots
- * left without an expert have index -1 and gate 0.
+ * left without an expert have index -1 and gate 0.  exp is good to 2 units in
+ * the last place; a p below 2^-125 is zero or denormal.
  *   logits [rows, experts] of type `in`; mask [rows] uint8 or NULL (keep all)
  *   out_experts [rows, topk] int32, gates [rows, topk]
  *   counts [experts] int32, load [experts], slope [experts], loss [1]
