@@ -1,0 +1,305 @@
+// lpc_muon.hip -- one step of the matrix optimizer over every matrix of a plan.
+//
+//   m = beta m + (1 - beta) g,  u = (1 - beta) g + beta m  (or m),  X = u / |u|
+//   iterations times:  A = X X^T,  B = b A + c A A,  X = a X + B X
+//   param = param (1 - lr wd) - lr scale X
+// Each iteration takes every singular value s of X to a s + b s^3 + c s^5, which draws them to about 1; X X^T is formed on the
+// shorter side (for a tall matrix X^T X, and X B).  All three products are matrix instructions on fp16 with FP32 sums.
+//
+// Precision.  X is held as fp16 high and low halves of together 22 bits: products take the high half, the term a X both.
+// Directions of small singular values live on that term alone (B is small there), so that they keep their precision: over
+// spectra of all kinds the update is off by 4e-4 to 2e-3 of itself (2-norm).  With the high half alone it was off by 4e-2
+// where a few strong directions hide the rest, and bf16 in its place gave 3e-1.  fp16 rather than bf16 as matrices
+// stay within known bounds: X, A and B are held times 2^10, which keeps elements of 2^-24 and up normal and the largest
+// (singular values stay below 1.3, A's below 1.7, B's below 3) far below 65504.
+#include "lpc_tile.hpp"
+
+namespace lpc {
+namespace {
+
+constexpr float kHeld = 1024.0f, kLow = 2048.0f;  // what X, A and B are held times; and what a low half is held times besides
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+
+// one matrix's parts of the workspace; all start at multiples of 128 bytes and their rows' ends are zeros
+struct Space {
+    _Float16 *high[2], *low, *a, *b;
+    double* partial;
+};
+
+__device__ __forceinline__ Space space_of(const MuonMatrix& m, uint8_t* w) {
+    w += m.space;
+    const size_t x = (size_t)m.rows * m.ldx * 2, s = (size_t)min(m.rows, m.cols) * m.lda * 2;
+    _Float16* h = reinterpret_cast<_Float16*>(w);
+    return {{h, reinterpret_cast<_Float16*>(w + x)}, reinterpret_cast<_Float16*>(w + 2 * x), reinterpret_cast<_Float16*>(w + 3 * x),
+            reinterpret_cast<_Float16*>(w + 3 * x + s), reinterpret_cast<double*>(w + 3 * x + 2 * s)};
+}
+
+// ---------------------------------------------------------------------------
+// momentum and the update's norm
+// ---------------------------------------------------------------------------
+
+constexpr uint32_t kChunkLanes = 256;
+
+typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x4u_t __attribute__((ext_vector_type(4), aligned(2)));
+
+// four elements from i on, fewer at a matrix's end (0 for the others); matrices of a tensor start at any element
+__device__ __forceinline__ f32x4_t load4(const float* p, size_t i, size_t n) {
+    if (i + 4 <= n) return *reinterpret_cast<const f32x4u_t*>(p + i);
+    f32x4_t v = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = i + e < n ? p[i + e] : 0.0f;
+    return v;
+}
+__device__ __forceinline__ f32x4_t load4(const uint16_t* p, size_t i, size_t n) {
+    f32x4_t v = {};
+    if (i + 4 <= n) {
+        const u16x4u_t h = *reinterpret_cast<const u16x4u_t*>(p + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = bf16lo(h[e]);
+        return v;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = i + e < n ? bf16lo(p[i + e]) : 0.0f;
+    return v;
+}
+
+__device__ __forceinline__ f32x4_t update_of(f32x4_t m, f32x4_t g, const MuonScalars& s) {
+    return s.nesterov ? g * s.rest + m * s.beta : m;
+}
+
+// Sum over a workgroup, in a fixed order.
+__device__ __forceinline__ double workgroup_sum(double v, double* lds) {
+#pragma unroll
+    for (int d = 32; d; d /= 2) v += __shfl_xor(v, d);
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double all = 0.0;
+    for (uint32_t w = 0; w < kChunkLanes / 64; ++w) all += lds[w];
+    return all;
+}
+
+// The sum of squares is held in 64 bits: an fp32 square has no range to spare, and nothing here is bound by arithmetic.
+template <typename Grad>
+__global__ __launch_bounds__(kChunkLanes) void muon_momentum_kernel(MuonPlan plan, uint8_t* space, const float* grad_scale, MuonScalars s) {
+    __shared__ double lds[kChunkLanes / 64];
+    const MuonPiece piece = plan.chunks[blockIdx.x];
+    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const size_t n = (size_t)x.rows * x.cols;
+    const Grad* grad = static_cast<const Grad*>(x.grad);
+    const float scale = grad_scale ? grad_scale[0] : 1.0f;
+    double sum = 0.0;
+    for (size_t i = (size_t)piece.index * kMuonChunk + threadIdx.x * 4; i < min(n, ((size_t)piece.index + 1) * kMuonChunk); i += kChunkLanes * 4) {
+        const f32x4_t g = load4(grad, i, n) * scale;
+        const f32x4_t m = load4(x.m, i, n) * s.beta + g * s.rest;
+        if (i + 4 <= n) {
+            *reinterpret_cast<f32x4u_t*>(x.m + i) = m;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < n) x.m[i + e] = m[e];
+        }
+        const f32x4_t u = update_of(m, g, s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += (double)u[e] * (double)u[e];
+    }
+    const double all = workgroup_sum(sum, lds);
+    if (threadIdx.x == 0) space_of(x, space).partial[piece.index] = all;
+}
+
+// X over its norm, in halves
+template <typename Grad>
+__global__ __launch_bounds__(kChunkLanes) void muon_start_kernel(MuonPlan plan, uint8_t* space, const float* grad_scale, MuonScalars s) {
+    __shared__ double lds[kChunkLanes / 64];
+    const MuonPiece piece = plan.chunks[blockIdx.x];
+    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const Space w = space_of(x, space);
+    const size_t n = (size_t)x.rows * x.cols;
+    const uint32_t chunks = (uint32_t)((n + kMuonChunk - 1) / kMuonChunk);
+    double sum = 0.0;
+    for (uint32_t c = threadIdx.x; c < chunks; c += kChunkLanes) sum += w.partial[c];
+    const double norm = sqrt(workgroup_sum(sum, lds)), by = norm > 0.0 ? (double)kHeld / norm : 0.0;
+    const Grad* grad = static_cast<const Grad*>(x.grad);
+    const float scale = grad_scale ? grad_scale[0] : 1.0f;
+    for (size_t i = (size_t)piece.index * kMuonChunk + threadIdx.x * 4; i < min(n, ((size_t)piece.index + 1) * kMuonChunk); i += kChunkLanes * 4) {
+        const f32x4_t u = update_of(load4(x.m, i, n), load4(grad, i, n) * scale, s);
+        uint32_t row = (uint32_t)(i / x.cols), col = (uint32_t)(i - (size_t)row * x.cols);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (i + e >= n) break;
+            const float v = (float)((double)u[e] * by);
+            const _Float16 high = (_Float16)v;
+            const size_t at = (size_t)row * x.ldx + col;
+            w.high[0][at] = high;
+            w.low[at] = (_Float16)((v - (float)high) * kLow);
+            if (++col == x.cols) {
+                for (size_t z = at + 1; col < x.ldx; ++col, ++z) w.high[0][z] = w.low[z] = (_Float16)0.0f;
+                col = 0;
+                ++row;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+
+using Tile = SmallOf<false>;
+static_assert(Tile::BQ == kMuonTile && Tile::BP == kMuonTile, "tiles as planned");
+
+__device__ __forceinline__ Operand operand(const _Float16* first, uint32_t ld, uint32_t n) {
+    return {reinterpret_cast<const uint8_t*>(first), (size_t)ld * 2, n, nullptr};
+}
+
+// the contraction's slabs; rows along are zeros from `length` to a multiple of 64
+__device__ __forceinline__ uint32_t slabs_of(uint32_t length, Tail* t) {
+    const uint32_t slabs = (length + kSlabRows - 1) / kSlabRows, last = length - (slabs - 1) * kSlabRows;
+    *t = Tail{2 * last, last};
+    return slabs;
+}
+
+// where a lane's four neighbouring elements (i, j) of a tile's sums are: row and first column within the tile
+struct Place {
+    uint32_t q, p;
+};
+template <typename S>
+__device__ __forceinline__ Place place_of(int i, int j) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    return {wave % S::WavesQ * S::QW + 16 * i + (lane & 15), wave / S::WavesQ * S::PW + 16 * j + 4 * (lane >> 4)};
+}
+
+template <typename F>
+__device__ __forceinline__ void each_place(f32x4_t (&acc)[Tile::Phases * Tile::F][Tile::PF], F f) {
+#pragma unroll
+    for (int i = 0; i < Tile::Phases * Tile::F; ++i)
+#pragma unroll
+        for (int j = 0; j < Tile::PF; ++j) {
+            const Place at = place_of<Tile>(i, j);
+            f(acc[i][j], at.q, at.p);
+        }
+}
+
+__device__ __forceinline__ f32x4_t halves(const _Float16* p) { return __builtin_convertvector(*reinterpret_cast<const f16x4_t*>(p), f32x4_t); }
+
+// A = X X^T (Second: B = b A + c A A), 128 x 128 of it
+template <bool Second>
+__global__ __launch_bounds__(kTileWaves * 64, 2) void muon_square_kernel(MuonPlan plan, uint8_t* space, uint32_t from) {
+    __shared__ __attribute__((aligned(128))) uint8_t lds[Tile::kBytes];
+    const MuonPiece piece = plan.squares[xcd_tile()];
+    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const Space w = space_of(x, space);
+    const bool tall = x.rows > x.cols;
+    const uint32_t s = min(x.rows, x.cols), tiles = (s + Tile::BP - 1) / Tile::BP;
+    const uint32_t q0 = piece.index / tiles * Tile::BQ, p0 = piece.index % tiles * Tile::BP;
+    const uint32_t nq = min(Tile::BQ, s - q0), np = min(Tile::BP, s - p0);
+    Tail t;
+    f32x4_t acc[Tile::Phases * Tile::F][Tile::PF];
+    if (Second) {
+        const uint32_t slabs = slabs_of(s, &t);
+        tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(w.a + (size_t)q0 * x.lda, x.lda, nq), operand(w.a + (size_t)p0 * x.lda, x.lda, np),
+                                                slabs, t, lds, acc);
+    } else if (tall) {
+        // columns up to ldx hold zeros, so that pieces of 8 are whole
+        const uint32_t slabs = slabs_of(x.rows, &t);
+        tile_sums<MmaF16, kAcross, kAcross, Tile>(operand(w.high[from] + q0, x.ldx, min(Tile::BQ, x.ldx - q0)),
+                                                  operand(w.high[from] + p0, x.ldx, min(Tile::BP, x.ldx - p0)), slabs, t, lds, acc);
+    } else {
+        const uint32_t slabs = slabs_of(x.cols, &t);
+        tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(w.high[from] + (size_t)q0 * x.ldx, x.ldx, nq),
+                                                operand(w.high[from] + (size_t)p0 * x.ldx, x.ldx, np), slabs, t, lds, acc);
+    }
+    each_place(acc, [&](f32x4_t& v, uint32_t q, uint32_t p) {
+        v = v * (1.0f / kHeld);
+        if (Second) v = v * kC + (q < nq && p < np ? halves(w.a + (size_t)(q0 + q) * x.lda + p0 + p) : f32x4_t{}) * kB;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (p + e >= np) v[e] = 0.0f;
+    });
+    store_tile<_Float16, Tile>(acc, (Second ? w.b : w.a) + (size_t)q0 * x.lda + p0, x.lda, nq, min(Tile::BP, x.lda - p0), lds);
+}
+
+// X = a X + B X (tall: X B), 128 x 128 of it; Last: the parameters with it
+template <bool Last>
+__global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPlan plan, uint8_t* space, uint32_t from, MuonScalars s) {
+    __shared__ __attribute__((aligned(128))) uint8_t lds[Tile::kBytes];
+    const MuonPiece piece = plan.updates[xcd_tile()];
+    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const Space w = space_of(x, space);
+    const uint32_t tiles = (x.cols + Tile::BP - 1) / Tile::BP;
+    const uint32_t q0 = piece.index / tiles * Tile::BQ, p0 = piece.index % tiles * Tile::BP;
+    const uint32_t nq = min(Tile::BQ, x.rows - q0), np = min(Tile::BP, x.cols - p0);
+    const _Float16* high = w.high[from];
+    Tail t;
+    f32x4_t acc[Tile::Phases * Tile::F][Tile::PF];
+    if (x.rows > x.cols) {
+        const uint32_t slabs = slabs_of(x.cols, &t);
+        tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(high + (size_t)q0 * x.ldx, x.ldx, nq), operand(w.b + (size_t)p0 * x.lda, x.lda, np), slabs,
+                                                t, lds, acc);
+    } else {
+        const uint32_t slabs = slabs_of(x.rows, &t);
+        tile_sums<MmaF16, kAlong, kAcross, Tile>(operand(w.b + (size_t)q0 * x.lda, x.lda, nq),
+                                                 operand(high + p0, x.ldx, min(Tile::BP, x.ldx - p0)), slabs, t, lds, acc);
+    }
+    each_place(acc, [&](f32x4_t& v, uint32_t q, uint32_t p) {
+        if (q >= nq || p >= np) {
+            v = f32x4_t{};
+            return;
+        }
+        const size_t at = (size_t)(q0 + q) * x.ldx + p0 + p;
+        v = v * (1.0f / kHeld) + (halves(high + at) + halves(w.low + at) * (1.0f / kLow)) * kA;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (p + e >= np) v[e] = 0.0f;
+        if (Last) {
+            const size_t out = (size_t)(q0 + q) * x.cols + p0 + p;
+            const float rate = s.lr * x.scale * (1.0f / kHeld);
+            if (p + 4 <= np) {
+                const f32x4_t now = *reinterpret_cast<const f32x4u_t*>(x.param + out) * s.keep - v * rate;
+                *reinterpret_cast<f32x4u_t*>(x.param + out) = now;
+                if (x.copy) {
+                    const u32x2_t c = {pack_bf16x2(now[0], now[1]), pack_bf16x2(now[2], now[3])};
+                    *reinterpret_cast<u16x4u_t*>(x.copy + out) = __builtin_bit_cast(u16x4u_t, c);
+                }
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e) {
+                    if (p + e >= np) break;
+                    const float now = x.param[out + e] * s.keep - v[e] * rate;
+                    x.param[out + e] = now;
+                    if (x.copy) x.copy[out + e] = (uint16_t)pack_bf16x2(now, now);
+                }
+            }
+        }
+    });
+    if (Last) return;
+    const uint32_t wide = min(Tile::BP, x.ldx - p0);
+    const size_t at = (size_t)q0 * x.ldx + p0;
+    store_tile<_Float16, Tile>(acc, w.high[1 - from] + at, x.ldx, nq, wide, lds);
+    each_place(acc, [&](f32x4_t& v, uint32_t, uint32_t) { v = (v - __builtin_convertvector(__builtin_convertvector(v, f16x4_t), f32x4_t)) * kLow; });
+    store_tile<_Float16, Tile>(acc, w.low + at, x.ldx, nq, wide, lds);
+}
+
+}  // namespace
+
+hipError_t launch_muon(const MuonPlan& plan, const MuonCounts& n, int grad_bf16, int iterations, const MuonScalars& s, const float* grad_scale,
+                       void* space, hipStream_t stream) {
+    uint8_t* w = static_cast<uint8_t*>(space);
+    const dim3 lanes(kTileWaves * 64), few(kChunkLanes);
+    hipError_t e = grad_bf16 ? enqueue(muon_momentum_kernel<uint16_t>, dim3(n.chunks), few, stream, plan, w, grad_scale, s)
+                             : enqueue(muon_momentum_kernel<float>, dim3(n.chunks), few, stream, plan, w, grad_scale, s);
+    if (e == hipSuccess)
+        e = grad_bf16 ? enqueue(muon_start_kernel<uint16_t>, dim3(n.chunks), few, stream, plan, w, grad_scale, s)
+                      : enqueue(muon_start_kernel<float>, dim3(n.chunks), few, stream, plan, w, grad_scale, s);
+    for (int i = 0; i < iterations && e == hipSuccess; ++i) {
+        const uint32_t from = i & 1;
+        e = enqueue(muon_square_kernel<false>, dim3(n.squares), lanes, stream, plan, w, from);
+        if (e == hipSuccess) e = enqueue(muon_square_kernel<true>, dim3(n.squares), lanes, stream, plan, w, from);
+        if (e == hipSuccess)
+            e = i + 1 < iterations ? enqueue(muon_update_kernel<false>, dim3(n.updates), lanes, stream, plan, w, from, s)
+                                   : enqueue(muon_update_kernel<true>, dim3(n.updates), lanes, stream, plan, w, from, s);
+    }
+    return e;
+}
+
+}  // namespace lpc

@@ -185,4 +185,53 @@ struct AdamwScalars {
 hipError_t launch_adamw(const void* plan, size_t chunks, int grad_bf16, int state_bits, const AdamwScalars& s,
                         const float* grad_scale, hipStream_t stream);
 
+hipError_t launch_gemm16(const uint16_t* x, size_t rows, size_t k, const uint16_t* w, size_t n, int groups,
+                         const int32_t* counts, void* out, int out_bf16, hipStream_t stream);
+hipError_t launch_gemm16_dgrad(const uint16_t* dy, size_t rows, size_t n, const uint16_t* w, size_t k, int groups,
+                               const int32_t* counts, void* dx, int out_bf16, hipStream_t stream);
+hipError_t launch_gemm16_wgrad(const uint16_t* dy, size_t n, const uint16_t* x, size_t k, size_t rows, int groups,
+                               const int32_t* counts, void* dw, int out_bf16, hipStream_t stream);
+
+hipError_t launch_mx_quantize(const void* x, int in_bf16, size_t n, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, size_t n, void* out, int out_bf16,
+                                hipStream_t stream);
+hipError_t launch_gemm_mxfp4(const uint8_t* x, const uint8_t* xs, size_t rows, size_t k, const uint8_t* w,
+                             const uint8_t* ws, size_t n, int groups, const int32_t* counts, void* out, int out_bf16,
+                             hipStream_t stream);
+
+// elements of a matrix that one workgroup of the matrix optimizer's elementwise kernels takes
+constexpr size_t kMuonChunk = 16384;
+constexpr size_t kMuonTile = 128;  // outputs along a side of a tile of its products
+
+// A plan is the matrices, then the pieces of each kind of launch: which matrix, and the piece's number within it (chunks of
+// its elements, tiles of its square products, tiles of the matrix).
+struct MuonMatrix {
+    float* param;
+    const void* grad;
+    float* m;
+    uint16_t* copy;
+    uint64_t space;  // bytes from the workspace's start
+    uint32_t rows, cols;
+    uint32_t ldx, lda;  // elements between rows of X, and of A and B
+    float scale;
+    uint32_t unused;
+};
+static_assert(sizeof(MuonMatrix) % 16 == 0, "pieces start aligned");
+struct MuonPiece {
+    uint32_t matrix, index;
+};
+struct MuonPlan {
+    const MuonMatrix* matrices;
+    const MuonPiece *chunks, *squares, *updates;
+};
+struct MuonCounts {
+    uint32_t chunks, squares, updates;
+};
+struct MuonScalars {
+    float beta, rest, keep, lr;
+    int nesterov;
+};
+hipError_t launch_muon(const MuonPlan& plan, const MuonCounts& n, int grad_bf16, int iterations, const MuonScalars& s,
+                       const float* grad_scale, void* space, hipStream_t stream);
+
 }  // namespace lpc

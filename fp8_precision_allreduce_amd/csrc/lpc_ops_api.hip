@@ -62,6 +62,50 @@ size_t plan_size(size_t chunks, size_t tensors) {
     return lpc::adamw_chunk_bytes(chunks) + tensors * sizeof(lpc_adamw_tensor);
 }
 
+// groups x rows of a grouped product with one weight [n, k] per group
+bool bad_product(size_t rows, size_t n, size_t k, int groups) {
+    return bad_groups(groups) || too_many(rows, k) || too_many(n, k) || too_many(rows, n) || n * k > LPC_MAX_MATRIX / (size_t)groups;
+}
+
+// pieces of a matrix optimizer's plan, of each kind
+constexpr size_t kMaxPieces = (size_t)1 << 24;
+constexpr size_t kMuonPad = 64;  // elements that rows of its workspace are padded to
+
+size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+
+struct MuonSizes {
+    size_t chunks, squares, updates, space;  // of one matrix
+};
+
+MuonSizes muon_sizes(size_t rows, size_t cols) {
+    const size_t s = rows < cols ? rows : cols, side = (s + lpc::kMuonTile - 1) / lpc::kMuonTile;
+    const size_t chunks = (rows * cols + lpc::kMuonChunk - 1) / lpc::kMuonChunk;
+    const size_t tiles = ((rows + lpc::kMuonTile - 1) / lpc::kMuonTile) * ((cols + lpc::kMuonTile - 1) / lpc::kMuonTile);
+    const size_t bytes = 6 * rows * up(cols, kMuonPad) + 4 * s * up(s, kMuonPad) + 8 * chunks;
+    return {chunks, side * side, tiles, up(bytes, 128)};
+}
+
+// false: refused
+bool muon_work(const lpc_muon_tensor* t, int count, lpc_muon_work* w) {
+    *w = lpc_muon_work{};
+    for (int i = 0; i < count; ++i) {
+        if (t[i].batch == 0 || t[i].rows == 0 || t[i].cols == 0) continue;
+        if (t[i].rows > LPC_MUON_MAX_SIDE || t[i].cols > LPC_MUON_MAX_SIDE || t[i].batch > kMaxPieces) return false;
+        const MuonSizes m = muon_sizes(t[i].rows, t[i].cols);
+        w->matrices += t[i].batch;
+        w->chunks += t[i].batch * m.chunks;
+        w->squares += t[i].batch * m.squares;
+        w->updates += t[i].batch * m.updates;
+        w->workspace_bytes += t[i].batch * m.space;  // below 2^24 pieces of 2^23 bytes
+        if (w->chunks > kMaxPieces || w->squares > kMaxPieces || w->updates > kMaxPieces) return false;
+    }
+    return true;
+}
+
+size_t muon_plan_size(const lpc_muon_work& w) {
+    return w.matrices * sizeof(lpc::MuonMatrix) + up((w.chunks + w.squares + w.updates) * sizeof(lpc::MuonPiece), 16);
+}
+
 }  // namespace
 
 extern "C" {
@@ -226,6 +270,155 @@ lpc_status lpc_adamw_step(const void* plan, size_t chunks, lpc_dtype grad_t, int
     s.root = (float)(1.0 / sqrt(1.0 - pow(beta2, (double)step)));
     s.eps = (float)eps;
     return hip_status(lpc::launch_adamw(plan, chunks, grad_t == LPC_BF16, state_bits, s, grad_scale, stream));
+}
+
+lpc_status lpc_gemm_bf16(const uint16_t* x, size_t rows, size_t k, const uint16_t* w, size_t n, int groups,
+                         const int32_t* counts, void* out, lpc_dtype out_t, hipStream_t stream) {
+    if (bad_dtype(out_t)) return LPC_ERR_DTYPE;
+    if (rows == 0 || n == 0) return LPC_OK;
+    if (any_null(x, w) || !out || missing_counts(groups, counts)) return LPC_ERR_NULL;
+    if (any_misaligned(x, w, out) || misaligned4(counts)) return LPC_ERR_ALIGN;
+    if (k == 0 || k % 8 || bad_product(rows, n, k, groups)) return LPC_ERR_SHAPE;
+    return hip_status(lpc::launch_gemm16(x, rows, k, w, n, groups, counts, out, out_t == LPC_BF16, stream));
+}
+
+lpc_status lpc_gemm_bf16_dgrad(const uint16_t* dy, size_t rows, size_t n, const uint16_t* w, size_t k, int groups,
+                               const int32_t* counts, void* dx, lpc_dtype out_t, hipStream_t stream) {
+    if (bad_dtype(out_t)) return LPC_ERR_DTYPE;
+    if (rows == 0 || k == 0) return LPC_OK;
+    if (any_null(dy, w) || !dx || missing_counts(groups, counts)) return LPC_ERR_NULL;
+    if (any_misaligned(dy, w, dx) || misaligned4(counts)) return LPC_ERR_ALIGN;
+    if (n == 0 || n % 8 || k % 8 || bad_product(rows, n, k, groups)) return LPC_ERR_SHAPE;
+    return hip_status(lpc::launch_gemm16_dgrad(dy, rows, n, w, k, groups, counts, dx, out_t == LPC_BF16, stream));
+}
+
+lpc_status lpc_gemm_bf16_wgrad(const uint16_t* dy, size_t n, const uint16_t* x, size_t k, size_t rows, int groups,
+                               const int32_t* counts, void* dw, lpc_dtype out_t, hipStream_t stream) {
+    if (bad_dtype(out_t)) return LPC_ERR_DTYPE;
+    if (n == 0 || k == 0) return LPC_OK;
+    if (!dw || missing_counts(groups, counts) || (rows != 0 && any_null(dy, x))) return LPC_ERR_NULL;
+    if (any_misaligned(dy, x, dw) || misaligned4(counts)) return LPC_ERR_ALIGN;
+    if (n % 8 || k % 8 || bad_product(rows, n, k, groups)) return LPC_ERR_SHAPE;
+    return hip_status(lpc::launch_gemm16_wgrad(dy, n, x, k, rows, groups, counts, dw, out_t == LPC_BF16, stream));
+}
+
+lpc_status lpc_quantize_mxfp4(const void* x, lpc_dtype in, size_t n, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+    if (bad_dtype(in)) return LPC_ERR_DTYPE;
+    if (n == 0) return LPC_OK;
+    if (!x || any_null(codes, scales)) return LPC_ERR_NULL;
+    if (any_misaligned(x, codes, scales)) return LPC_ERR_ALIGN;
+    if (n % 32 || n > LPC_MAX_MATRIX) return LPC_ERR_SHAPE;
+    return hip_status(lpc::launch_mx_quantize(x, in == LPC_BF16, n, codes, scales, stream));
+}
+
+lpc_status lpc_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, size_t n, void* out, lpc_dtype out_t,
+                                hipStream_t stream) {
+    if (bad_dtype(out_t)) return LPC_ERR_DTYPE;
+    if (n == 0) return LPC_OK;
+    if (any_null(codes, scales) || !out) return LPC_ERR_NULL;
+    if (any_misaligned(codes, scales, out)) return LPC_ERR_ALIGN;
+    if (n % 32 || n > LPC_MAX_MATRIX) return LPC_ERR_SHAPE;
+    return hip_status(lpc::launch_mx_dequantize(codes, scales, n, out, out_t == LPC_BF16, stream));
+}
+
+lpc_status lpc_gemm_mxfp4(const uint8_t* x, const uint8_t* xs, size_t rows, size_t k, const uint8_t* w, const uint8_t* ws, size_t n,
+                          int groups, const int32_t* counts, void* out, lpc_dtype out_t, hipStream_t stream) {
+    if (bad_dtype(out_t)) return LPC_ERR_DTYPE;
+    if (rows == 0 || n == 0) return LPC_OK;
+    if (any_null(x, xs, w, ws) || !out || missing_counts(groups, counts)) return LPC_ERR_NULL;
+    if (any_misaligned(x, xs, w, ws, out) || misaligned4(counts)) return LPC_ERR_ALIGN;
+    if (k == 0 || k % LPC_BLOCK || bad_product(rows, n, k, groups)) return LPC_ERR_SHAPE;
+    return hip_status(lpc::launch_gemm_mxfp4(x, xs, rows, k, w, ws, n, groups, counts, out, out_t == LPC_BF16, stream));
+}
+
+size_t lpc_muon_plan_bytes(const lpc_muon_tensor* tensors, int count) {
+    lpc_muon_work w;
+    if (!tensors || count < 1 || !muon_work(tensors, count, &w)) return 0;
+    return muon_plan_size(w);
+}
+
+lpc_status lpc_muon_plan(const lpc_muon_tensor* tensors, int count, lpc_dtype grad_t, void* plan, size_t plan_bytes,
+                         lpc_muon_work* work) {
+    if (bad_dtype(grad_t)) return LPC_ERR_DTYPE;
+    if (!work) return LPC_ERR_NULL;
+    *work = lpc_muon_work{};
+    if (count < 0) return LPC_ERR_SHAPE;
+    if (count == 0) return LPC_OK;
+    if (!tensors) return LPC_ERR_NULL;
+    const auto empty = [](const lpc_muon_tensor& t) { return t.batch == 0 || t.rows == 0 || t.cols == 0; };
+    for (int i = 0; i < count; ++i) {
+        const lpc_muon_tensor& t = tensors[i];
+        if (!empty(t) && (!t.param || !t.grad || !t.m)) return LPC_ERR_NULL;
+    }
+    for (int i = 0; i < count; ++i) {
+        const lpc_muon_tensor& t = tensors[i];
+        if (!empty(t) && any_misaligned(t.param, t.grad, t.m, t.copy)) return LPC_ERR_ALIGN;
+    }
+    lpc_muon_work w;
+    if (!muon_work(tensors, count, &w)) return LPC_ERR_SHAPE;
+    if (w.matrices == 0) return LPC_OK;
+    if (!plan) return LPC_ERR_NULL;
+    if (plan_bytes < muon_plan_size(w)) return LPC_ERR_SHAPE;
+    memset(plan, 0, muon_plan_size(w));
+    uint8_t* matrices = static_cast<uint8_t*>(plan);
+    uint8_t* pieces[3];  // chunks, squares, updates
+    pieces[0] = matrices + w.matrices * sizeof(lpc::MuonMatrix);
+    pieces[1] = pieces[0] + w.chunks * sizeof(lpc::MuonPiece);
+    pieces[2] = pieces[1] + w.squares * sizeof(lpc::MuonPiece);
+    uint32_t at = 0;
+    uint64_t space = 0;
+    for (int i = 0; i < count; ++i) {
+        const lpc_muon_tensor& t = tensors[i];
+        if (empty(t)) continue;
+        const MuonSizes sizes = muon_sizes(t.rows, t.cols);
+        const size_t counts[3] = {sizes.chunks, sizes.squares, sizes.updates}, n = t.rows * t.cols;
+        const size_t element = grad_t == LPC_BF16 ? 2 : 4;
+        for (size_t b = 0; b < t.batch; ++b, ++at) {
+            lpc::MuonMatrix m{};
+            m.param = t.param + b * n;
+            m.grad = static_cast<const uint8_t*>(t.grad) + b * n * element;
+            m.m = t.m + b * n;
+            m.copy = t.copy ? t.copy + b * n : nullptr;
+            m.space = space;
+            m.rows = (uint32_t)t.rows;
+            m.cols = (uint32_t)t.cols;
+            m.ldx = (uint32_t)up(t.cols, kMuonPad);
+            m.lda = (uint32_t)up(t.rows < t.cols ? t.rows : t.cols, kMuonPad);
+            m.scale = (float)t.scale;
+            memcpy(matrices + at * sizeof(m), &m, sizeof(m));
+            space += sizes.space;
+            for (int kind = 0; kind < 3; ++kind)
+                for (size_t j = 0; j < counts[kind]; ++j, pieces[kind] += sizeof(lpc::MuonPiece)) {
+                    const lpc::MuonPiece piece{at, (uint32_t)j};
+                    memcpy(pieces[kind], &piece, sizeof(piece));
+                }
+        }
+    }
+    *work = w;
+    return LPC_OK;
+}
+
+lpc_status lpc_muon_step(const void* plan, const lpc_muon_work* work, lpc_dtype grad_t, double lr, double beta, int nesterov,
+                         double weight_decay, int iterations, const float* grad_scale, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream) {
+    if (bad_dtype(grad_t)) return LPC_ERR_DTYPE;
+    if (!work) return LPC_ERR_NULL;
+    if (work->matrices == 0) return LPC_OK;
+    if (!plan || !workspace) return LPC_ERR_NULL;
+    if (misaligned(plan) || misaligned(workspace) || misaligned4(grad_scale)) return LPC_ERR_ALIGN;
+    if (work->matrices > kMaxPieces || work->chunks > kMaxPieces || work->squares > kMaxPieces || work->updates > kMaxPieces ||
+        workspace_bytes < work->workspace_bytes || !(beta >= 0.0 && beta < 1.0) || iterations < 1 ||
+        iterations > LPC_MUON_MAX_ITERATIONS)
+        return LPC_ERR_SHAPE;
+    const uint8_t* b = static_cast<const uint8_t*>(plan);
+    lpc::MuonPlan p;
+    p.matrices = reinterpret_cast<const lpc::MuonMatrix*>(b);
+    p.chunks = reinterpret_cast<const lpc::MuonPiece*>(b + work->matrices * sizeof(lpc::MuonMatrix));
+    p.squares = p.chunks + work->chunks;
+    p.updates = p.squares + work->squares;
+    const lpc::MuonCounts n{(uint32_t)work->chunks, (uint32_t)work->squares, (uint32_t)work->updates};
+    const lpc::MuonScalars s{(float)beta, (float)(1.0 - beta), (float)(1.0 - lr * weight_decay), (float)lr, nesterov != 0};
+    return hip_status(lpc::launch_muon(p, n, grad_t == LPC_BF16, iterations, s, grad_scale, workspace, stream));
 }
 
 }  // extern "C"

@@ -49,9 +49,19 @@ class _AdamwTensor(ctypes.Structure):
         ("n", ctypes.c_size_t)]
 
 
+class _MuonTensor(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("param", "grad", "m", "copy")] + [
+        (f, ctypes.c_size_t) for f in ("batch", "rows", "cols")] + [("scale", ctypes.c_double)]
+
+
+class _MuonWork(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_size_t) for f in ("matrices", "chunks", "squares", "updates", "workspace_bytes")]
+
+
 _vp, _sz, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _f32, _f64, _szp, _tp = ctypes.c_float, ctypes.c_double, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(_AdamwTensor)
 _pp = ctypes.POINTER(ctypes.c_void_p)
+_mp, _wp = ctypes.POINTER(_MuonTensor), ctypes.POINTER(_MuonWork)
 SIGNATURES = {
     "lpc_quantize_fp8": [_vp, _int, _sz, _vp, _vp, _vp],
     "lpc_reduce_scatter_chunk": [_pp, _pp, _int, _int, _sz, _vp, _vp, _vp],
@@ -81,12 +91,22 @@ SIGNATURES = {
     "lpc_adamw_plan_bytes": [_tp, _int],
     "lpc_adamw_plan": [_tp, _int, _int, _int, _vp, _sz, _szp],
     "lpc_adamw_step": [_vp, _sz, _int, _int, ctypes.c_int64, _f64, _f64, _f64, _f64, _f64, _vp, _vp],
+    "lpc_gemm_bf16": [_vp, _sz, _sz, _vp, _sz, _int, _vp, _vp, _int, _vp],
+    "lpc_gemm_bf16_dgrad": [_vp, _sz, _sz, _vp, _sz, _int, _vp, _vp, _int, _vp],
+    "lpc_gemm_bf16_wgrad": [_vp, _sz, _vp, _sz, _sz, _int, _vp, _vp, _int, _vp],
+    "lpc_quantize_mxfp4": [_vp, _int, _sz, _vp, _vp, _vp],
+    "lpc_dequantize_mxfp4": [_vp, _vp, _sz, _vp, _int, _vp],
+    "lpc_gemm_mxfp4": [_vp, _vp, _sz, _sz, _vp, _vp, _sz, _int, _vp, _vp, _int, _vp],
+    "lpc_muon_plan_bytes": [_mp, _int],
+    "lpc_muon_plan": [_mp, _int, _int, _vp, _sz, _wp],
+    "lpc_muon_step": [_vp, _wp, _int, _f64, _f64, _int, _f64, _int, _vp, _vp, _sz, _vp],
     # reference kernels for measurement (include/lpc_measure.h)
     "lpc_measure_stream": [_vp, _sz, _vp, _sz, _int, _vp],
     "lpc_measure_empty": [ctypes.c_uint, ctypes.c_uint, ctypes.c_uint, _sz, _vp, _vp],
 }
 
-SIZES = ("lpc_padded_rows", "lpc_router_workspace_bytes", "lpc_adamw_plan_bytes")  # these return a size_t, not a status
+SIZES = ("lpc_padded_rows", "lpc_router_workspace_bytes", "lpc_adamw_plan_bytes",
+         "lpc_muon_plan_bytes")  # these return a size_t, not a status
 
 _lock = threading.Lock()
 _lib = None
@@ -653,3 +673,159 @@ class AdamW:
             self._streams.add(handle)
         _run("lpc_adamw_step", self.device, handle, self._plan.data_ptr(), self._chunks, self.grad_dtype,
              self.state_bits, step, lr, beta1, beta2, eps, weight_decay, p.optional(grad_scale, "grad_scale", _F32, 1))
+
+
+_BF = (torch.bfloat16,)
+MX = 32  # elements of a microscaled block
+
+
+def _grouped_weight(w, groups, what="w"):
+    """(rows, columns) of each of a weight's matrices: [groups, rows, columns], or two dimensions for one group."""
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3) or w.numel() != groups * w.shape[-2] * w.shape[-1]:
+        raise ValueError("%s has shape %s, expected [%d, n, k]" % (what, tuple(getattr(w, "shape", ())), groups))
+    return w.shape[-2:]
+
+
+def _expect2(t, what, shape):
+    if _shape2(t, what) != shape:
+        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), list(shape)))
+
+
+def lpc_gemm_bf16(x, w, out, counts=None, stream=None):
+    """out [rows, n] (fp32 or bf16) = x [rows, k] times w [groups, n, k] (or [n, k]) transposed, bf16; counts [groups] int32:
+    rows of each group."""
+    (rows, k), groups = _shape2(x, "x"), _groups(counts)
+    n, kw = _grouped_weight(w, groups)
+    if kw != k:
+        raise ValueError("w has shape %s, expected [%d, n, %d]" % (tuple(w.shape), groups, k))
+    _expect2(out, "out", (rows, n))
+    p = _Args()
+    args = (p(x, "x", _BF, 0), rows, k, p(w, "w", _BF, 0), n, groups, p.optional(counts, "counts", _I32, 1),
+            p(out, "out", _FB, 0), _dtype(out))
+    _run("lpc_gemm_bf16", p.device, stream, *args)
+
+
+def lpc_gemm_bf16_dgrad(dy, w, dx, counts=None, stream=None):
+    """dx [rows, k] (fp32 or bf16) = dy [rows, n] times w [groups, n, k] (or [n, k]), bf16: the gradient of lpc_gemm_bf16's
+    rows."""
+    (rows, n), groups = _shape2(dy, "dy"), _groups(counts)
+    nw, k = _grouped_weight(w, groups)
+    if nw != n:
+        raise ValueError("w has shape %s, expected [%d, %d, k]" % (tuple(w.shape), groups, n))
+    _expect2(dx, "dx", (rows, k))
+    p = _Args()
+    args = (p(dy, "dy", _BF, 0), rows, n, p(w, "w", _BF, 0), k, groups, p.optional(counts, "counts", _I32, 1),
+            p(dx, "dx", _FB, 0), _dtype(dx))
+    _run("lpc_gemm_bf16_dgrad", p.device, stream, *args)
+
+
+def lpc_gemm_bf16_wgrad(dy, x, dw, counts=None, stream=None):
+    """dw [groups, n, k] (or [n, k]; fp32 or bf16) = each group's rows of dy [rows, n] transposed times those of x [rows, k],
+    bf16: the gradient of lpc_gemm_bf16's weights."""
+    (rows, n), groups = _shape2(dy, "dy"), _groups(counts)
+    _expect2(x, "x", (rows, _grouped_weight(dw, groups, "dw")[1]))
+    if dw.shape[-2] != n:
+        raise ValueError("dw has shape %s, expected [%d, %d, k]" % (tuple(dw.shape), groups, n))
+    p = _Args()
+    args = (p(dy, "dy", _BF, 0), n, p(x, "x", _BF, 0), x.shape[1], rows, groups, p.optional(counts, "counts", _I32, 1),
+            p(dw, "dw", _FB, 0), _dtype(dw))
+    _run("lpc_gemm_bf16_wgrad", p.device, stream, *args)
+
+
+def lpc_quantize_mxfp4(x, codes, scales, stream=None):
+    """E2M1 codes (two to a byte) and exponent bytes, one per 32 elements, of x (fp32 or bf16, a multiple of 32 elements)."""
+    p = _Args()
+    address, n = p(x, "x", _FB, 0), x.numel()
+    args = (address, _dtype(x), n, p(codes, "codes", _U8, n // 2, True), p(scales, "scales", _U8, n // MX, True))
+    _run("lpc_quantize_mxfp4", p.device, stream, *args)
+
+
+def lpc_dequantize_mxfp4(codes, scales, out, stream=None):
+    """The values (fp32 or bf16) that codes and exponent bytes stand for."""
+    p = _Args()
+    address, n = p(out, "out", _FB, 0), out.numel()
+    args = (p(codes, "codes", _U8, n // 2, True), p(scales, "scales", _U8, n // MX, True), n, address, _dtype(out))
+    _run("lpc_dequantize_mxfp4", p.device, stream, *args)
+
+
+def lpc_gemm_mxfp4(x, xs, w, ws, out, counts=None, stream=None):
+    """out [rows, n] (fp32 or bf16) = x [rows, k] times w [groups, n, k] (or [n, k]) transposed, held as E2M1 codes x [rows, k/2],
+    w [groups, n, k/2] with exponent bytes xs [rows, k/32], ws [groups, n, k/32]; counts [groups] int32: rows of each group."""
+    (rows, half), groups = _shape2(x, "x"), _groups(counts)
+    n, hw = _grouped_weight(w, groups)
+    if hw != half:
+        raise ValueError("w has shape %s, expected [%d, n, %d]" % (tuple(w.shape), groups, half))
+    _expect2(out, "out", (rows, n))
+    blocks = 2 * half // MX
+    p = _Args()
+    args = (p(x, "x", _U8, 0), p(xs, "xs", _U8, rows * blocks, True), rows, 2 * half, p(w, "w", _U8, 0),
+            p(ws, "ws", _U8, groups * n * blocks, True), n, groups, p.optional(counts, "counts", _I32, 1),
+            p(out, "out", _FB, 0), _dtype(out))
+    _run("lpc_gemm_mxfp4", p.device, stream, *args)
+
+
+class Muon:
+    """Muon over many matrices (lpc_muon_plan, lpc_muon_step): momentum, the update orthogonalised by Newton-Schulz iterations,
+    decoupled weight decay.
+
+    params (fp32), grads (all fp32 or all bf16) and the momenta m (fp32) are lists of contiguous tensors [rows, cols] or
+    [batch, rows, cols], checked once and updated in place; the tensors must stay where they are.  scales: one number per
+    tensor that multiplies its updates, by default 0.2 sqrt(max(rows, cols)), which gives an update the rms of 0.2 lr whatever
+    its shape.  copies: bf16 tensors that get the updated params.  The plan and a workspace of 6 bytes an element and more are
+    kept with the object.  A step reads no tensor's address again, so it can be captured in a graph (its hyperparameters are
+    then the captured ones; the object has to live as long as the graph is replayed); steps of one object must not overlap, and
+    a gradient that a program replaces by another tensor needs a new Muon."""
+
+    def __init__(self, params, grads, m, scales=None, copies=None):
+        lists = {"grads": grads, "m": m, "scales": scales, "copies": copies}
+        for what, ts in lists.items():
+            if ts is not None and len(ts) != len(params):
+                raise ValueError("%s has %d entries, params %d" % (what, len(ts), len(params)))
+        p, count = _Args(), len(params)
+        table = (_MuonTensor * max(count, 1))()
+        if count:
+            shapes = []
+            for i, t in enumerate(params):
+                if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
+                    raise ValueError("params[%d] must be a 2-D or 3-D tensor" % i)
+                shapes.append((1,) * (3 - t.dim()) + tuple(t.shape))
+            sizes = [t.numel() for t in params]
+            fields = {"param": p.many(params, "params", _F32, sizes),
+                      "grad": p.many(grads, "grads", (getattr(grads[0], "dtype", None),) if getattr(grads[0], "dtype", None) in _FB else _FB, sizes),
+                      "m": p.many(m, "m", _F32, sizes)}
+            if copies is not None:
+                fields["copy"] = p.many(copies, "copies", _BF, sizes)
+            for i, (batch, rows, cols) in enumerate(shapes):
+                for name, pointers in fields.items():
+                    setattr(table[i], name, pointers[i])
+                table[i].batch, table[i].rows, table[i].cols = batch, rows, cols
+                table[i].scale = 0.2 * max(rows, cols) ** 0.5 if scales is None else float(scales[i])
+        self.grad_dtype = _dtype(grads[0]) if count else LPC_F32
+        self.device = p.device
+        self._tensors = (list(params), list(grads), list(m), None if copies is None else list(copies))  # kept alive
+        size = lib().lpc_muon_plan_bytes(table, count)
+        host = torch.empty(size, dtype=torch.uint8)
+        self._work = _MuonWork()
+        _call("lpc_muon_plan", table, count, self.grad_dtype, host.data_ptr() if size else None, size, ctypes.byref(self._work))
+        self._plan = self._space = None
+        if self._work.matrices:
+            self._plan = host.to("cuda:%d" % self.device)
+            self._space = torch.empty(self._work.workspace_bytes, dtype=torch.uint8, device=self._plan.device)
+        # streams after whose work plan and workspace may be handed out again when this object goes
+        self._streams = {torch._C._cuda_getCurrentRawStream(self.device)} if self._work.matrices else set()
+
+    def step(self, lr: float, beta: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True, iterations: int = 5,
+             grad_scale=None, stream=None):
+        """One update; grad_scale: a GPU tensor whose first element multiplies every gradient."""
+        if self._plan is None:
+            return
+        p = _Args()
+        p.device = self.device
+        handle = torch._C._cuda_getCurrentRawStream(self.device) if stream is None else getattr(stream, "cuda_stream", stream)
+        if handle not in self._streams:
+            for t in (self._plan, self._space):
+                t.record_stream(_torch_stream(handle, t.device))
+            self._streams.add(handle)
+        _run("lpc_muon_step", self.device, handle, self._plan.data_ptr(), ctypes.byref(self._work), self.grad_dtype, lr, beta,
+             1 if nesterov else 0, weight_decay, iterations, p.optional(grad_scale, "grad_scale", _F32, 1),
+             self._space.data_ptr(), self._work.workspace_bytes)

@@ -3,7 +3,9 @@
  * to the low-precision collectives: what a rank computes with the E4M3 rows an
  * all-to-all delivers (the FP8 block-scaled product, for one weight or for one
  * weight per expert, and its backward pass), what decides where rows go (the
- * expert router), and what follows the gradient allreduce (AdamW).
+ * expert router), what follows the gradient allreduce (AdamW, and Muon for
+ * matrices), and the same experts' layers in bf16 (products and their backward
+ * pass) and with weights in microscaled 4-bit floating point.
  *
  * Formats are those of lpc.h: E4M3FN codes, one FP32 scale s = absmax/448 per
  * 128 elements, code = E4M3(fl32(x / s)), a block whose scale is zero has all
@@ -218,6 +220,143 @@ lpc_status lpc_adamw_plan(const lpc_adamw_tensor *tensors, int count, lpc_dtype 
 lpc_status lpc_adamw_step(const void *plan, size_t chunks, lpc_dtype grad_t, int state_bits,
                           int64_t step, double lr, double beta1, double beta2, double eps,
                           double weight_decay, const float *grad_scale, hipStream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* bf16 products                                                            */
+/* ---------------------------------------------------------------------- */
+
+/* out[r, j] = sum over i of x[r, i] * w[g, j, i] for the group g that row r
+ * belongs to, rounded once to out_t.  Products are exact and sums are held in
+ * FP32: off by at most 2 k 2^-24 of the sum of the terms' magnitudes.
+ *   x [rows, k], w [groups, n, k] bf16; out [rows, n] of type out_t
+ *   counts as for lpc_gemm_fp8: group g's rows follow group g-1's, a negative
+ *      count is taken as 0, groups end at `rows`, rows past the last group give
+ *      zeros; may be NULL when groups == 1
+ *   k a positive multiple of 8; any n; rows, k, n < 2^31, groups in
+ *   1..LPC_MAX_GROUPS, each matrix at most LPC_MAX_MATRIX elements (else
+ *   LPC_ERR_SHAPE).  rows == 0 or n == 0: LPC_OK, no work.                   */
+lpc_status lpc_gemm_bf16(const uint16_t *x, size_t rows, size_t k,
+                         const uint16_t *w, size_t n, int groups, const int32_t *counts,
+                         void *out, lpc_dtype out_t, hipStream_t stream);
+
+/* Gradient of the rows: dx[r, i] = sum over j of dy[r, j] * w[g, j, i], of the
+ * weight as it lies; rows past the last group give zeros.
+ *   dy [rows, n], w [groups, n, k] bf16; dx [rows, k] of type out_t
+ *   n and k positive multiples of 8 (else LPC_ERR_SHAPE), the rest as above.
+ *   rows == 0 or k == 0: LPC_OK, no work.                                    */
+lpc_status lpc_gemm_bf16_dgrad(const uint16_t *dy, size_t rows, size_t n,
+                               const uint16_t *w, size_t k, int groups, const int32_t *counts,
+                               void *dx, lpc_dtype out_t, hipStream_t stream);
+
+/* Gradient of the weights: dw[g, j, i] = sum over the rows r of group g of
+ * dy[r, j] * x[r, i]; zeros for a group without rows.
+ *   dy [rows, n], x [rows, k] bf16; dw [groups, n, k] of type out_t
+ *   n and k multiples of 8 (else LPC_ERR_SHAPE).  n == 0 or k == 0: LPC_OK, no
+ *   work; rows == 0 writes zeros (dy and x may then be NULL).                */
+lpc_status lpc_gemm_bf16_wgrad(const uint16_t *dy, size_t n, const uint16_t *x, size_t k,
+                               size_t rows, int groups, const int32_t *counts,
+                               void *dw, lpc_dtype out_t, hipStream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Microscaled 4-bit floating point (MXFP4)                                 */
+/* ---------------------------------------------------------------------- */
+
+/* The OCP format: E2M1 codes (sign, then magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6),
+ * two to a byte, the first of the two in the low bits, and per 32 elements an
+ * exponent byte e for the scale 2^(e-127).  For n elements: codes [n/2] and
+ * scales [n/32].                                                             */
+
+/* scale = 2^(floor(log2(absmax of the 32)) - 2), no less than 2^-127 (which a
+ * block of zeros gets); code = E2M1(x / scale), to nearest, ties to even, what
+ * is above 5 to 6.
+ *   x [n] of type `in`; n a multiple of 32, at most LPC_MAX_MATRIX (else
+ *   LPC_ERR_SHAPE).  A matrix's rows are quantized by one call if their length
+ *   is a multiple of 32.  n == 0: LPC_OK, no work.                           */
+lpc_status lpc_quantize_mxfp4(const void *x, lpc_dtype in, size_t n,
+                              uint8_t *codes, uint8_t *scales, hipStream_t stream);
+
+/* out[i] = E2M1 value of code i times its block's scale, rounded to out_t
+ * (exact but for what lies below out_t's normal numbers).  Bytes as
+ * lpc_quantize_mxfp4 writes them, 0 to 252.                                  */
+lpc_status lpc_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, size_t n,
+                                void *out, lpc_dtype out_t, hipStream_t stream);
+
+/* out[r, j] = sum over blocks b of 32 of
+ *   2^(xs[r, b] - 127) * 2^(ws[g, j, b] - 127) * (sum over i in b of x[r, i] * w[g, j, i])
+ * for the group g that row r belongs to, rounded once to out_t.  Sums are held
+ * in FP32: off by at most 2 k 2^-24 of the sum of the terms' magnitudes.
+ *   x  codes [rows, k/2], xs [rows, k/32]; w codes [groups, n, k/2], ws
+ *      [groups, n, k/32]: rows as lpc_quantize_mxfp4 writes them; an exponent
+ *      byte of 255 makes a NaN of every sum it is part of
+ *   counts, rows past the last group and limits as for lpc_gemm_bf16, but k a
+ *   positive multiple of 128                                                 */
+lpc_status lpc_gemm_mxfp4(const uint8_t *x, const uint8_t *xs, size_t rows, size_t k,
+                          const uint8_t *w, const uint8_t *ws, size_t n,
+                          int groups, const int32_t *counts,
+                          void *out, lpc_dtype out_t, hipStream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Muon over many matrices                                                  */
+/* ---------------------------------------------------------------------- */
+
+#define LPC_MUON_MAX_SIDE ((size_t)1 << 20)    /* rows or columns of a matrix */
+#define LPC_MUON_MAX_ITERATIONS 10
+
+/* `batch` matrices of rows x cols one after the other, as a layer of experts
+ * holds them.  Device pointers, 16-byte aligned.
+ *   param  FP32, updated in place;  grad  of the plan's type, read
+ *   m      FP32 momentum, updated in place
+ *   copy   bf16 copy of the updated param, or NULL (for each tensor)
+ *   scale  of this tensor's updates                                          */
+typedef struct {
+    float *param;
+    const void *grad;
+    float *m;
+    uint16_t *copy;
+    size_t batch, rows, cols;
+    double scale;
+} lpc_muon_tensor;
+
+/* What a step of a plan launches; lpc_muon_plan writes it and lpc_muon_step
+ * takes it as it is.                                                         */
+typedef struct {
+    size_t matrices, chunks, squares, updates;
+    size_t workspace_bytes;
+} lpc_muon_work;
+
+/* Bytes of the plan of these tensors.  tensors: host array; 0 for no work, for
+ * sizes that are refused and for NULL.  No HIP call.                         */
+size_t lpc_muon_plan_bytes(const lpc_muon_tensor *tensors, int count);
+
+/* Check the tensors and write the plan to HOST memory (`plan`, of
+ * lpc_muon_plan_bytes bytes); the caller copies it to a 16-byte aligned device
+ * buffer and keeps it as long as the tensors stay where they are.
+ *   Tensors without elements are left out.  rows and cols at most
+ *   LPC_MUON_MAX_SIDE, 2^24 pieces of a kind at most (tiles of 128 x 128, chunks
+ *   of 16,384 elements; else LPC_ERR_SHAPE).  Tensors must not overlap.      */
+lpc_status lpc_muon_plan(const lpc_muon_tensor *tensors, int count, lpc_dtype grad_t,
+                         void *plan, size_t plan_bytes, lpc_muon_work *work);
+
+/* One step over every matrix of a plan:
+ *   g = grad * grad_scale[0] (grad_scale NULL: 1)
+ *   m = beta m + (1 - beta) g
+ *   u = nesterov ? (1 - beta) g + beta m : m
+ *   X = u / |u| (Frobenius; zeros if u is), then `iterations` times
+ *       A = X X^T,  B = -4.775 A + 2.0315 A A,  X = 3.4445 X + B X
+ *   param = param (1 - lr weight_decay) - lr scale X
+ * m and the parameters' last line in FP32, every operation rounded on its own;
+ * |u| in 64 bits.  X is held in fp16 halves of together 22 bits and the products
+ * take its high half, A and B in fp16, sums in FP32: X is off by 2e-3 of itself
+ * (2-norm) at most on the matrices measured, whatever their singular values.
+ *   plan   DEVICE copy of the plan;  work, grad_t as planned
+ *   workspace  device memory of work->workspace_bytes, no initial contents
+ *      needed; steps that overlap need one each
+ *   beta in [0, 1), iterations in 1..LPC_MUON_MAX_ITERATIONS (else
+ *   LPC_ERR_SHAPE)                                                           */
+lpc_status lpc_muon_step(const void *plan, const lpc_muon_work *work, lpc_dtype grad_t,
+                         double lr, double beta, int nesterov, double weight_decay, int iterations,
+                         const float *grad_scale, void *workspace, size_t workspace_bytes,
+                         hipStream_t stream);
 
 #ifdef __cplusplus
 }

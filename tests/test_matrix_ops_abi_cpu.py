@@ -1,0 +1,165 @@
+"""Argument checks of the bf16 products, the 4-bit microscaled operators and Muon (include/lpc_ops.h) on the host, no GPU needed:
+every call here is one that validation must refuse or that has nothing to do, so the fake addresses are never used.  Also
+Muon's plan."""
+import ctypes
+
+import pytest
+import torch
+
+from fp8_precision_allreduce_amd import lpc
+from test_ops_abi_cpu import ALIGN, A, B, BF16, DTYPE, F32, HIP, L, NULL, OK, SHAPE, replaced  # noqa: F401
+
+
+def test_bf16_product_errors(L):  # noqa: F811
+    f = L.lpc_gemm_bf16
+    ok = [A, 4, 264, A, 101, 2, A, A, BF16, None]
+    assert f(*ok) == HIP and f(*replaced(ok, _8=F32)) == HIP        # passes the checks; no device
+    assert f(*replaced(ok, _8=2)) == DTYPE
+    assert f(*replaced(ok, _1=0, _0=None)) == OK and f(*replaced(ok, _4=0, _7=None)) == OK
+    for i in (0, 3, 6, 7):
+        assert f(*replaced(ok, **{"_%d" % i: None})) == NULL, i
+    assert f(*replaced(ok, _6=None, _5=1)) == HIP                   # one group needs no counts
+    for i in (0, 3, 7):
+        assert f(*replaced(ok, **{"_%d" % i: B})) == ALIGN, i
+    assert f(*replaced(ok, _6=A + 2)) == ALIGN and f(*replaced(ok, _6=A + 4)) == HIP
+    for bad in (dict(_2=0), dict(_2=12), dict(_5=0), dict(_5=1025), dict(_5=-1), dict(_1=1 << 31), dict(_4=1 << 31), dict(_2=1 << 31),
+                dict(_1=(1 << 64) - 8), dict(_1=1 << 30, _2=1 << 20), dict(_4=1 << 25, _2=1 << 14, _5=1024)):
+        assert f(*replaced(ok, **bad)) == SHAPE, bad
+
+
+def test_bf16_dgrad_errors(L):  # noqa: F811
+    f = L.lpc_gemm_bf16_dgrad
+    ok = [A, 4, 104, A, 264, 2, A, A, BF16, None]
+    assert f(*ok) == HIP and f(*replaced(ok, _8=7)) == DTYPE
+    assert f(*replaced(ok, _1=0, _0=None)) == OK and f(*replaced(ok, _4=0, _7=None)) == OK
+    for i in (0, 3, 6, 7):
+        assert f(*replaced(ok, **{"_%d" % i: None})) == NULL, i
+    for i in (0, 3, 7):
+        assert f(*replaced(ok, **{"_%d" % i: B})) == ALIGN, i
+    for bad in (dict(_2=0), dict(_2=100), dict(_4=12), dict(_5=0), dict(_5=1025), dict(_1=1 << 31), dict(_2=1 << 31), dict(_4=1 << 31)):
+        assert f(*replaced(ok, **bad)) == SHAPE, bad
+
+
+def test_bf16_wgrad_errors(L):  # noqa: F811
+    f = L.lpc_gemm_bf16_wgrad
+    ok = [A, 104, A, 264, 5, 2, A, A, F32, None]
+    assert f(*ok) == HIP and f(*replaced(ok, _8=7)) == DTYPE
+    assert f(*replaced(ok, _1=0)) == OK and f(*replaced(ok, _3=0)) == OK
+    for i in (0, 2, 6, 7):
+        assert f(*replaced(ok, **{"_%d" % i: None})) == NULL, i
+    assert f(*replaced(ok, _0=None, _2=None, _4=0)) == HIP          # no rows: zeros are still written
+    for i in (0, 2, 7):
+        assert f(*replaced(ok, **{"_%d" % i: B})) == ALIGN, i
+    for bad in (dict(_1=100), dict(_3=12), dict(_5=0), dict(_5=1025), dict(_4=1 << 31), dict(_1=1 << 31), dict(_1=1 << 21, _3=1 << 20)):
+        assert f(*replaced(ok, **bad)) == SHAPE, bad
+
+
+def test_mxfp4_errors(L):  # noqa: F811
+    f, g, h = L.lpc_quantize_mxfp4, L.lpc_dequantize_mxfp4, L.lpc_gemm_mxfp4
+    q, d = [A, BF16, 96, A, A, None], [A, A, 96, A, BF16, None]
+    assert f(*q) == HIP and g(*d) == HIP
+    assert f(*replaced(q, _1=2)) == DTYPE and g(*replaced(d, _4=2)) == DTYPE
+    assert f(*replaced(q, _2=0, _0=None)) == OK and g(*replaced(d, _2=0, _0=None)) == OK
+    for i in (0, 3, 4):
+        assert f(*replaced(q, **{"_%d" % i: None})) == NULL and f(*replaced(q, **{"_%d" % i: B})) == ALIGN
+    for i in (0, 1, 3):
+        assert g(*replaced(d, **{"_%d" % i: None})) == NULL and g(*replaced(d, **{"_%d" % i: B})) == ALIGN
+    for n in (1, 31, 33, 100, (1 << 40) + 32, (1 << 64) - 32):
+        assert f(*replaced(q, _2=n)) == SHAPE and g(*replaced(d, _2=n)) == SHAPE, n
+    ok = [A, A, 4, 256, A, A, 101, 2, A, A, BF16, None]
+    assert h(*ok) == HIP and h(*replaced(ok, _10=3)) == DTYPE
+    assert h(*replaced(ok, _2=0, _0=None)) == OK and h(*replaced(ok, _6=0, _9=None)) == OK
+    for i in (0, 1, 4, 5, 8, 9):
+        assert h(*replaced(ok, **{"_%d" % i: None})) == NULL, i
+    assert h(*replaced(ok, _8=None, _7=1)) == HIP
+    for i in (0, 1, 4, 5, 9):
+        assert h(*replaced(ok, **{"_%d" % i: B})) == ALIGN, i
+    for bad in (dict(_3=0), dict(_3=32), dict(_3=192), dict(_7=0), dict(_7=1025), dict(_2=1 << 31), dict(_6=1 << 31),
+                dict(_2=1 << 30, _3=1 << 20)):
+        assert h(*replaced(ok, **bad)) == SHAPE, bad
+
+
+def plan(L, rows, grad=F32):  # noqa: F811
+    t = (lpc._MuonTensor * max(len(rows), 1))(*[lpc._MuonTensor(*r) for r in rows])
+    size = L.lpc_muon_plan_bytes(t, len(rows))
+    host, work = (ctypes.c_uint8 * max(size, 1))(), lpc._MuonWork(9, 9, 9, 9, 9)
+    return L.lpc_muon_plan(t, len(rows), grad, host, size, ctypes.byref(work)), work, bytes(host[:size])
+
+
+def test_muon_plan(L):  # noqa: F811
+    row = (A, A, A, None, 2, 300, 100, 0.5)
+    assert plan(L, [])[0] == OK and plan(L, [])[1].matrices == 0
+    for i in (4, 5, 6):
+        st, work, data = plan(L, [(None,) * 4 + row[4:i] + (0,) + row[i + 1:]])
+        assert st == OK and work.matrices == 0 and not data
+    st, work, data = plan(L, [row, (A, A, A, A, 1, 1, 1, 1.0)])
+    assert st == OK and work.matrices == 3 and len(data) % 16 == 0
+    # X's halves twice and once, [300, 128]; A and B, [100, 128]; a sum for each of two chunks
+    assert work.workspace_bytes >= 2 * (3 * 300 * 128 * 2 + 2 * 100 * 128 * 2 + 2 * 8)
+    for i in range(3):
+        assert plan(L, [row[:i] + (None,) + row[i + 1:]])[0] == NULL
+        assert plan(L, [row[:i] + (B,) + row[i + 1:]])[0] == ALIGN
+    assert plan(L, [row[:3] + (B,) + row[4:]])[0] == ALIGN
+    assert plan(L, [row], 5)[0] == DTYPE
+    side = 1 << 20
+    for bad in ((1, side + 1, 4), (1, 4, side + 1), (1, side, side), (1 << 40, 4, 4), ((1 << 64) - 1, 4, 4), (1, (1 << 64) - 1, 4)):
+        t = (lpc._MuonTensor * 1)(lpc._MuonTensor(A, A, A, None, *bad, 1.0))
+        work = lpc._MuonWork(9, 9, 9, 9, 9)
+        assert L.lpc_muon_plan_bytes(t, 1) == 0
+        assert L.lpc_muon_plan(t, 1, F32, (ctypes.c_uint8 * 64)(), 64, ctypes.byref(work)) == SHAPE and work.matrices == 0, bad
+    t, work = (lpc._MuonTensor * 1)(lpc._MuonTensor(*row)), lpc._MuonWork()
+    need = L.lpc_muon_plan_bytes(t, 1)
+    host = (ctypes.c_uint8 * need)()
+    assert L.lpc_muon_plan(t, 1, F32, host, need - 1, ctypes.byref(work)) == SHAPE
+    assert L.lpc_muon_plan(t, 1, F32, None, need, ctypes.byref(work)) == NULL
+    assert L.lpc_muon_plan(t, 1, F32, host, need, None) == NULL
+    assert L.lpc_muon_plan(t, -1, F32, host, need, ctypes.byref(work)) == SHAPE
+    assert L.lpc_muon_plan(None, 1, F32, host, need, ctypes.byref(work)) == NULL
+
+
+def test_muon_step_errors(L):  # noqa: F811
+    f = L.lpc_muon_step
+    _, work, _ = plan(L, [(A, A, A, None, 2, 300, 100, 0.5)])
+    w = ctypes.byref(work)
+    ok = [A, w, F32, 0.02, 0.95, 1, 0.1, 5, None, A, work.workspace_bytes, None]
+    assert f(*ok) == HIP and f(*replaced(ok, _8=A + 4, _2=BF16)) == HIP
+    assert f(*replaced(ok, _2=4)) == DTYPE
+    none = lpc._MuonWork()
+    assert f(*replaced(ok, _1=ctypes.byref(none), _0=None, _9=None)) == OK
+    for i in (0, 1, 9):
+        assert f(*replaced(ok, **{"_%d" % i: None})) == NULL, i
+    assert f(*replaced(ok, _0=B)) == ALIGN and f(*replaced(ok, _9=B)) == ALIGN and f(*replaced(ok, _8=A + 2)) == ALIGN
+    for bad in (dict(_4=1.0), dict(_4=-0.1), dict(_4=float("nan")), dict(_7=0), dict(_7=-1), dict(_7=11), dict(_10=work.workspace_bytes - 1)):
+        assert f(*replaced(ok, **bad)) == SHAPE, bad
+    for field in ("matrices", "chunks", "squares", "updates"):
+        odd = lpc._MuonWork.from_buffer_copy(work)
+        setattr(odd, field, (1 << 24) + 1)
+        assert f(*replaced(ok, _1=ctypes.byref(odd))) == SHAPE, field
+
+
+def test_binding_refusals(L):  # noqa: F811
+    bf, f32, u8 = torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(4, 4), torch.zeros(4, 64, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        lpc.lpc_gemm_bf16(bf, bf, f32)
+    with pytest.raises(ValueError, match="w has shape"):
+        lpc.lpc_gemm_bf16(bf, bf[:, :64], f32)
+    with pytest.raises(ValueError, match="out has shape"):
+        lpc.lpc_gemm_bf16(bf, bf, torch.zeros(4, 5))
+    with pytest.raises(ValueError, match="w has shape"):
+        lpc.lpc_gemm_bf16_dgrad(f32, bf[:3], bf)
+    with pytest.raises(ValueError, match="dx has shape"):
+        lpc.lpc_gemm_bf16_dgrad(f32, bf, f32)
+    with pytest.raises(ValueError, match="dw has shape"):
+        lpc.lpc_gemm_bf16_wgrad(f32, bf, torch.zeros(5, 128))
+    with pytest.raises(ValueError, match="x has shape"):
+        lpc.lpc_gemm_bf16_wgrad(f32, bf[:3], torch.zeros(4, 128))
+    with pytest.raises(ValueError, match="GPU tensor"):
+        lpc.lpc_quantize_mxfp4(bf, u8, u8)
+    with pytest.raises(ValueError, match="w has shape"):
+        lpc.lpc_gemm_mxfp4(u8, u8, u8[:, :32], u8, f32)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        lpc.Muon([f32], [f32], [f32])
+    with pytest.raises(ValueError, match="2-D or 3-D"):
+        lpc.Muon([f32.view(-1)], [f32], [f32])
+    with pytest.raises(ValueError, match="grads has 2 entries"):
+        lpc.Muon([f32], [f32, f32], [f32])
