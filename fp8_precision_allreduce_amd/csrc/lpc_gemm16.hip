@@ -38,7 +38,6 @@ __device__ __forceinline__ void tile(const Gemm16Args& a, uint32_t g, uint32_t q
                                      uint8_t* lds) {
     const uint32_t np = min(S::BP, outputs_p<M>(a) - p0);
     const uint32_t length = M == kWgrad ? r1 - r0 : g == a.groups ? 0 : M == kProduct ? a.k : a.n;
-    const uint32_t slabs = (length + kSlabRows - 1) / kSlabRows, last = slabs ? length - (slabs - 1) * kSlabRows : 0;
     const size_t matrix = (size_t)(g == a.groups ? 0 : g) * a.n * a.k;
     Operand q, p;
     if constexpr (M == kProduct) {
@@ -52,45 +51,69 @@ __device__ __forceinline__ void tile(const Gemm16Args& a, uint32_t g, uint32_t q
         p = operand(a.p + (size_t)r0 * a.k + p0, a.k, np);
     }
     f32x4_t acc[S::Phases * S::F][S::PF];
-    tile_sums<MmaBf16, kFormQ<M>, kFormP<M>, S>(q, p, slabs, Tail{2 * last, last}, lds, acc);
+    tile_sums<MmaBf16, kFormQ<M>, kFormP<M>, S>(q, p, contraction(length), lds, acc);
     const uint32_t ldo = outputs_p<M>(a);
     Out* out = static_cast<Out*>(a.out) + (M == kWgrad ? matrix : 0) + (size_t)q0 * ldo + p0;
     store_tile<Out, S>(acc, out, ldo, nq, np, lds);
 }
 
+using Large = LargeOf<false>;
 using Small = SmallOf<false>;
 
-template <int M, typename Out, typename S>
-__global__ __launch_bounds__(kTileWaves * 64, 2) void gemm16_kernel(Gemm16Args a) {
-    __shared__ __attribute__((aligned(128))) uint8_t lds[S::kBytes];
-    const uint32_t tiles_p = (outputs_p<M>(a) + S::BP - 1) / S::BP;
-    const uint32_t t = (uint32_t)xcd_tile(), tq = t / tiles_p, p0 = t % tiles_p * S::BP;
-    if constexpr (M == kWgrad) {
-        const GroupTile g = find_group(a.counts, a.groups, a.rows, 1, blockIdx.y);
-        tile<M, Out, S>(a, g.group, tq * S::BQ, min(S::BQ, a.n - tq * S::BQ), p0, g.row, g.row + g.rows, lds);
-    } else {
-        const GroupTile w = find_tile(a.counts, a.groups, a.rows, S::BQ, tq);
-        if (w.rows != 0) tile<M, Out, S>(a, w.group, w.row, w.rows, p0, 0, 0, lds);
+// product and dgrad: large tiles, and small ones where these fill the chip better
+template <int M, typename Out>
+__global__ __launch_bounds__(kTileWaves * 64, 2) void gemm16_rows_kernel(Gemm16Args a) {
+    __shared__ __attribute__((aligned(128))) uint8_t lds[Large::kBytes > Small::kBytes ? Large::kBytes : Small::kBytes];
+    Share s;
+    if (!find_share<Large, Small>(a.counts, a.groups, a.rows, outputs_p<M>(a), &s)) return;
+    if (s.large) {
+        tile<M, Out, Large>(a, s.w.group, s.w.row, s.w.rows, s.p0, 0, 0, lds);
+        return;
+    }
+    for (uint32_t p = s.p0; p < s.p1; p += Small::BP) {
+        tile<M, Out, Small>(a, s.w.group, s.w.row, s.w.rows, p, 0, 0, lds);
+        __syncthreads();  // LDS may be written again
     }
 }
 
-// Tiles of T rows that any counts can make of `rows` rows in `groups` groups and the rows past them: every group and the
-// rest may end in a short tile.
-uint64_t most_tiles(const Gemm16Args& a, uint32_t T) {
-    return (a.rows + (uint64_t)T - 1) / T + (a.counts ? a.groups : 0);
+template <typename Out, typename S>
+__global__ __launch_bounds__(kTileWaves * 64, 2) void gemm16_wgrad_kernel(Gemm16Args a) {
+    __shared__ __attribute__((aligned(128))) uint8_t lds[S::kBytes];
+    const uint32_t tiles_p = (a.k + S::BP - 1) / S::BP;
+    const uint2 t = in_bands((uint32_t)xcd_tile(), gridDim.x / tiles_p, tiles_p);
+    const GroupTile g = group_by_rows(a.counts, a.groups, a.rows, blockIdx.y);
+    tile<kWgrad, Out, S>(a, g.group, t.x * S::BQ, min(S::BQ, a.n - t.x * S::BQ), t.y * S::BP, g.row, g.row + g.rows, lds);
 }
 
-template <int M, typename Out, typename S>
-hipError_t launch_tiled(const Gemm16Args& a, hipStream_t stream) {
-    const uint64_t tiles_p = (outputs_p<M>(a) + (uint64_t)S::BP - 1) / S::BP;
-    const uint64_t wgs = (M == kWgrad ? (a.n + (uint64_t)S::BQ - 1) / S::BQ : most_tiles(a, S::BQ)) * tiles_p;
+template <int M, typename Out>
+hipError_t launch_rows(const Gemm16Args& a, hipStream_t stream) {
+    const uint64_t tiles_p = (outputs_p<M>(a) + (uint64_t)Large::BP - 1) / Large::BP;
+    const uint64_t wgs = shares<Large, Small>(most_tiles(a.counts, a.groups, a.rows, Large::BQ) * tiles_p);
     if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
-    return enqueue(gemm16_kernel<M, Out, S>, dim3((uint32_t)wgs, M == kWgrad ? a.groups : 1), dim3(kTileWaves * 64), stream, a);
+    return enqueue(gemm16_rows_kernel<M, Out>, dim3((uint32_t)wgs), dim3(kTileWaves * 64), stream, a);
+}
+
+template <typename S>
+uint64_t wgrad_tiles(const Gemm16Args& a) {
+    return ((a.n + (uint64_t)S::BQ - 1) / S::BQ) * ((a.k + (uint64_t)S::BP - 1) / S::BP);
+}
+
+template <typename Out, typename S>
+hipError_t launch_wgrad(const Gemm16Args& a, hipStream_t stream) {
+    const uint64_t wgs = wgrad_tiles<S>(a);
+    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    return enqueue(gemm16_wgrad_kernel<Out, S>, dim3((uint32_t)wgs, a.groups), dim3(kTileWaves * 64), stream, a);
 }
 
 template <int M>
 hipError_t launch(const Gemm16Args& a, int out_bf16, hipStream_t stream) {
-    return out_bf16 ? launch_tiled<M, uint16_t, Small>(a, stream) : launch_tiled<M, float, Small>(a, stream);
+    if constexpr (M == kWgrad) {
+        const bool small = wgrad_tiles<Large>(a) * a.groups <= 128;
+        if (small) return out_bf16 ? launch_wgrad<uint16_t, Small>(a, stream) : launch_wgrad<float, Small>(a, stream);
+        return out_bf16 ? launch_wgrad<uint16_t, Large>(a, stream) : launch_wgrad<float, Large>(a, stream);
+    } else {
+        return out_bf16 ? launch_rows<M, uint16_t>(a, stream) : launch_rows<M, float>(a, stream);
+    }
 }
 
 }  // namespace

@@ -152,13 +152,6 @@ __device__ __forceinline__ Operand operand(const _Float16* first, uint32_t ld, u
     return {reinterpret_cast<const uint8_t*>(first), (size_t)ld * 2, n, nullptr};
 }
 
-// the contraction's slabs; rows along are zeros from `length` to a multiple of 64
-__device__ __forceinline__ uint32_t slabs_of(uint32_t length, Tail* t) {
-    const uint32_t slabs = (length + kSlabRows - 1) / kSlabRows, last = length - (slabs - 1) * kSlabRows;
-    *t = Tail{2 * last, last};
-    return slabs;
-}
-
 // where a lane's four neighbouring elements (i, j) of a tile's sums are: row and first column within the tile
 struct Place {
     uint32_t q, p;
@@ -193,21 +186,17 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_square_kernel(MuonPla
     const uint32_t s = min(x.rows, x.cols), tiles = (s + Tile::BP - 1) / Tile::BP;
     const uint32_t q0 = piece.index / tiles * Tile::BQ, p0 = piece.index % tiles * Tile::BP;
     const uint32_t nq = min(Tile::BQ, s - q0), np = min(Tile::BP, s - p0);
-    Tail t;
     f32x4_t acc[Tile::Phases * Tile::F][Tile::PF];
     if (Second) {
-        const uint32_t slabs = slabs_of(s, &t);
         tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(w.a + (size_t)q0 * x.lda, x.lda, nq), operand(w.a + (size_t)p0 * x.lda, x.lda, np),
-                                                slabs, t, lds, acc);
+                                                contraction(s), lds, acc);
     } else if (tall) {
         // columns up to ldx hold zeros, so that pieces of 8 are whole
-        const uint32_t slabs = slabs_of(x.rows, &t);
         tile_sums<MmaF16, kAcross, kAcross, Tile>(operand(w.high[from] + q0, x.ldx, min(Tile::BQ, x.ldx - q0)),
-                                                  operand(w.high[from] + p0, x.ldx, min(Tile::BP, x.ldx - p0)), slabs, t, lds, acc);
+                                                  operand(w.high[from] + p0, x.ldx, min(Tile::BP, x.ldx - p0)), contraction(x.rows), lds, acc);
     } else {
-        const uint32_t slabs = slabs_of(x.cols, &t);
         tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(w.high[from] + (size_t)q0 * x.ldx, x.ldx, nq),
-                                                operand(w.high[from] + (size_t)p0 * x.ldx, x.ldx, np), slabs, t, lds, acc);
+                                                operand(w.high[from] + (size_t)p0 * x.ldx, x.ldx, np), contraction(x.cols), lds, acc);
     }
     each_place(acc, [&](f32x4_t& v, uint32_t q, uint32_t p) {
         v = v * (1.0f / kHeld);
@@ -230,16 +219,12 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPla
     const uint32_t q0 = piece.index / tiles * Tile::BQ, p0 = piece.index % tiles * Tile::BP;
     const uint32_t nq = min(Tile::BQ, x.rows - q0), np = min(Tile::BP, x.cols - p0);
     const _Float16* high = w.high[from];
-    Tail t;
     f32x4_t acc[Tile::Phases * Tile::F][Tile::PF];
     if (x.rows > x.cols) {
-        const uint32_t slabs = slabs_of(x.cols, &t);
-        tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(high + (size_t)q0 * x.ldx, x.ldx, nq), operand(w.b + (size_t)p0 * x.lda, x.lda, np), slabs,
-                                                t, lds, acc);
+        tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(high + (size_t)q0 * x.ldx, x.ldx, nq), operand(w.b + (size_t)p0 * x.lda, x.lda, np), contraction(x.cols), lds, acc);
     } else {
-        const uint32_t slabs = slabs_of(x.rows, &t);
         tile_sums<MmaF16, kAlong, kAcross, Tile>(operand(w.b + (size_t)q0 * x.lda, x.lda, nq),
-                                                 operand(high + p0, x.ldx, min(Tile::BP, x.ldx - p0)), slabs, t, lds, acc);
+                                                 operand(high + p0, x.ldx, min(Tile::BP, x.ldx - p0)), contraction(x.rows), lds, acc);
     }
     each_place(acc, [&](f32x4_t& v, uint32_t q, uint32_t p) {
         if (q >= nq || p >= np) {

@@ -81,37 +81,43 @@ struct Mxfp4Args {
     uint32_t groups, rows, n, k;
 };
 
+using Large = LargeOf<true>;
 using Small = SmallOf<true>;
 
 // outputs [q0, + nq) x [p0, + np) of group g (== groups: rows past the last one, whose sums are empty)
 template <typename Out, typename S>
 __device__ __forceinline__ void tile(const Mxfp4Args& a, uint32_t g, uint32_t q0, uint32_t nq, uint32_t p0, uint8_t* lds) {
     const uint32_t np = min(S::BP, a.n - p0), row = a.k / 2, scale_row = a.k / 32;
-    const uint32_t slabs = g == a.groups ? 0 : (row + kSlab - 1) / kSlab, last = row - (slabs - 1) * kSlab;
     const size_t first = (size_t)(g == a.groups ? 0 : g) * a.n + p0;
     const Operand q{a.x + (size_t)q0 * row, row, nq, a.xs + (size_t)q0 * scale_row};
     const Operand p{a.w + first * row, row, np, a.ws + first * scale_row};
     f32x4_t acc[S::Phases * S::F][S::PF];
-    tile_sums<MmaMxfp4, kAlong, kAlong, S>(q, p, slabs, Tail{last, 0}, lds, acc);
+    tile_sums<MmaMxfp4, kAlong, kAlong, S>(q, p, contraction(g == a.groups ? 0 : row / 2), lds, acc);
     store_tile<Out, S>(acc, static_cast<Out*>(a.out) + (size_t)q0 * a.n + p0, a.n, nq, np, lds);
 }
 
-template <typename Out, typename S>
+// large tiles, and small ones where these fill the chip better
+template <typename Out>
 __global__ __launch_bounds__(kTileWaves * 64, 2) void mxfp4_kernel(Mxfp4Args a) {
-    __shared__ __attribute__((aligned(128))) uint8_t lds[S::kBytes];
-    const uint32_t tiles_p = (a.n + S::BP - 1) / S::BP, t = (uint32_t)xcd_tile();
-    const GroupTile w = find_tile(a.counts, a.groups, a.rows, S::BQ, t / tiles_p);
-    if (w.rows != 0) tile<Out, S>(a, w.group, w.row, w.rows, t % tiles_p * S::BP, lds);
+    __shared__ __attribute__((aligned(128))) uint8_t lds[Large::kBytes > Small::kBytes ? Large::kBytes : Small::kBytes];
+    Share s;
+    if (!find_share<Large, Small>(a.counts, a.groups, a.rows, a.n, &s)) return;
+    if (s.large) {
+        tile<Out, Large>(a, s.w.group, s.w.row, s.w.rows, s.p0, lds);
+        return;
+    }
+    for (uint32_t p = s.p0; p < s.p1; p += Small::BP) {
+        tile<Out, Small>(a, s.w.group, s.w.row, s.w.rows, p, lds);
+        __syncthreads();  // LDS may be written again
+    }
 }
 
-// Tiles of T rows that any counts can make of `rows` rows in `groups` groups and the rows past them.
-uint64_t most_tiles(const Mxfp4Args& a, uint32_t T) { return (a.rows + (uint64_t)T - 1) / T + (a.counts ? a.groups : 0); }
-
-template <typename Out, typename S>
+template <typename Out>
 hipError_t launch_tiled(const Mxfp4Args& a, hipStream_t stream) {
-    const uint64_t wgs = most_tiles(a, S::BQ) * ((a.n + (uint64_t)S::BP - 1) / S::BP);
+    const uint64_t tiles_p = (a.n + (uint64_t)Large::BP - 1) / Large::BP;
+    const uint64_t wgs = shares<Large, Small>(most_tiles(a.counts, a.groups, a.rows, Large::BQ) * tiles_p);
     if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
-    return enqueue(mxfp4_kernel<Out, S>, dim3((uint32_t)wgs), dim3(kTileWaves * 64), stream, a);
+    return enqueue(mxfp4_kernel<Out>, dim3((uint32_t)wgs), dim3(kTileWaves * 64), stream, a);
 }
 
 }  // namespace
@@ -135,7 +141,7 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, siz
 hipError_t launch_gemm_mxfp4(const uint8_t* x, const uint8_t* xs, size_t rows, size_t k, const uint8_t* w, const uint8_t* ws, size_t n,
                              int groups, const int32_t* counts, void* out, int out_bf16, hipStream_t stream) {
     const Mxfp4Args a{x, xs, w, ws, counts, out, (uint32_t)groups, (uint32_t)rows, (uint32_t)n, (uint32_t)k};
-    return out_bf16 ? launch_tiled<uint16_t, Small>(a, stream) : launch_tiled<float, Small>(a, stream);
+    return out_bf16 ? launch_tiled<uint16_t>(a, stream) : launch_tiled<float>(a, stream);
 }
 
 }  // namespace lpc

@@ -62,9 +62,9 @@ size_t plan_size(size_t chunks, size_t tensors) {
     return lpc::adamw_chunk_bytes(chunks) + tensors * sizeof(lpc_adamw_tensor);
 }
 
-// groups x rows of a grouped product with one weight [n, k] per group
+// a grouped product of rows [rows, k] with one weight [n, k] per group
 bool bad_product(size_t rows, size_t n, size_t k, int groups) {
-    return bad_groups(groups) || too_many(rows, k) || too_many(n, k) || too_many(rows, n) || n * k > LPC_MAX_MATRIX / (size_t)groups;
+    return n >= LPC_MAX_ROW || k >= LPC_MAX_ROW || bad_groups(groups) || too_many(rows, k) || too_many(n, k) || too_many(rows, n) || n * k > LPC_MAX_MATRIX / (size_t)groups;
 }
 
 // pieces of a matrix optimizer's plan, of each kind

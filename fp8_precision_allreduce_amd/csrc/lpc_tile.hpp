@@ -48,6 +48,7 @@ struct Fragment {
 
 struct MmaBf16 {
     static constexpr bool kScaled = false;
+    template <int H>
     static __device__ __forceinline__ f32x4_t mul(i32x4_t p, i32x4_t q, f32x4_t c, int, int) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, p), __builtin_bit_cast(bf16x8_t, q), c, 0, 0, 0);
     }
@@ -55,18 +56,26 @@ struct MmaBf16 {
 
 struct MmaF16 {
     static constexpr bool kScaled = false;
+    template <int H>
     static __device__ __forceinline__ f32x4_t mul(i32x4_t p, i32x4_t q, f32x4_t c, int, int) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, p), __builtin_bit_cast(f16x8_t, q), c, 0, 0, 0);
     }
 };
 
-// E2M1 codes; ps, qs: the exponent byte of the lane's 32 codes in the low bits
+// E2M1 codes; ps, qs: the exponent bytes of the lane's 32 codes of half H in byte H.  In assembly, as the compiler keeps the
+// accumulators of the scaled instruction in other registers than it adds to, and then has not enough of them (it put 60 into
+// memory, and the product took 1.8 times as long).  It does not know then that a result is not there at once: wait() is
+// between the last of these instructions and whatever else touches a result.
 struct MmaMxfp4 {
     static constexpr bool kScaled = true;
+    static __device__ __forceinline__ void wait() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }  // 24 states; the instruction takes up to 20
+    template <int H>
     static __device__ __forceinline__ f32x4_t mul(i32x4_t p, i32x4_t q, f32x4_t c, int ps, int qs) {
-        const i32x8_t a = __builtin_shufflevector(p, p, 0, 1, 2, 3, -1, -1, -1, -1);
-        const i32x8_t b = __builtin_shufflevector(q, q, 0, 1, 2, 3, -1, -1, -1, -1);
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, ps, 0, qs);
+        if constexpr (H == 0)
+            asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4" : "+v"(c) : "v"(p), "v"(q), "v"(ps), "v"(qs));
+        else
+            asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4" : "+v"(c) : "v"(p), "v"(q), "v"(ps), "v"(qs));
+        return c;
     }
 };
 
@@ -78,7 +87,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
-// 16 (4) bytes a lane from base + off, or from an address of its own, to LDS at `to` + 16 (4) lane.  The compiler does not
+// 16 (4) bytes a lane from base + off to LDS at `to` + 16 (4) lane.  The compiler does not
 // count these loads: lds_arrived() waits until at most `Left` of them are on their way.  M0 is read one wait state after it
 // is written, and is named as overwritten, so that no use of it by the compiler is carried across (the warning says that it
 // is not saved either).
@@ -87,11 +96,8 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 __device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "m0");
 }
-__device__ __forceinline__ void load_lds16_at(const void* from, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "m0");
-}
-__device__ __forceinline__ void load_lds4_at(const void* from, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "m0");
+__device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base) : "m0");
 }
 #pragma clang diagnostic pop
 template <int Left>
@@ -99,9 +105,6 @@ __device__ __forceinline__ void lds_arrived() {
     static_assert(Left < 64, "what the wait instruction can count");
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Left) : "memory");
 }
-
-// what lies past the end of the contraction
-__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
 // ---------------------------------------------------------------------------
 // operands
@@ -121,49 +124,72 @@ __device__ __forceinline__ size_t scalar(size_t v) { return (size_t)scalar((uint
 __device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) { return reinterpret_cast<const uint8_t*>(scalar((size_t)p)); }
 __device__ __forceinline__ Operand scalar(const Operand& o) { return {scalar(o.base), scalar(o.ld), scalar(o.n), scalar(o.scale)}; }
 
-// A lane's part of the loads of one operand: load i brings, along, rows 8 i' + lane/8 (i' = i Waves + wave: rows past the last
-// repeat it, and their sums are not stored); across, columns 64 i .. + 63 of contraction rows 8 wave + lane/8 (here the
-// wavefronts that share a stage are 8, or one that does all 8 parts by itself).
+// The last slab may be short: `count` contraction indices of 16 bits (of 4 bits: a quarter of the indices).
+// Loads past its end repeat what is at the end, so that nothing outside of the tile's rows is read, and the fragments of P are
+// zeros there.
+struct Contraction {
+    uint32_t slabs, count;  // count in 1..64
+};
+
+// of `length` 16-bit indices
+__device__ __forceinline__ Contraction contraction(uint32_t length) {
+    const uint32_t slabs = (length + kSlabRows - 1) / kSlabRows;
+    return {slabs, length - (slabs - 1) * kSlabRows};
+}
+
+// The loads of one operand: load i brings, along, rows 64 i + 8 wave + lane/8 (rows past the last repeat it, and their sums are
+// not stored); across, columns 64 i .. + 63 of contraction rows 8 wave + lane/8.  A load's first row is found in 64 bits, so
+// that a lane's offset is that of 8 rows, below 32 bits for rows of less than 2^29 bytes.
 //
 // LDS keeps a run of 128 bytes in 8 pieces of 16.  Along, piece c of row r is at place c ^ (r % 8): the 16 lanes that read
 // a fragment together then use all banks.  Across, lanes read 8 bytes of each of 8 rows of one parity at a time, so pairs of
 // pieces are moved: piece c of row r is at place c ^ 2 f(r), f(r) = bits 1 and 3 of r, which differ among those 8 rows.  An
 // asynchronous load writes lane after lane, so the places are made by the addresses it reads.
-template <int F>
-__device__ __forceinline__ uint32_t piece_of_lane(uint32_t lane, uint32_t part) {
-    const uint32_t lr = lane >> 3;
-    if constexpr (F == kAlong) return ((lane & 7) ^ lr) * 16;
-    else return ((lane & 7) ^ (2 * ((lr >> 1 & 1) + 2 * (part & 1)))) * 16;
-}
+template <int F, int N>
+struct Loads {
+    const uint8_t* from[N];  // the same for the wavefront
+    uint32_t off[N];
+    size_t step, back;       // bytes from slab to slab; how far the last slab's loads start before what `from` says
+    uint32_t less;           // and how much less a lane's offset is there
 
-// the offset of a lane's 16 bytes from the slab's start; row: along, the row; across, the contraction row; col: across, byte
-// of the column block
-template <int F, typename T>
-__device__ __forceinline__ T lane_offset(const Operand& o, uint32_t row, uint32_t col, uint32_t piece) {
-    if constexpr (F == kAlong) return (T)min(row, o.n - 1) * (T)o.ld + piece;
-    else return (T)row * (T)o.ld + min(col + piece, (o.n - 8) * 2);
-}
+    __device__ __forceinline__ Loads(const Operand& o, const Contraction& k, uint32_t wave, uint32_t lane) {
+        const uint32_t lr = lane >> 3, ld = (uint32_t)o.ld;
+        if constexpr (F == kAlong) {
+            const uint32_t piece = ((lane & 7) ^ lr) * 16, end = (2 * k.count - 1) / 16 * 16;
+            step = kSlab;
+            back = 0;
+            less = piece - min(piece, end);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t row = min(64 * i + 8 * wave, o.n - 1);
+                from[i] = o.base + row * o.ld;
+                off[i] = min(lr, o.n - 1 - row) * ld + piece;
+            }
+        } else {
+            const uint32_t piece = ((lane & 7) ^ (2 * ((lr >> 1 & 1) + 2 * (wave & 1)))) * 16;
+            const uint32_t row = min(8 * wave, k.count - 1);
+            step = kSlabRows * o.ld;
+            back = (8 * wave - row) * o.ld;
+            less = (lr - min(lr, k.count - 1 - row)) * ld;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                from[i] = o.base + 8 * wave * o.ld;
+                off[i] = lr * ld + min(i * kSlab + piece, (o.n - 8) * 2);
+            }
+        }
+    }
 
-template <int F>
-__device__ __forceinline__ size_t slab_step(const Operand& o) {
-    return F == kAlong ? kSlab : kSlabRows * o.ld;
-}
+    // Sums of products come as register pairs, whose other half is let go of here.
+    __device__ __forceinline__ void settle() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm volatile("" : "+v"(off[i]));
+        asm volatile("" : "+v"(less));
+    }
 
-// The last slab may be short: `tail` bytes along (a multiple of 16), contraction rows across.
-struct Tail {
-    uint32_t bytes, rows;
+    __device__ __forceinline__ void load(int i, uint32_t slab, bool last, uint32_t to) const {
+        load_lds16(from[i] + slab * step - (last ? back : 0), off[i] - (last ? less : 0), to);
+    }
 };
-
-template <int F>
-__device__ __forceinline__ void load_checked(const Operand& o, uint32_t slab, bool last, const Tail& t, uint32_t row, uint32_t col,
-                                             uint32_t piece, uint32_t to) {
-    const bool in = !last || (F == kAlong ? piece < t.bytes : row < t.rows);
-    const uint8_t* from = o.base + slab * slab_step<F>(o) + lane_offset<F, size_t>(o, row, col, piece);
-    load_lds16_at(in ? from : reinterpret_cast<const uint8_t*>(kZeros), to);
-}
-
-// Offsets within a slab of up to 256 rows are held in 32 bits; longer rows' loads take an address a lane.
-__device__ __forceinline__ bool wide_rows(const Operand& o) { return o.ld >= (1u << 23); }
 
 // ---------------------------------------------------------------------------
 // fragments
@@ -202,6 +228,17 @@ struct Reader {
         return r;
     }
 };
+
+// Zeros from the count-th contraction index of a slab on.
+__device__ __forceinline__ void cut(Fragment& f, uint32_t lane, uint32_t count) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int left = (int)count - (int)(8 * ((lane >> 4) + 4 * h) + 2 * d);  // of the dword's two
+            f.h[h][d] &= left >= 2 ? -1 : left == 1 ? 0xFFFF : 0;
+        }
+}
 
 // ---------------------------------------------------------------------------
 // tiled: one workgroup of 8 wavefronts per BQ x BP outputs; slabs of both operands go to LDS by asynchronous loads, two or
@@ -246,9 +283,9 @@ template <bool Scaled> struct LargeOf : Shape<2, 4, 2, 4, Scaled> {};  // 256 x 
 template <bool Scaled> struct SmallOf : Shape<2, 4, 1, 2, Scaled> {};  // 128 x 128
 
 // Sums of one tile: acc[i][j] holds rows 16 i + lane % 16 and columns 16 j + 4 (lane / 16) .. + 3 of the wavefront's part.
-// `slabs` may be zero.  Ends with every wavefront past its last read of LDS.
+// There may be no slabs.  Ends with every wavefront past its last read of LDS.
 template <typename Mma, int FQ, int FP, typename S>
-__device__ __forceinline__ void tile_sums(const Operand& q_, const Operand& p_, uint32_t slabs_, const Tail& tail_, uint8_t* lds,
+__device__ __forceinline__ void tile_sums(const Operand& q_, const Operand& p_, const Contraction& k_, uint8_t* lds,
                                           f32x4_t (&acc)[S::Phases * S::F][S::PF]) {
     constexpr int WavesQ = S::WavesQ, F = S::F, Phases = S::Phases, PF = S::PF, QW = S::QW, PW = S::PW;
     constexpr uint32_t BQ = S::BQ, BP = S::BP, Stages = S::Stages;
@@ -260,65 +297,57 @@ __device__ __forceinline__ void tile_sums(const Operand& q_, const Operand& p_, 
     for (int i = 0; i < Phases * F; ++i)
 #pragma unroll
         for (int j = 0; j < PF; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const uint32_t slabs = scalar(slabs_);
+    const Contraction k{scalar(k_.slabs), scalar(k_.count)};
+    const uint32_t slabs = k.slabs;
     if (slabs == 0) return;
     const Operand q = scalar(q_), p = scalar(p_);
-    const Tail tail{scalar(tail_.bytes), scalar(tail_.rows)};
 
-    const uint32_t lane = threadIdx.x & 63, lr = lane >> 3;
+    const uint32_t lane = threadIdx.x & 63;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const uint32_t group = wave / 4, wq = wave % WavesQ, wp = wave / WavesQ;
 
-    const uint32_t qpiece = piece_of_lane<FQ>(lane, wave), ppiece = piece_of_lane<FP>(lane, wave);
-    auto qrow = [&](int i) { return (FQ == kAlong ? 64 * i : 0) + 8 * wave + lr; };
-    auto prow = [&](int i) { return (FP == kAlong ? 64 * i : 0) + 8 * wave + lr; };
-    const bool checked = wide_rows(q) || wide_rows(p);
-    uint32_t qoff[QLoads], poff[PLoads];
+    Loads<FQ, QLoads> lq(q, k, wave, lane);
+    Loads<FP, PLoads> lp(p, k, wave, lane);
+    lq.settle();
+    lp.settle();
+    const bool cuts = k.count != kSlabRows;
+    const uint8_t* sbase[SLoads + 1];
+    uint32_t soff[SLoads + 1];
+    if constexpr (Mma::kScaled) {
 #pragma unroll
-    for (int i = 0; i < QLoads; ++i) qoff[i] = lane_offset<FQ, uint32_t>(q, qrow(i), i * kSlab, qpiece);
-#pragma unroll
-    for (int i = 0; i < PLoads; ++i) poff[i] = lane_offset<FP, uint32_t>(p, prow(i), i * kSlab, ppiece);
-    const size_t qstep = slab_step<FQ>(q), pstep = slab_step<FP>(p);
-    const bool short_tail = tail.bytes != kSlab;
+        for (int n = 0; n < SLoads; ++n) {
+            const uint32_t part = n * kTileWaves + wave;  // 32 rows of Q, then of P
+            const bool of_q = part < BQ / 32;
+            const Operand& o = of_q ? q : p;
+            const uint32_t row = (of_q ? part : part - BQ / 32) * 32 + lane / 2;
+            sbase[n] = o.scale;
+            soff[n] = min(row, o.n - 1) * (uint32_t)(o.ld / 16) + (lane & 1) * 4;
+            asm volatile("" : "+v"(soff[n]));
+        }
+    }
 
     // load n of a slab's: the scales, P and the Q of phase 0, then (from kEarly on) the Q of phase 1
     constexpr int kLoads = SLoads + PLoads + QLoads, kEarly = kLoads - (Phases == 1 ? 0 : QLoads / 2);
     auto load_range = [&](int from, int upto, uint32_t c, uint32_t at) {
         const uint32_t to = lds_address(lds) + at * S::kStage;
-        const bool last = c + 1 == slabs && short_tail;
+        const bool last = c + 1 == slabs && cuts;
         if constexpr (Mma::kScaled) {
 #pragma unroll
-            for (int n = 0; n < SLoads; ++n) {
-                if (n < from || n >= upto) continue;
-                const uint32_t part = n * kTileWaves + wave;  // 32 rows of Q, then of P
-                const bool of_q = part < BQ / 32;
-                const Operand& o = of_q ? q : p;
-                const uint32_t row = min((of_q ? part : part - BQ / 32) * 32 + lane / 2, o.n - 1);
-                const uint8_t* at8 = o.scale + row * (o.ld / 16) + c * 8 + (lane & 1) * 4;
-                load_lds4_at(last && (lane & 1) ? reinterpret_cast<const uint8_t*>(kZeros) : at8,
-                             to + (BQ + BP) * kSlab + part * 256);
-            }
+            for (int n = 0; n < SLoads; ++n)
+                // in a short slab the second half's bytes are those of the first once more
+                if (n >= from && n < upto) load_lds4(sbase[n] + c * 8, soff[n] - (last ? (lane & 1) * 4 : 0), to + (BQ + BP) * kSlab + (n * kTileWaves + wave) * 256);
         }
-        auto each = [&](auto load_p, auto load_q) {
 #pragma unroll
-            for (int n = SLoads; n < kLoads; ++n) {
-                if (n < from || n >= upto) continue;
-                if (n < SLoads + PLoads) {
-                    const int i = n - SLoads;
-                    load_p(i, to + BQ * kSlab + i * 8192 + wave * 1024);
-                } else {
-                    const int m = n - SLoads - PLoads;
-                    const int i = Phases == 1 ? m : m < QLoads / 2 ? 2 * m : 2 * (m - QLoads / 2) + 1;
-                    load_q(i, to + i * 8192 + wave * 1024);
-                }
+        for (int n = SLoads; n < kLoads; ++n) {
+            if (n < from || n >= upto) continue;
+            if (n < SLoads + PLoads) {
+                const int i = n - SLoads;
+                lp.load(i, c, last, to + BQ * kSlab + i * 8192 + wave * 1024);
+            } else {
+                const int m = n - SLoads - PLoads;
+                const int i = Phases == 1 ? m : m < QLoads / 2 ? 2 * m : 2 * (m - QLoads / 2) + 1;
+                lq.load(i, c, last, to + i * 8192 + wave * 1024);
             }
-        };
-        if (last || checked) {
-            each([&](int i, uint32_t l) { load_checked<FP>(p, c, last, tail, prow(i), i * kSlab, ppiece, l); },
-                 [&](int i, uint32_t l) { load_checked<FQ>(q, c, last, tail, qrow(i), i * kSlab, qpiece, l); });
-        } else {
-            const uint8_t *pb = p.base + c * pstep, *qb = q.base + c * qstep;
-            each([&](int i, uint32_t l) { load_lds16(pb, poff[i], l); }, [&](int i, uint32_t l) { load_lds16(qb, qoff[i], l); });
         }
     };
     // before the first reads of a part of slab c
@@ -340,31 +369,33 @@ __device__ __forceinline__ void tile_sums(const Operand& q_, const Operand& p_, 
         const uint8_t* s = lds + at * S::kStage;
         const uint32_t after = at + 1 == Stages ? 0 : at + 1, last = Stages == 2 ? after : 3 - at - after;
         Fragment pv[PF];
-        int ps[PF][2] = {};
+        int ps[PF] = {};
 #pragma unroll
         for (int ph = 0; ph < Phases; ++ph) {
             Fragment qv[F];
-            int qs[F][2] = {};
-            const uint8_t* sc = s + (BQ + BP) * kSlab + (lane & 15) * 8;
-            const uint32_t shift = (lane >> 4) * 8;  // the byte of the lane's 32 codes
+            int qs[F] = {};
+            // the exponent bytes of the lane's codes, lane / 16 of each half's four, from row r of a stage
+            auto bytes_of = [&](uint32_t r) {
+                const i32x2_t v = *reinterpret_cast<const i32x2_t*>(s + (BQ + BP) * kSlab + (r + (lane & 15)) * 8);
+                return (int)__builtin_amdgcn_perm((uint32_t)v[1], (uint32_t)v[0], (lane >> 4) * 0x0101 + 0x0400);
+            };
             if (ph == 0) {
 #pragma unroll
                 for (int j = 0; j < PF; ++j) {
                     pv[j] = rp.read(s + BQ * kSlab + wp * PW / 64 * 8192, wp * PW / 16 % 4 + j);
-                    if constexpr (Mma::kScaled) {
-                        const i32x2_t v = *reinterpret_cast<const i32x2_t*>(sc + (BQ + wp * PW + 16 * j) * 8);
-                        ps[j][0] = (int)((uint32_t)v[0] >> shift);
-                        ps[j][1] = (int)((uint32_t)v[1] >> shift);
-                    }
+                    if constexpr (Mma::kScaled) ps[j] = bytes_of(BQ + wp * PW + 16 * j);
                 }
             }
 #pragma unroll
             for (int i = 0; i < F; ++i) {
                 qv[i] = rq.read(s + wq * QW / 64 * 8192, ph * F + i);
-                if constexpr (Mma::kScaled) {
-                    const i32x2_t v = *reinterpret_cast<const i32x2_t*>(sc + (wq * QW + 16 * (ph * F + i)) * 8);
-                    qs[i][0] = (int)((uint32_t)v[0] >> shift);
-                    qs[i][1] = (int)((uint32_t)v[1] >> shift);
+                if constexpr (Mma::kScaled) qs[i] = bytes_of(wq * QW + 16 * (ph * F + i));
+            }
+            if (ph == 0 && cuts && b + 1 == slabs) {
+#pragma unroll
+                for (int j = 0; j < PF; ++j) {
+                    if constexpr (Mma::kScaled) pv[j].h[1] = i32x4_t{};  // codes come by 128
+                    else cut(pv[j], lane, k.count);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -377,12 +408,20 @@ __device__ __forceinline__ void tile_sums(const Operand& q_, const Operand& p_, 
             }
             end_slot();
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int n = 0; n < F * PF; ++n) {
+                const int i = n / PF, j = n % PF;
+                acc[ph * F + i][j] = Mma::template mul<0>(pv[j].h[0], qv[i].h[0], acc[ph * F + i][j], ps[j], qs[i]);
+            }
 #pragma unroll
-                for (int i = 0; i < F; ++i)
+            for (int n = 0; n < F * PF; ++n) {
+                const int i = n / PF, j = n % PF;
+                acc[ph * F + i][j] = Mma::template mul<1>(pv[j].h[1], qv[i].h[1], acc[ph * F + i][j], ps[j], qs[i]);
+            }
+            if constexpr (Mma::kScaled) {
+                Mma::wait();
 #pragma unroll
-                    for (int j = 0; j < PF; ++j)
-                        acc[ph * F + i][j] = Mma::mul(pv[j].h[h], qv[i].h[h], acc[ph * F + i][j], ps[j][h], qs[i][h]);
+                for (int n = 0; n < F * PF; ++n) asm volatile("" : "+v"(acc[ph * F + n / PF][n % PF]));
+            }
             if (group == 0) {
                 if (Phases == 2 && ph == 0) arrived(b);
                 else if (b + 1 < slabs) arrived(b + 1);
@@ -426,25 +465,26 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[S::Phases * S::F
     const uint32_t wq = wave % S::WavesQ, wp = wave / S::WavesQ;
     constexpr uint32_t kPer = 16 / sizeof(Out), kLanes = PW / kPer;  // outputs of 16 bytes, lanes of a row
     if (ldo % kPer == 0 && np % kPer == 0) {
-        // 16 F rows at a time through LDS, which is free, so that a store covers whole lines: it costs by the lines it
+        // Rows of some fragments at a time through LDS, which is free, so that a store covers whole lines: it costs by the lines it
         // touches, like a load, and a fragment's rows would be 16 pieces of 32 (16-bit) or 64 bytes.  A wavefront has a
         // part of its own; rows are 16 bytes further apart than they are long, which spreads them over the banks.
         constexpr uint32_t kPitch = PW * sizeof(Out) + 16;
-        static_assert(kTileWaves * 16 * F * kPitch <= S::kBytes, "LDS for the outputs");
-        uint8_t* own = lds + wave * 16 * F * kPitch;
+        constexpr int FS = kTileWaves * 16 * F * kPitch <= S::kBytes ? F : F / 2;
+        static_assert(kTileWaves * 16 * FS * kPitch <= S::kBytes, "LDS for the outputs");
+        uint8_t* own = lds + wave * 16 * FS * kPitch;
 #pragma unroll
-        for (int ph = 0; ph < Phases; ++ph) {
+        for (int f = 0; f < Phases * F; f += FS) {
 #pragma unroll
-            for (int i = 0; i < F; ++i)
+            for (int i = 0; i < FS; ++i)
 #pragma unroll
                 for (int j = 0; j < PF; ++j)
-                    pack4(acc[ph * F + i][j], reinterpret_cast<Out*>(own + (16 * i + l16) * kPitch) + 16 * j + 4 * l4);
+                    pack4(acc[f + i][j], reinterpret_cast<Out*>(own + (16 * i + l16) * kPitch) + 16 * j + 4 * l4);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-            for (uint32_t r = 0; r < 16 * F; r += 64 / kLanes) {
+            for (uint32_t r = 0; r < 16 * FS; r += 64 / kLanes) {
                 const uint32_t row = r + lane / kLanes, col = lane % kLanes;
                 const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + row * kPitch + col * 16);
-                const uint32_t q = wq * QW + ph * 16 * F + row, p = wp * PW + col * kPer;
+                const uint32_t q = wq * QW + f * 16 + row, p = wp * PW + col * kPer;
                 if (q < nq && p < np) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(out + q * ldo + p));
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -460,6 +500,91 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[S::Phases * S::F
             if (q < nq && p < np) store_some(acc[i][j], out + q * ldo + p, np - p);
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// which tile a workgroup takes
+// ---------------------------------------------------------------------------
+
+// Tiles along q that neighbouring workgroups share P with: an XCD's 32 CUs then work on about 6 x 5 tiles, whose operands
+// its L2 serves.
+constexpr uint32_t kBand = 6;
+
+// Tile number t of tiles_q x tiles_p: bands of kBand tiles along q, and in a band tile after tile along p.
+__device__ __forceinline__ uint2 in_bands(uint32_t t, uint32_t tiles_q, uint32_t tiles_p) {
+    const uint32_t band = t / (kBand * tiles_p), in = t - band * kBand * tiles_p;
+    const uint32_t high = min(kBand, tiles_q - band * kBand), tp = in / high;
+    return make_uint2(band * kBand + in - tp * high, tp);
+}
+
+// A large tile's workgroup has a CU to itself, and each XCD works through its own run of tiles, 32 at a time.  Where a last
+// round would leave half of the CUs or more without a tile, its tiles are split into parts of the small size.  How many tiles
+// the counts make is known here and not on the host.
+constexpr uint32_t kXcds = 8, kXcdCus = 32, kMostSplit = kXcdCus / 2;
+
+// Rows [w.row, + w.rows) of a group and outputs [p0, p1) for one workgroup: as one tile of the large shape, or as small tiles.
+struct Share {
+    GroupTile w;
+    uint32_t p0, p1;
+    bool large;
+};
+
+// false: nothing to do
+template <typename L, typename Small>
+__device__ __forceinline__ bool find_share(const int32_t* counts, uint32_t groups, uint32_t rows, uint32_t outputs_p, Share* s) {
+    constexpr uint32_t PartsP = L::BP / Small::BP, Parts = L::BQ / Small::BQ * PartsP;
+    const TileScan tiles(counts, groups, rows, L::BQ);
+    const uint32_t tiles_q = tiles.all, tiles_p = (outputs_p + L::BP - 1) / L::BP;
+    const uint32_t x = blockIdx.x % kXcds, k = blockIdx.x / kXcds;
+    const uint32_t all = tiles_q * tiles_p, rest = all % kXcds;
+    const uint32_t first = x * (all / kXcds) + min(x, rest), mine = all / kXcds + (x < rest);
+    const uint32_t last = mine % kXcdCus, split = last <= kMostSplit ? last : 0;
+    const uint32_t whole = mine - split;
+    if (k >= whole + split * Parts) return false;
+    const uint32_t n = k < whole ? k : whole + (k - whole) / Parts;
+    const uint2 t = in_bands(first + n, tiles_q, tiles_p);
+    s->w = tiles.find(t.x);
+    s->p0 = t.y * L::BP;
+    s->p1 = min(s->p0 + L::BP, outputs_p);
+    s->large = k < whole && s->w.rows > Small::BQ;
+    if (s->large) return true;
+    // one part, or the upper ones of a tile that has rows for these only: a group's last, or a small group's
+    const uint32_t part = k < whole ? 0 : (k - whole) % Parts, q = part / PartsP * Small::BQ;
+    if (q >= s->w.rows) return false;
+    s->w.row += q;
+    s->w.rows = min(s->w.rows - q, Small::BQ);
+    if (k >= whole) {
+        s->p0 += part % PartsP * Small::BP;
+        s->p1 = min(s->p0 + Small::BP, outputs_p);
+    }
+    return s->p0 < s->p1;
+}
+
+// workgroups that cover what any counts make of `most_tiles` tiles: up to kMostSplit tiles of every XCD are split
+template <typename L, typename Small>
+uint64_t shares(uint64_t most_tiles) {
+    constexpr uint64_t Parts = (L::BQ / Small::BQ) * (L::BP / Small::BP);
+    return kXcds * ((most_tiles + kXcds - 1) / kXcds + kMostSplit * (Parts - 1));
+}
+
+// Tiles of T rows that any counts can make of `rows` rows in `groups` groups and the rows past them: every group and the
+// rest may end in a short tile.
+inline uint64_t most_tiles(const int32_t* counts, uint32_t groups, uint32_t rows, uint32_t T) {
+    return (rows + (uint64_t)T - 1) / T + (counts ? groups : 0);
+}
+
+// The group with the z-th most rows, for up to 64 groups: their tiles take times that differ as their rows do, and the
+// long ones come first, so that short ones fill the end.
+__device__ __forceinline__ GroupTile group_by_rows(const int32_t* counts, uint32_t groups, uint32_t rows, uint32_t z) {
+    if (groups > 64) return find_group(counts, groups, rows, 1, z);
+    const GroupScan s(counts, groups, rows, 1, 0, 0, 0);
+    const uint32_t lane = threadIdx.x & 63, mine = s.end - s.begin;
+    uint32_t rank = 0;
+    for (uint32_t g = 0; g < groups; ++g) {
+        const uint32_t other = from_lane(mine, g);
+        rank += other > mine || (other == mine && g < lane);
+    }
+    return group_of_lane(s, 0, (uint32_t)__builtin_ctzll(__ballot(lane < groups && rank == z)));
 }
 
 }  // namespace

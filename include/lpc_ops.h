@@ -42,6 +42,7 @@ extern "C" {
 #define LPC_MAX_GROUPS 1024    /* weights of one grouped product */
 #define LPC_MAX_EXPERTS 1024   /* experts of one router */
 #define LPC_MAX_TOPK 16        /* experts a row is sent to */
+#define LPC_MAX_ROW ((size_t)1 << 28)      /* n and k of bf16 and MXFP4 products are below this */
 #define LPC_MAX_MATRIX ((size_t)1 << 40)   /* elements of one matrix operand */
 
 /* ---------------------------------------------------------------------- */
@@ -232,9 +233,9 @@ lpc_status lpc_adamw_step(const void *plan, size_t chunks, lpc_dtype grad_t, int
  *   counts as for lpc_gemm_fp8: group g's rows follow group g-1's, a negative
  *      count is taken as 0, groups end at `rows`, rows past the last group give
  *      zeros; may be NULL when groups == 1
- *   k a positive multiple of 8; any n; rows, k, n < 2^31, groups in
- *   1..LPC_MAX_GROUPS, each matrix at most LPC_MAX_MATRIX elements (else
- *   LPC_ERR_SHAPE).  rows == 0 or n == 0: LPC_OK, no work.                   */
+ *   k a positive multiple of 8; any n; k, n < LPC_MAX_ROW, rows < 2^31,
+ *   groups in 1..LPC_MAX_GROUPS, each matrix at most LPC_MAX_MATRIX elements
+ *   (else LPC_ERR_SHAPE).  rows == 0 or n == 0: LPC_OK, no work.             */
 lpc_status lpc_gemm_bf16(const uint16_t *x, size_t rows, size_t k,
                          const uint16_t *w, size_t n, int groups, const int32_t *counts,
                          void *out, lpc_dtype out_t, hipStream_t stream);
