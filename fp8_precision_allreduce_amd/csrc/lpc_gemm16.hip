@@ -50,7 +50,7 @@ __device__ __forceinline__ void tile(const Gemm16Args& a, uint32_t g, uint32_t q
         q = operand(a.q + (size_t)r0 * a.n + q0, a.n, nq);
         p = operand(a.p + (size_t)r0 * a.k + p0, a.k, np);
     }
-    f32x4_t acc[S::Phases * S::F][S::PF];
+    f32x4_t acc[S::AQ][S::AP];
     tile_sums<MmaBf16, kFormQ<M>, kFormP<M>, S>(q, p, contraction(length), lds, acc);
     const uint32_t ldo = outputs_p<M>(a);
     Out* out = static_cast<Out*>(a.out) + (M == kWgrad ? matrix : 0) + (size_t)q0 * ldo + p0;

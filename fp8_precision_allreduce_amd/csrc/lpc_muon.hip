@@ -159,15 +159,15 @@ struct Place {
 template <typename S>
 __device__ __forceinline__ Place place_of(int i, int j) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    return {wave % S::WavesQ * S::QW + 16 * i + (lane & 15), wave / S::WavesQ * S::PW + 16 * j + 4 * (lane >> 4)};
+    return {S::q0(wave) + 16 * i + (lane & 15), S::p0(wave) + 16 * j + 4 * (lane >> 4)};
 }
 
 template <typename F>
-__device__ __forceinline__ void each_place(f32x4_t (&acc)[Tile::Phases * Tile::F][Tile::PF], F f) {
+__device__ __forceinline__ void each_place(f32x4_t (&acc)[Tile::AQ][Tile::AP], F f) {
 #pragma unroll
-    for (int i = 0; i < Tile::Phases * Tile::F; ++i)
+    for (int i = 0; i < Tile::AQ; ++i)
 #pragma unroll
-        for (int j = 0; j < Tile::PF; ++j) {
+        for (int j = 0; j < Tile::AP; ++j) {
             const Place at = place_of<Tile>(i, j);
             f(acc[i][j], at.q, at.p);
         }
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_square_kernel(MuonPla
     const uint32_t s = min(x.rows, x.cols), tiles = (s + Tile::BP - 1) / Tile::BP;
     const uint32_t q0 = piece.index / tiles * Tile::BQ, p0 = piece.index % tiles * Tile::BP;
     const uint32_t nq = min(Tile::BQ, s - q0), np = min(Tile::BP, s - p0);
-    f32x4_t acc[Tile::Phases * Tile::F][Tile::PF];
+    f32x4_t acc[Tile::AQ][Tile::AP];
     if (Second) {
         tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(w.a + (size_t)q0 * x.lda, x.lda, nq), operand(w.a + (size_t)p0 * x.lda, x.lda, np),
                                                 contraction(s), lds, acc);
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPla
     const uint32_t q0 = piece.index / tiles * Tile::BQ, p0 = piece.index % tiles * Tile::BP;
     const uint32_t nq = min(Tile::BQ, x.rows - q0), np = min(Tile::BP, x.cols - p0);
     const _Float16* high = w.high[from];
-    f32x4_t acc[Tile::Phases * Tile::F][Tile::PF];
+    f32x4_t acc[Tile::AQ][Tile::AP];
     if (x.rows > x.cols) {
         tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(high + (size_t)q0 * x.ldx, x.ldx, nq), operand(w.b + (size_t)p0 * x.lda, x.lda, np), contraction(x.cols), lds, acc);
     } else {

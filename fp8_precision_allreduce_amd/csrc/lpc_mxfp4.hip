@@ -91,7 +91,7 @@ __device__ __forceinline__ void tile(const Mxfp4Args& a, uint32_t g, uint32_t q0
     const size_t first = (size_t)(g == a.groups ? 0 : g) * a.n + p0;
     const Operand q{a.x + (size_t)q0 * row, row, nq, a.xs + (size_t)q0 * scale_row};
     const Operand p{a.w + first * row, row, np, a.ws + first * scale_row};
-    f32x4_t acc[S::Phases * S::F][S::PF];
+    f32x4_t acc[S::AQ][S::AP];
     tile_sums<MmaMxfp4, kAlong, kAlong, S>(q, p, contraction(g == a.groups ? 0 : row / 2), lds, acc);
     store_tile<Out, S>(acc, static_cast<Out*>(a.out) + (size_t)q0 * a.n + p0, a.n, nq, np, lds);
 }

@@ -241,20 +241,18 @@ __device__ __forceinline__ void cut(Fragment& f, uint32_t lane, uint32_t count) 
 }
 
 // ---------------------------------------------------------------------------
-// tiled: one workgroup of 8 wavefronts per BQ x BP outputs; slabs of both operands go to LDS by asynchronous loads, two or
-// three stages deep; a wavefront owns 16 F Phases x 16 PF outputs.
+// tiles: one workgroup of 8 wavefronts per BQ x BP outputs; slabs of both operands go to LDS by asynchronous loads, two or
+// four stages deep.
 //
 // The wavefronts form two groups, one of each on every SIMD, that take turns: in every slot between two barriers one group
-// reads its fragments of a phase from LDS while the other multiplies, and then they change over.
-//   slot           0     1     2     3    ...         (Phases == 1)
-//   group 0      read0 mult0 read1 mult1
+// reads its fragments from LDS while the other multiplies, and then they change over.
+//   large, slot    0     1     2     3    ...
+//   group 0      read0 mult0 read1 mult1          phases of 64 of a wavefront's 128 rows
 //   group 1        -   read0 mult0 read1
 // Loads of a part of LDS start in the reading slot after its last reads by either group, and are waited for, by every
-// wavefront for its own, in the slot before its first:
-//   Phases == 2, two stages   P, scales and the Q of phase 0 of slab c start in slot 4 c - 6 (group 1: - 5) and arrive
-//                   before 4 c, the Q of phase 1 from 4 c - 4 (- 3) to 4 c + 2
-//   Phases == 1, three stages  everything from slot 2 c - 4 (- 3) to 2 c
-// In both a wavefront waits until only one slab's worth of loads is on its way.
+// wavefront for its own, in the slot before its first: P, scales and the Q of phase 0 of slab c start in slot 4 c - 6 (group 1:
+// - 5) and arrive before 4 c, the Q of phase 1 from 4 c - 4 (- 3) to 4 c + 2.  A wavefront waits until only one slab's worth of
+// loads is on its way.
 // ---------------------------------------------------------------------------
 
 constexpr int kTileWaves = 8;
@@ -266,171 +264,275 @@ __device__ __forceinline__ void end_slot() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Shape of a tile: WavesQ wavefronts along q, each with 16 F Phases x 16 PF outputs.
-template <int WQ, int F_, int Phases_, int PF_, bool Scaled>
-struct Shape {
-    static constexpr int WavesQ = WQ, WavesP = kTileWaves / WQ, F = F_, Phases = Phases_, PF = PF_;
-    static constexpr int QW = 16 * F * Phases, PW = 16 * PF;
-    static constexpr uint32_t BQ = WavesQ * QW, BP = WavesP * PW, Stages = Phases == 1 ? 3 : 2;
+// Large: two wavefronts along q and four along p, each with 128 x 64 outputs in two phases of 64 x 64.
+template <bool Scaled>
+struct LargeOf {
+    static constexpr int WavesQ = 2, F = 4, Phases = 2, PF = 4, AQ = F * Phases, AP = PF;  // fragments of 16 x 16
+    static constexpr uint32_t QW = 128, PW = 64, BQ = 256, BP = 256, Stages = 2;
     static constexpr uint32_t kScaleBytes = Scaled ? 8 * (BQ + BP) : 0;  // 8 exponent bytes a row and slab
     static constexpr uint32_t kStage = (BQ + BP) * kSlab + kScaleBytes;
-    static constexpr size_t kBytes = Stages * kStage;
-    static constexpr bool kScaled = Scaled;
-    static_assert(BQ % 64 == 0 && BP % 64 == 0, "loads of 64 rows");
-    static_assert(Phases == 1 || QW == 128, "loads of 64 rows: even ones are phase 0, odd ones phase 1");
+    static constexpr uint32_t kBytes = Stages * kStage;
+    static constexpr bool kScaled = Scaled, kPair = false;
+    static __device__ __forceinline__ uint32_t q0(uint32_t wave) { return wave % 2 * QW; }
+    static __device__ __forceinline__ uint32_t p0(uint32_t wave) { return wave / 2 * PW; }
 };
-template <bool Scaled> struct LargeOf : Shape<2, 4, 2, 4, Scaled> {};  // 256 x 256
-template <bool Scaled> struct SmallOf : Shape<2, 4, 1, 2, Scaled> {};  // 128 x 128
 
-// Sums of one tile: acc[i][j] holds rows 16 i + lane % 16 and columns 16 j + 4 (lane / 16) .. + 3 of the wavefront's part.
-// There may be no slabs.  Ends with every wavefront past its last read of LDS.
-template <typename Mma, int FQ, int FP, typename S>
-__device__ __forceinline__ void tile_sums(const Operand& q_, const Operand& p_, const Contraction& k_, uint8_t* lds,
-                                          f32x4_t (&acc)[S::Phases * S::F][S::PF]) {
-    constexpr int WavesQ = S::WavesQ, F = S::F, Phases = S::Phases, PF = S::PF, QW = S::QW, PW = S::PW;
-    constexpr uint32_t BQ = S::BQ, BP = S::BP, Stages = S::Stages;
-    constexpr int QLoads = BQ / 64, PLoads = BP / 64;
+// Small: 128 x 128 by each of the two groups, which take the slabs in turn and add up at the end; a wavefront multiplies 64 x 64
+// outputs and ends with 32 x 64 of the sums.
+template <bool Scaled>
+struct SmallOf {
+    static constexpr int F = 4, PF = 4, AQ = 2, AP = 4;
+    static constexpr uint32_t QW = 32, PW = 64, BQ = 128, BP = 128, Stages = 4;
+    static constexpr uint32_t kScaleBytes = Scaled ? 8 * (BQ + BP) : 0;
+    static constexpr uint32_t kStage = (BQ + BP) * kSlab + kScaleBytes;
+    static constexpr uint32_t kBytes = Stages * kStage;
+    static constexpr bool kScaled = Scaled, kPair = true;
+    static __device__ __forceinline__ uint32_t q0(uint32_t wave) { return wave % 2 * 64 + wave / 4 * QW; }
+    static __device__ __forceinline__ uint32_t p0(uint32_t wave) { return wave % 4 / 2 * PW; }
+};
+
+// A workgroup's loads of the slabs of both operands.
+template <typename S, int FQ, int FP>
+struct SlabLoads {
+    static constexpr int QLoads = S::BQ / 64, PLoads = S::BP / 64;
     // exponent bytes: 2 lanes a row, 32 rows a load; a wavefront does SLoads of the (BQ + BP) / 32
-    constexpr int SLoads = Mma::kScaled ? (BQ + BP) / 32 / kTileWaves : 0;
-    static_assert(Mma::kScaled == S::kScaled && (!Mma::kScaled || (FQ == kAlong && FP == kAlong)), "scales lie along");
-#pragma unroll
-    for (int i = 0; i < Phases * F; ++i)
-#pragma unroll
-        for (int j = 0; j < PF; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const Contraction k{scalar(k_.slabs), scalar(k_.count)};
-    const uint32_t slabs = k.slabs;
-    if (slabs == 0) return;
-    const Operand q = scalar(q_), p = scalar(p_);
-
-    const uint32_t lane = threadIdx.x & 63;
-    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const uint32_t group = wave / 4, wq = wave % WavesQ, wp = wave / WavesQ;
-
-    Loads<FQ, QLoads> lq(q, k, wave, lane);
-    Loads<FP, PLoads> lp(p, k, wave, lane);
-    lq.settle();
-    lp.settle();
-    const bool cuts = k.count != kSlabRows;
+    static constexpr int SLoads = S::kScaled ? (S::BQ + S::BP) / 32 / kTileWaves : 0;
+    static constexpr int kLoads = SLoads + PLoads + QLoads;
+    Loads<FQ, QLoads> q;
+    Loads<FP, PLoads> p;
     const uint8_t* sbase[SLoads + 1];
     uint32_t soff[SLoads + 1];
-    if constexpr (Mma::kScaled) {
+    uint32_t slabs, wave, lane;
+    bool cuts;
+
+    __device__ __forceinline__ SlabLoads(const Operand& oq, const Operand& op, const Contraction& k, uint32_t w, uint32_t l)
+        : q(oq, k, w, l), p(op, k, w, l), slabs(k.slabs), wave(w), lane(l), cuts(k.count != kSlabRows) {
+        q.settle();
+        p.settle();
 #pragma unroll
         for (int n = 0; n < SLoads; ++n) {
             const uint32_t part = n * kTileWaves + wave;  // 32 rows of Q, then of P
-            const bool of_q = part < BQ / 32;
-            const Operand& o = of_q ? q : p;
-            const uint32_t row = (of_q ? part : part - BQ / 32) * 32 + lane / 2;
+            const bool of_q = part < S::BQ / 32;
+            const Operand& o = of_q ? oq : op;
+            const uint32_t row = (of_q ? part : part - S::BQ / 32) * 32 + lane / 2;
             sbase[n] = o.scale;
             soff[n] = min(row, o.n - 1) * (uint32_t)(o.ld / 16) + (lane & 1) * 4;
             asm volatile("" : "+v"(soff[n]));
         }
     }
 
-    // load n of a slab's: the scales, P and the Q of phase 0, then (from kEarly on) the Q of phase 1
-    constexpr int kLoads = SLoads + PLoads + QLoads, kEarly = kLoads - (Phases == 1 ? 0 : QLoads / 2);
-    auto load_range = [&](int from, int upto, uint32_t c, uint32_t at) {
-        const uint32_t to = lds_address(lds) + at * S::kStage;
+    // load n of slab c: exponent bytes, P, the even loads of Q, the odd ones
+    __device__ __forceinline__ void load(int n, uint32_t c, uint32_t to) const {
         const bool last = c + 1 == slabs && cuts;
-        if constexpr (Mma::kScaled) {
-#pragma unroll
-            for (int n = 0; n < SLoads; ++n)
-                // in a short slab the second half's bytes are those of the first once more
-                if (n >= from && n < upto) load_lds4(sbase[n] + c * 8, soff[n] - (last ? (lane & 1) * 4 : 0), to + (BQ + BP) * kSlab + (n * kTileWaves + wave) * 256);
+        if (n < SLoads) {
+            // in a short slab the second half's bytes are those of the first once more
+            load_lds4(sbase[n] + c * 8, soff[n] - (last ? (lane & 1) * 4 : 0), to + (S::BQ + S::BP) * kSlab + (n * kTileWaves + wave) * 256);
+        } else if (n < SLoads + PLoads) {
+            const int i = n - SLoads;
+            p.load(i, c, last, to + S::BQ * kSlab + i * 8192 + wave * 1024);
+        } else {
+            const int m = n - SLoads - PLoads, i = m < QLoads / 2 ? 2 * m : 2 * (m - QLoads / 2) + 1;
+            q.load(i, c, last, to + i * 8192 + wave * 1024);
         }
+    }
+    __device__ __forceinline__ void range(int from, int upto, uint32_t c, uint32_t to) const {
 #pragma unroll
-        for (int n = SLoads; n < kLoads; ++n) {
-            if (n < from || n >= upto) continue;
-            if (n < SLoads + PLoads) {
-                const int i = n - SLoads;
-                lp.load(i, c, last, to + BQ * kSlab + i * 8192 + wave * 1024);
-            } else {
-                const int m = n - SLoads - PLoads;
-                const int i = Phases == 1 ? m : m < QLoads / 2 ? 2 * m : 2 * (m - QLoads / 2) + 1;
-                lq.load(i, c, last, to + i * 8192 + wave * 1024);
+        for (int n = 0; n < kLoads; ++n)
+            if (n >= from && n < upto) load(n, c, to);
+    }
+};
+
+// A wavefront's reads of N fragments, f .. f + N - 1 of an operand whose rows (columns) from 64 c on are at `at`.
+template <typename Mma, int F, int N>
+struct Fragments {
+    Fragment f[N];
+    int s[N] = {};
+    __device__ __forceinline__ void read(const Reader<F>& r, const uint8_t* at, uint32_t first, const uint8_t* bytes, uint32_t lane) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            f[i] = r.read(at, first + i);
+            if constexpr (Mma::kScaled) {
+                // the exponent bytes of the lane's codes: of 8 in a row, lane / 16 of each half's four
+                const i32x2_t v = *reinterpret_cast<const i32x2_t*>(bytes + (16 * i + (lane & 15)) * 8);
+                s[i] = (int)__builtin_amdgcn_perm((uint32_t)v[1], (uint32_t)v[0], (lane >> 4) * 0x0101 + 0x0400);
             }
         }
-    };
+    }
+    __device__ __forceinline__ void cut(uint32_t lane, uint32_t count) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (Mma::kScaled) f[i].h[1] = i32x4_t{};  // codes come by 128
+            else lpc::cut(f[i], lane, count);
+        }
+    }
+};
+
+// acc[i][j] += the slab's products
+template <typename Mma, int FQ, int FP, int NQ, int NP>
+__device__ __forceinline__ void multiply(f32x4_t (*acc)[NP], const Fragments<Mma, FQ, NQ>& q, const Fragments<Mma, FP, NP>& p) {
+#pragma unroll
+    for (int n = 0; n < NQ * NP; ++n) {
+        f32x4_t& a = acc[n / NP][n % NP];
+        a = Mma::template mul<0>(p.f[n % NP].h[0], q.f[n / NP].h[0], a, p.s[n % NP], q.s[n / NP]);
+    }
+#pragma unroll
+    for (int n = 0; n < NQ * NP; ++n) {
+        f32x4_t& a = acc[n / NP][n % NP];
+        a = Mma::template mul<1>(p.f[n % NP].h[1], q.f[n / NP].h[1], a, p.s[n % NP], q.s[n / NP]);
+    }
+    if constexpr (Mma::kScaled) {
+        Mma::wait();
+#pragma unroll
+        for (int n = 0; n < NQ * NP; ++n) asm volatile("" : "+v"(acc[n / NP][n % NP]));
+    }
+}
+
+template <int AQ, int AP>
+__device__ __forceinline__ void clear(f32x4_t (&acc)[AQ][AP]) {
+#pragma unroll
+    for (int i = 0; i < AQ; ++i)
+#pragma unroll
+        for (int j = 0; j < AP; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+// There are slabs.
+template <typename Mma, int FQ, int FP, typename S>
+__device__ __forceinline__ void large_sums(const Operand& q, const Operand& p, const Contraction& k, uint8_t* lds, f32x4_t (&acc)[S::AQ][S::AP]) {
+    constexpr uint32_t BQ = S::BQ;
+    const uint32_t lane = threadIdx.x & 63, slabs = k.slabs;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t group = wave / 4, wq = S::q0(wave), wp = S::p0(wave);
+    const SlabLoads<S, FQ, FP> loads(q, p, k, wave, lane);
+    // scales, P and the Q of phase 0 come early, the Q of phase 1 late
+    constexpr int kLoads = loads.kLoads, kEarly = kLoads - loads.QLoads / 2;
+    const uint32_t to[2] = {lds_address(lds), lds_address(lds) + S::kStage};
     // before the first reads of a part of slab c
     auto arrived = [&](uint32_t c) {
         if (c + 1 < slabs) lds_arrived<kLoads>();
         else lds_arrived<0>();
     };
-
-    load_range(0, kLoads, 0, 0);
-    if (slabs > 1) load_range(0, kEarly, 1, 1);
+    loads.range(0, kLoads, 0, to[0]);
+    if (slabs > 1) loads.range(0, kEarly, 1, to[1]);
     if (slabs > 1) lds_arrived<kLoads>();  // what is left: the late ones of slab 0 and the early ones of slab 1
     else lds_arrived<0>();
     end_slot();
     if (group == 1) end_slot();
     const Reader<FQ> rq(lane);
     const Reader<FP> rp(lane);
-    uint32_t at = 0;  // stage of slab b
     for (uint32_t b = 0; b < slabs; ++b) {
+        const uint32_t at = b & 1;
         const uint8_t* s = lds + at * S::kStage;
-        const uint32_t after = at + 1 == Stages ? 0 : at + 1, last = Stages == 2 ? after : 3 - at - after;
-        Fragment pv[PF];
-        int ps[PF] = {};
+        const uint8_t* bytes = s + (BQ + S::BP) * kSlab;
+        Fragments<Mma, FP, S::PF> pv;
 #pragma unroll
-        for (int ph = 0; ph < Phases; ++ph) {
-            Fragment qv[F];
-            int qs[F] = {};
-            // the exponent bytes of the lane's codes, lane / 16 of each half's four, from row r of a stage
-            auto bytes_of = [&](uint32_t r) {
-                const i32x2_t v = *reinterpret_cast<const i32x2_t*>(s + (BQ + BP) * kSlab + (r + (lane & 15)) * 8);
-                return (int)__builtin_amdgcn_perm((uint32_t)v[1], (uint32_t)v[0], (lane >> 4) * 0x0101 + 0x0400);
-            };
+        for (int ph = 0; ph < 2; ++ph) {
+            Fragments<Mma, FQ, S::F> qv;
             if (ph == 0) {
-#pragma unroll
-                for (int j = 0; j < PF; ++j) {
-                    pv[j] = rp.read(s + BQ * kSlab + wp * PW / 64 * 8192, wp * PW / 16 % 4 + j);
-                    if constexpr (Mma::kScaled) ps[j] = bytes_of(BQ + wp * PW + 16 * j);
-                }
+                pv.read(rp, s + BQ * kSlab + wp / 64 * 8192, 0, bytes + (BQ + wp) * 8, lane);
+                if (loads.cuts && b + 1 == slabs) pv.cut(lane, k.count);
             }
-#pragma unroll
-            for (int i = 0; i < F; ++i) {
-                qv[i] = rq.read(s + wq * QW / 64 * 8192, ph * F + i);
-                if constexpr (Mma::kScaled) qs[i] = bytes_of(wq * QW + 16 * (ph * F + i));
-            }
-            if (ph == 0 && cuts && b + 1 == slabs) {
-#pragma unroll
-                for (int j = 0; j < PF; ++j) {
-                    if constexpr (Mma::kScaled) pv[j].h[1] = i32x4_t{};  // codes come by 128
-                    else cut(pv[j], lane, k.count);
-                }
-            }
+            qv.read(rq, s + wq / 64 * 8192, ph * S::F, bytes + (wq + 64 * ph) * 8, lane);
             __builtin_amdgcn_sched_barrier(0);
-            if (Phases == 1 && b + 2 < slabs) load_range(0, kLoads, b + 2, last);
-            if (Phases == 2 && ph == 0 && b + 1 < slabs) load_range(kEarly, kLoads, b + 1, after);
-            if (Phases == 2 && ph == 1 && b + 2 < slabs) load_range(0, kEarly, b + 2, at);
+            if (ph == 0 && b + 1 < slabs) loads.range(kEarly, kLoads, b + 1, to[0] + to[1] - to[at]);
+            if (ph == 1 && b + 2 < slabs) loads.range(0, kEarly, b + 2, to[at]);
             if (group == 1) {
-                if (Phases == 2 && ph == 0) arrived(b);
+                if (ph == 0) arrived(b);
                 else if (b + 1 < slabs) arrived(b + 1);
             }
             end_slot();
-#pragma unroll
-            for (int n = 0; n < F * PF; ++n) {
-                const int i = n / PF, j = n % PF;
-                acc[ph * F + i][j] = Mma::template mul<0>(pv[j].h[0], qv[i].h[0], acc[ph * F + i][j], ps[j], qs[i]);
-            }
-#pragma unroll
-            for (int n = 0; n < F * PF; ++n) {
-                const int i = n / PF, j = n % PF;
-                acc[ph * F + i][j] = Mma::template mul<1>(pv[j].h[1], qv[i].h[1], acc[ph * F + i][j], ps[j], qs[i]);
-            }
-            if constexpr (Mma::kScaled) {
-                Mma::wait();
-#pragma unroll
-                for (int n = 0; n < F * PF; ++n) asm volatile("" : "+v"(acc[ph * F + n / PF][n % PF]));
-            }
+            multiply<Mma>(acc + ph * S::F, qv, pv);
             if (group == 0) {
-                if (Phases == 2 && ph == 0) arrived(b);
+                if (ph == 0) arrived(b);
                 else if (b + 1 < slabs) arrived(b + 1);
             }
             end_slot();
         }
-        at = after;
     }
     if (group == 0) end_slot();
+}
+
+// There are slabs.  In slot c group c % 2 reads slab c while the other multiplies slab c - 1; the loads of slab c + 3 start there, into
+// the stage of slab c - 1, and have arrived before slot c + 3.
+template <typename Mma, int FQ, int FP, typename S>
+__device__ __forceinline__ void small_sums(const Operand& q, const Operand& p, const Contraction& k, uint8_t* lds, f32x4_t (&out)[S::AQ][S::AP]) {
+    constexpr uint32_t BQ = S::BQ;
+    const uint32_t lane = threadIdx.x & 63, slabs = k.slabs;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t group = wave / 4, wq = wave % 2 * 64, wp = wave % 4 / 2 * 64;
+    const SlabLoads<S, FQ, FP> loads(q, p, k, wave, lane);
+    constexpr int kLoads = loads.kLoads;
+    f32x4_t acc[S::F][S::PF];
+    clear(acc);
+    uint32_t into = 0;  // stage of the next slab to load
+    auto load_next = [&](uint32_t c) {
+        if (c < slabs) loads.range(0, kLoads, c, lds_address(lds) + into * S::kStage);
+        into = (into + 1) % S::Stages;
+    };
+    // slab c, where those up to c + 2 have been started
+    auto arrived = [&](uint32_t c) {
+        if (c + 2 < slabs) lds_arrived<2 * kLoads>();
+        else if (c + 1 < slabs) lds_arrived<kLoads>();
+        else lds_arrived<0>();
+    };
+    load_next(0);
+    load_next(1);
+    load_next(2);
+    arrived(0);
+    end_slot();
+    const Reader<FQ> rq(lane);
+    const Reader<FP> rp(lane);
+    auto slot = [&](uint32_t c) {  // the loads of a slot, and what they have to have brought by its end
+        load_next(c + 3);
+        if (c + 1 < slabs) arrived(c + 1);
+    };
+    if (group == 1) {
+        slot(0);
+        end_slot();
+    }
+    for (uint32_t b = group; b < slabs; b += 2) {
+        const uint8_t* s = lds + b % S::Stages * S::kStage;
+        const uint8_t* bytes = s + (BQ + S::BP) * kSlab;
+        Fragments<Mma, FP, S::PF> pv;
+        Fragments<Mma, FQ, S::F> qv;
+        pv.read(rp, s + BQ * kSlab + wp / 64 * 8192, 0, bytes + (BQ + wp) * 8, lane);
+        if (loads.cuts && b + 1 == slabs) pv.cut(lane, k.count);
+        qv.read(rq, s + wq / 64 * 8192, 0, bytes + wq * 8, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        slot(b);
+        end_slot();
+        if (b + 1 < slabs) load_next(b + 4);
+        multiply<Mma>(acc, qv, pv);
+        if (b + 2 < slabs) arrived(b + 2);
+        end_slot();
+    }
+    // slots of both: group 0 is in slot slabs + 1 (slabs even: slabs), group 1 in slabs + 1 - slabs % 2
+    if ((slabs & 1) == group) end_slot();
+    // each group gives the other half of its sums; those of even slabs come first
+    f32x4_t* mine = reinterpret_cast<f32x4_t*>(lds) + wave * (S::AQ * S::AP * 64) + lane;
+    const f32x4_t* other = reinterpret_cast<const f32x4_t*>(lds) + (wave ^ 4) * (S::AQ * S::AP * 64) + lane;
+    static_assert(kTileWaves * S::AQ * S::AP * 64 * 16 <= S::kBytes && S::F == 2 * S::AQ, "LDS for the sums");
+#pragma unroll
+    for (int n = 0; n < S::AQ * S::AP; ++n) mine[n * 64] = group ? acc[n / S::AP][n % S::AP] : acc[S::AQ + n / S::AP][n % S::AP];
+    end_slot();
+#pragma unroll
+    for (int n = 0; n < S::AQ * S::AP; ++n) {
+        const f32x4_t a = acc[n / S::AP][n % S::AP], b = acc[S::AQ + n / S::AP][n % S::AP], o = other[n * 64];
+        out[n / S::AP][n % S::AP] = group ? o + b : a + o;
+    }
+    end_slot();
+}
+
+// Sums of one tile: acc[i][j] holds rows 16 i + lane % 16 and columns 16 j + 4 (lane / 16) .. + 3 of the wavefront's part.
+// There may be no slabs.  Ends with every wavefront past its last use of LDS.
+template <typename Mma, int FQ, int FP, typename S>
+__device__ __forceinline__ void tile_sums(const Operand& q_, const Operand& p_, const Contraction& k_, uint8_t* lds, f32x4_t (&acc)[S::AQ][S::AP]) {
+    static_assert(Mma::kScaled == S::kScaled && (!Mma::kScaled || (FQ == kAlong && FP == kAlong)), "scales lie along");
+    clear(acc);
+    const Contraction k{scalar(k_.slabs), scalar(k_.count)};
+    if (k.slabs == 0) return;
+    const Operand q = scalar(q_), p = scalar(p_);
+    if constexpr (S::kPair) small_sums<Mma, FQ, FP, S>(q, p, k, lds, acc);
+    else large_sums<Mma, FQ, FP, S>(q, p, k, lds, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -457,34 +559,34 @@ __device__ __forceinline__ void store_some(const f32x4_t& v, Out* o, uint32_t le
 // Stores a tile's sums to out (its first row and column), ldo elements between rows, nq x np of them.  After tile_sums by
 // every wavefront of the workgroup; LDS may be written again after a barrier.
 template <typename Out, typename S>
-__device__ __forceinline__ void store_tile(const f32x4_t (&acc)[S::Phases * S::F][S::PF], Out* out, size_t ldo, uint32_t nq, uint32_t np,
+__device__ __forceinline__ void store_tile(const f32x4_t (&acc)[S::AQ][S::AP], Out* out, size_t ldo, uint32_t nq, uint32_t np,
                                            uint8_t* lds) {
-    constexpr int F = S::F, Phases = S::Phases, PF = S::PF, QW = S::QW, PW = S::PW;
+    constexpr int AQ = S::AQ, AP = S::AP, PW = S::PW;
     const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const uint32_t wq = wave % S::WavesQ, wp = wave / S::WavesQ;
+    const uint32_t wq = S::q0(wave), wp = S::p0(wave);
     constexpr uint32_t kPer = 16 / sizeof(Out), kLanes = PW / kPer;  // outputs of 16 bytes, lanes of a row
     if (ldo % kPer == 0 && np % kPer == 0) {
         // Rows of some fragments at a time through LDS, which is free, so that a store covers whole lines: it costs by the lines it
         // touches, like a load, and a fragment's rows would be 16 pieces of 32 (16-bit) or 64 bytes.  A wavefront has a
         // part of its own; rows are 16 bytes further apart than they are long, which spreads them over the banks.
         constexpr uint32_t kPitch = PW * sizeof(Out) + 16;
-        constexpr int FS = kTileWaves * 16 * F * kPitch <= S::kBytes ? F : F / 2;
+        constexpr int FS = AQ < 4 ? AQ : kTileWaves * 64 * kPitch <= S::kBytes ? 4 : 2;
         static_assert(kTileWaves * 16 * FS * kPitch <= S::kBytes, "LDS for the outputs");
         uint8_t* own = lds + wave * 16 * FS * kPitch;
 #pragma unroll
-        for (int f = 0; f < Phases * F; f += FS) {
+        for (int f = 0; f < AQ; f += FS) {
 #pragma unroll
             for (int i = 0; i < FS; ++i)
 #pragma unroll
-                for (int j = 0; j < PF; ++j)
+                for (int j = 0; j < AP; ++j)
                     pack4(acc[f + i][j], reinterpret_cast<Out*>(own + (16 * i + l16) * kPitch) + 16 * j + 4 * l4);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
             for (uint32_t r = 0; r < 16 * FS; r += 64 / kLanes) {
                 const uint32_t row = r + lane / kLanes, col = lane % kLanes;
                 const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + row * kPitch + col * 16);
-                const uint32_t q = wq * QW + f * 16 + row, p = wp * PW + col * kPer;
+                const uint32_t q = wq + f * 16 + row, p = wp + col * kPer;
                 if (q < nq && p < np) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(out + q * ldo + p));
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -492,11 +594,11 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[S::Phases * S::F
         return;
     }
 #pragma unroll
-    for (int i = 0; i < Phases * F; ++i) {
-        const uint32_t q = wq * QW + 16 * i + l16;
+    for (int i = 0; i < AQ; ++i) {
+        const uint32_t q = wq + 16 * i + l16;
 #pragma unroll
-        for (int j = 0; j < PF; ++j) {
-            const uint32_t p = wp * PW + 16 * j + 4 * l4;
+        for (int j = 0; j < AP; ++j) {
+            const uint32_t p = wp + 16 * j + 4 * l4;
             if (q < nq && p < np) store_some(acc[i][j], out + q * ldo + p, np - p);
         }
     }
