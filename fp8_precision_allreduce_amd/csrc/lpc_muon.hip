@@ -145,88 +145,102 @@ __global__ __launch_bounds__(kChunkLanes) void muon_start_kernel(MuonPlan plan, 
 // products
 // ---------------------------------------------------------------------------
 
-using Tile = SmallOf<false>;
-static_assert(Tile::BQ == kMuonTile && Tile::BP == kMuonTile, "tiles as planned");
+using Large = LargeOf<false>;
+using Small = SmallOf<false>;
+static_assert(Large::BQ == kMuonTile && Large::BP == kMuonTile && Small::BQ == Small::BP, "tiles as planned");
 
 __device__ __forceinline__ Operand operand(const _Float16* first, uint32_t ld, uint32_t n) {
     return {reinterpret_cast<const uint8_t*>(first), (size_t)ld * 2, n, nullptr};
 }
 
-// where a lane's four neighbouring elements (i, j) of a tile's sums are: row and first column within the tile
-struct Place {
-    uint32_t q, p;
-};
-template <typename S>
-__device__ __forceinline__ Place place_of(int i, int j) {
+// f(sums, row, column) for each of a lane's four neighbouring elements of a tile
+template <typename S, typename F>
+__device__ __forceinline__ void each_place(f32x4_t (&acc)[S::AQ][S::AP], F f) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    return {S::q0(wave) + 16 * i + (lane & 15), S::p0(wave) + 16 * j + 4 * (lane >> 4)};
-}
-
-template <typename F>
-__device__ __forceinline__ void each_place(f32x4_t (&acc)[Tile::AQ][Tile::AP], F f) {
+    const uint32_t q = S::q0(wave) + (lane & 15), p = S::p0(wave) + 4 * (lane >> 4);
 #pragma unroll
-    for (int i = 0; i < Tile::AQ; ++i)
+    for (int i = 0; i < S::AQ; ++i)
 #pragma unroll
-        for (int j = 0; j < Tile::AP; ++j) {
-            const Place at = place_of<Tile>(i, j);
-            f(acc[i][j], at.q, at.p);
-        }
+        for (int j = 0; j < S::AP; ++j) f(acc[i][j], q + 16 * i, p + 16 * j);
 }
 
 __device__ __forceinline__ f32x4_t halves(const _Float16* p) { return __builtin_convertvector(*reinterpret_cast<const f16x4_t*>(p), f32x4_t); }
 
-// A = X X^T (Second: B = b A + c A A), 128 x 128 of it
-template <bool Second>
-__global__ __launch_bounds__(kTileWaves * 64, 2) void muon_square_kernel(MuonPlan plan, uint8_t* space, uint32_t from) {
-    __shared__ __attribute__((aligned(128))) uint8_t lds[Tile::kBytes];
-    const MuonPiece piece = plan.squares[xcd_tile()];
-    const MuonMatrix& x = plan.matrices[piece.matrix];
-    const Space w = space_of(x, space);
-    const bool tall = x.rows > x.cols;
-    const uint32_t s = min(x.rows, x.cols), tiles = (s + Tile::BP - 1) / Tile::BP;
-    const uint32_t q0 = piece.index / tiles * Tile::BQ, p0 = piece.index % tiles * Tile::BP;
-    const uint32_t nq = min(Tile::BQ, s - q0), np = min(Tile::BP, s - p0);
-    f32x4_t acc[Tile::AQ][Tile::AP];
-    if (Second) {
-        tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(w.a + (size_t)q0 * x.lda, x.lda, nq), operand(w.a + (size_t)p0 * x.lda, x.lda, np),
-                                                contraction(s), lds, acc);
-    } else if (tall) {
-        // columns up to ldx hold zeros, so that pieces of 8 are whole
-        tile_sums<MmaF16, kAcross, kAcross, Tile>(operand(w.high[from] + q0, x.ldx, min(Tile::BQ, x.ldx - q0)),
-                                                  operand(w.high[from] + p0, x.ldx, min(Tile::BP, x.ldx - p0)), contraction(x.rows), lds, acc);
-    } else {
-        tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(w.high[from] + (size_t)q0 * x.ldx, x.ldx, nq),
-                                                operand(w.high[from] + (size_t)p0 * x.ldx, x.ldx, np), contraction(x.cols), lds, acc);
+// Stores a tile's sums with rows and columns exchanged: nq columns, np rows from out on.  Through LDS like store_tile.
+template <typename S>
+__device__ __forceinline__ void store_turned(const f32x4_t (&acc)[S::AQ][S::AP], _Float16* out, size_t ldo, uint32_t nq, uint32_t np, uint8_t* lds) {
+    constexpr int FS = S::AQ < 4 ? S::AQ : 4;
+    constexpr uint32_t kPitch = 16 * FS * 2 + 16, kLanes = 2 * FS;
+    static_assert(kTileWaves * S::PW * kPitch <= S::kBytes, "LDS for the outputs");
+    const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    uint8_t* own = lds + wave * S::PW * kPitch;
+#pragma unroll
+    for (int f = 0; f < S::AQ; f += FS) {
+#pragma unroll
+        for (int i = 0; i < FS; ++i)
+#pragma unroll
+            for (int j = 0; j < S::AP; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<_Float16*>(own + (16 * j + 4 * l4 + e) * kPitch + (16 * i + l16) * 2) = (_Float16)acc[f + i][j][e];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (uint32_t r = 0; r < S::PW; r += 64 / kLanes) {
+            const uint32_t row = r + lane / kLanes, col = lane % kLanes;
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + row * kPitch + col * 16);
+            const uint32_t p = S::p0(wave) + row, q = S::q0(wave) + f * 16 + col * 8;
+            if (q < nq && p < np) *reinterpret_cast<u32x4_t*>(out + p * ldo + q) = v;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-    each_place(acc, [&](f32x4_t& v, uint32_t q, uint32_t p) {
+}
+
+// Rows from q0 and columns from p0 of A = X X^T (Second: of B = b A + c A A).  Both are symmetric: what is below the diagonal
+// is stored above it too.
+template <bool Second, typename S>
+__device__ __forceinline__ void square_tile(const MuonMatrix& x, const Space& w, uint32_t from, uint32_t q0, uint32_t p0, uint8_t* lds) {
+    const uint32_t s = min(x.rows, x.cols), nq = min(S::BQ, s - q0), np = min(S::BP, s - p0);
+    f32x4_t acc[S::AQ][S::AP];
+    if (Second) {
+        tile_sums<MmaF16, kAlong, kAlong, S>(operand(w.a + (size_t)q0 * x.lda, x.lda, nq), operand(w.a + (size_t)p0 * x.lda, x.lda, np),
+                                             contraction(s), lds, acc);
+    } else if (x.rows > x.cols) {
+        // columns up to ldx hold zeros, so that pieces of 8 are whole
+        tile_sums<MmaF16, kAcross, kAcross, S>(operand(w.high[from] + q0, x.ldx, min(S::BQ, x.ldx - q0)),
+                                               operand(w.high[from] + p0, x.ldx, min(S::BP, x.ldx - p0)), contraction(x.rows), lds, acc);
+    } else {
+        tile_sums<MmaF16, kAlong, kAlong, S>(operand(w.high[from] + (size_t)q0 * x.ldx, x.ldx, nq),
+                                             operand(w.high[from] + (size_t)p0 * x.ldx, x.ldx, np), contraction(x.cols), lds, acc);
+    }
+    each_place<S>(acc, [&](f32x4_t& v, uint32_t q, uint32_t p) {
         v = v * (1.0f / kHeld);
         if (Second) v = v * kC + (q < nq && p < np ? halves(w.a + (size_t)(q0 + q) * x.lda + p0 + p) : f32x4_t{}) * kB;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (p + e >= np) v[e] = 0.0f;
+            if (q >= nq || p + e >= np) v[e] = 0.0f;
     });
-    store_tile<_Float16, Tile>(acc, (Second ? w.b : w.a) + (size_t)q0 * x.lda + p0, x.lda, nq, min(Tile::BP, x.lda - p0), lds);
+    _Float16* out = Second ? w.b : w.a;
+    store_tile<_Float16, S>(acc, out + (size_t)q0 * x.lda + p0, x.lda, nq, min(S::BP, x.lda - p0), lds);
+    if (q0 == p0) return;
+    __syncthreads();  // the wavefronts' parts of LDS are others now
+    store_turned<S>(acc, out + (size_t)p0 * x.lda + q0, x.lda, min(S::BQ, x.lda - q0), np, lds);
 }
 
-// X = a X + B X (tall: X B), 128 x 128 of it; Last: the parameters with it
-template <bool Last>
-__global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPlan plan, uint8_t* space, uint32_t from, MuonScalars s) {
-    __shared__ __attribute__((aligned(128))) uint8_t lds[Tile::kBytes];
-    const MuonPiece piece = plan.updates[xcd_tile()];
-    const MuonMatrix& x = plan.matrices[piece.matrix];
-    const Space w = space_of(x, space);
-    const uint32_t tiles = (x.cols + Tile::BP - 1) / Tile::BP;
-    const uint32_t q0 = piece.index / tiles * Tile::BQ, p0 = piece.index % tiles * Tile::BP;
-    const uint32_t nq = min(Tile::BQ, x.rows - q0), np = min(Tile::BP, x.cols - p0);
+// Rows from q0 and columns from p0 of X = a X + B X (tall: X B); Last: of the parameters with it.
+template <bool Last, typename S>
+__device__ __forceinline__ void update_tile(const MuonMatrix& x, const Space& w, uint32_t from, const MuonScalars& s, uint32_t q0, uint32_t p0,
+                                            uint8_t* lds) {
+    const uint32_t nq = min(S::BQ, x.rows - q0), np = min(S::BP, x.cols - p0);
     const _Float16* high = w.high[from];
-    f32x4_t acc[Tile::AQ][Tile::AP];
-    if (x.rows > x.cols) {
-        tile_sums<MmaF16, kAlong, kAlong, Tile>(operand(high + (size_t)q0 * x.ldx, x.ldx, nq), operand(w.b + (size_t)p0 * x.lda, x.lda, np), contraction(x.cols), lds, acc);
-    } else {
-        tile_sums<MmaF16, kAlong, kAcross, Tile>(operand(w.b + (size_t)q0 * x.lda, x.lda, nq),
-                                                 operand(high + p0, x.ldx, min(Tile::BP, x.ldx - p0)), contraction(x.rows), lds, acc);
-    }
-    each_place(acc, [&](f32x4_t& v, uint32_t q, uint32_t p) {
+    f32x4_t acc[S::AQ][S::AP];
+    if (x.rows > x.cols)
+        tile_sums<MmaF16, kAlong, kAlong, S>(operand(high + (size_t)q0 * x.ldx, x.ldx, nq), operand(w.b + (size_t)p0 * x.lda, x.lda, np),
+                                             contraction(x.cols), lds, acc);
+    else
+        tile_sums<MmaF16, kAlong, kAcross, S>(operand(w.b + (size_t)q0 * x.lda, x.lda, nq), operand(high + p0, x.ldx, min(S::BP, x.ldx - p0)),
+                                              contraction(x.rows), lds, acc);
+    each_place<S>(acc, [&](f32x4_t& v, uint32_t q, uint32_t p) {
         if (q >= nq || p >= np) {
             v = f32x4_t{};
             return;
@@ -258,11 +272,78 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPla
         }
     });
     if (Last) return;
-    const uint32_t wide = min(Tile::BP, x.ldx - p0);
+    const uint32_t wide = min(S::BP, x.ldx - p0);
     const size_t at = (size_t)q0 * x.ldx + p0;
-    store_tile<_Float16, Tile>(acc, w.high[1 - from] + at, x.ldx, nq, wide, lds);
-    each_place(acc, [&](f32x4_t& v, uint32_t, uint32_t) { v = (v - __builtin_convertvector(__builtin_convertvector(v, f16x4_t), f32x4_t)) * kLow; });
-    store_tile<_Float16, Tile>(acc, w.low + at, x.ldx, nq, wide, lds);
+    store_tile<_Float16, S>(acc, w.high[1 - from] + at, x.ldx, nq, wide, lds);
+    each_place<S>(acc, [&](f32x4_t& v, uint32_t, uint32_t) { v = (v - __builtin_convertvector(__builtin_convertvector(v, f16x4_t), f32x4_t)) * kLow; });
+    store_tile<_Float16, S>(acc, w.low + at, x.ldx, nq, wide, lds);
+}
+
+// Which of `all` large tiles, and which part of it, a workgroup takes: each XCD has a run of them, and where its last round would
+// leave half of its CUs or more without one, that round's tiles are split into four.
+struct Turn {
+    uint32_t tile, part;  // part == 4: all of it
+};
+constexpr uint32_t kParts = 4;
+__host__ __device__ __forceinline__ uint32_t split_of(uint32_t mine) { return mine % kXcdCus <= kMostSplit ? mine % kXcdCus : 0; }
+__device__ __forceinline__ bool find_turn(uint32_t all, Turn* t) {
+    const uint32_t x = blockIdx.x % kXcds, k = blockIdx.x / kXcds, rest = all % kXcds;
+    const uint32_t first = x * (all / kXcds) + min(x, rest), mine = all / kXcds + (x < rest);
+    const uint32_t split = split_of(mine), whole = mine - split;
+    if (k >= whole + split * kParts) return false;
+    *t = k < whole ? Turn{first + k, kParts} : Turn{first + whole + (k - whole) / kParts, (k - whole) % kParts};
+    return true;
+}
+uint32_t turns(uint32_t all) {
+    const uint32_t least = all / kXcds, most = least + 1;
+    const auto of = [](uint32_t mine) { return mine + (kParts - 1) * split_of(mine); };
+    return kXcds * (all % kXcds && of(most) > of(least) ? of(most) : of(least));
+}
+
+// Calls large(q0, p0), or small(q0, p0) for what a turn has of a tile of rows x cols outputs.
+template <typename F, typename G>
+__device__ __forceinline__ void do_turn(const MuonPiece& piece, uint32_t part, uint32_t rows, uint32_t cols, F large, G small) {
+    const uint32_t q0 = (piece.index >> 16) * kMuonTile, p0 = (piece.index & 0xFFFF) * kMuonTile;
+    const uint32_t nq = min(rows - q0, Large::BQ), np = min(cols - p0, Large::BP);
+    if (part == kParts && nq > Small::BQ && np > Small::BP) {
+        large(q0, p0);
+        return;
+    }
+    for (uint32_t i = 0; i < kParts; ++i) {
+        const uint32_t q = i / 2 * Small::BQ, p = i % 2 * Small::BP;
+        if ((part != kParts && part != i) || q >= nq || p >= np) continue;
+        small(q0 + q, p0 + p);
+        __syncthreads();  // LDS may be written again
+    }
+}
+
+constexpr uint32_t kLdsBytes = Large::kBytes > Small::kBytes ? Large::kBytes : Small::kBytes;
+
+template <bool Second>
+__global__ __launch_bounds__(kTileWaves * 64, 2) void muon_square_kernel(MuonPlan plan, uint32_t all, uint8_t* space, uint32_t from) {
+    __shared__ __attribute__((aligned(128))) uint8_t lds[kLdsBytes];
+    Turn t;
+    if (!find_turn(all, &t)) return;
+    const MuonPiece piece = plan.squares[t.tile];
+    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const Space w = space_of(x, space);
+    const uint32_t s = min(x.rows, x.cols);
+    do_turn(piece, t.part, s, s, [&](uint32_t q, uint32_t p) { square_tile<Second, Large>(x, w, from, q, p, lds); },
+            [&](uint32_t q, uint32_t p) {
+                if (p <= q) square_tile<Second, Small>(x, w, from, q, p, lds);
+            });
+}
+
+template <bool Last>
+__global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPlan plan, uint32_t all, uint8_t* space, uint32_t from, MuonScalars s) {
+    __shared__ __attribute__((aligned(128))) uint8_t lds[kLdsBytes];
+    Turn t;
+    if (!find_turn(all, &t)) return;
+    const MuonPiece piece = plan.updates[t.tile];
+    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const Space w = space_of(x, space);
+    do_turn(piece, t.part, x.rows, x.cols, [&](uint32_t q, uint32_t p) { update_tile<Last, Large>(x, w, from, s, q, p, lds); },
+            [&](uint32_t q, uint32_t p) { update_tile<Last, Small>(x, w, from, s, q, p, lds); });
 }
 
 }  // namespace
@@ -278,11 +359,11 @@ hipError_t launch_muon(const MuonPlan& plan, const MuonCounts& n, int grad_bf16,
                       : enqueue(muon_start_kernel<float>, dim3(n.chunks), few, stream, plan, w, grad_scale, s);
     for (int i = 0; i < iterations && e == hipSuccess; ++i) {
         const uint32_t from = i & 1;
-        e = enqueue(muon_square_kernel<false>, dim3(n.squares), lanes, stream, plan, w, from);
-        if (e == hipSuccess) e = enqueue(muon_square_kernel<true>, dim3(n.squares), lanes, stream, plan, w, from);
+        e = enqueue(muon_square_kernel<false>, dim3(turns(n.squares)), lanes, stream, plan, n.squares, w, from);
+        if (e == hipSuccess) e = enqueue(muon_square_kernel<true>, dim3(turns(n.squares)), lanes, stream, plan, n.squares, w, from);
         if (e == hipSuccess)
-            e = i + 1 < iterations ? enqueue(muon_update_kernel<false>, dim3(n.updates), lanes, stream, plan, w, from, s)
-                                   : enqueue(muon_update_kernel<true>, dim3(n.updates), lanes, stream, plan, w, from, s);
+            e = i + 1 < iterations ? enqueue(muon_update_kernel<false>, dim3(turns(n.updates)), lanes, stream, plan, n.updates, w, from, s)
+                                   : enqueue(muon_update_kernel<true>, dim3(turns(n.updates)), lanes, stream, plan, n.updates, w, from, s);
     }
     return e;
 }

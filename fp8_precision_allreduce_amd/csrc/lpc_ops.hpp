@@ -201,10 +201,10 @@ hipError_t launch_gemm_mxfp4(const uint8_t* x, const uint8_t* xs, size_t rows, s
 
 // elements of a matrix that one workgroup of the matrix optimizer's elementwise kernels takes
 constexpr size_t kMuonChunk = 16384;
-constexpr size_t kMuonTile = 128;  // outputs along a side of a tile of its products
+constexpr size_t kMuonTile = 256;  // outputs along a side of a tile of its products
 
-// A plan is the matrices, then the pieces of each kind of launch: which matrix, and the piece's number within it (chunks of
-// its elements, tiles of its square products, tiles of the matrix).
+// A plan is the matrices, then the pieces of each kind of launch: which matrix, and the chunk's number within it, or the tile's
+// row and column (16 bits each) in its square products, of which those above the diagonal are left out, or in the matrix.
 struct MuonMatrix {
     float* param;
     const void* grad;

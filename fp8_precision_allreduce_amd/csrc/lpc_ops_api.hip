@@ -82,7 +82,7 @@ MuonSizes muon_sizes(size_t rows, size_t cols) {
     const size_t chunks = (rows * cols + lpc::kMuonChunk - 1) / lpc::kMuonChunk;
     const size_t tiles = ((rows + lpc::kMuonTile - 1) / lpc::kMuonTile) * ((cols + lpc::kMuonTile - 1) / lpc::kMuonTile);
     const size_t bytes = 6 * rows * up(cols, kMuonPad) + 4 * s * up(s, kMuonPad) + 8 * chunks;
-    return {chunks, side * side, tiles, up(bytes, 128)};
+    return {chunks, side * (side + 1) / 2, tiles, up(bytes, 128)};
 }
 
 // false: refused
@@ -371,7 +371,7 @@ lpc_status lpc_muon_plan(const lpc_muon_tensor* tensors, int count, lpc_dtype gr
         const lpc_muon_tensor& t = tensors[i];
         if (empty(t)) continue;
         const MuonSizes sizes = muon_sizes(t.rows, t.cols);
-        const size_t counts[3] = {sizes.chunks, sizes.squares, sizes.updates}, n = t.rows * t.cols;
+        const size_t n = t.rows * t.cols, side = t.rows < t.cols ? t.rows : t.cols;
         const size_t element = grad_t == LPC_BF16 ? 2 : 4;
         for (size_t b = 0; b < t.batch; ++b, ++at) {
             lpc::MuonMatrix m{};
@@ -387,11 +387,16 @@ lpc_status lpc_muon_plan(const lpc_muon_tensor* tensors, int count, lpc_dtype gr
             m.scale = (float)t.scale;
             memcpy(matrices + at * sizeof(m), &m, sizeof(m));
             space += sizes.space;
-            for (int kind = 0; kind < 3; ++kind)
-                for (size_t j = 0; j < counts[kind]; ++j, pieces[kind] += sizeof(lpc::MuonPiece)) {
-                    const lpc::MuonPiece piece{at, (uint32_t)j};
-                    memcpy(pieces[kind], &piece, sizeof(piece));
-                }
+            const auto add = [&](int kind, size_t index) {
+                const lpc::MuonPiece piece{at, (uint32_t)index};
+                memcpy(pieces[kind], &piece, sizeof(piece));
+                pieces[kind] += sizeof(piece);
+            };
+            for (size_t j = 0; j < sizes.chunks; ++j) add(0, j);
+            for (size_t q = 0; q * lpc::kMuonTile < side; ++q)
+                for (size_t p = 0; p <= q; ++p) add(1, q << 16 | p);
+            for (size_t q = 0; q * lpc::kMuonTile < t.rows; ++q)
+                for (size_t p = 0; p * lpc::kMuonTile < t.cols; ++p) add(2, q << 16 | p);
         }
     }
     *work = w;

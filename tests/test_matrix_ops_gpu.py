@@ -403,6 +403,12 @@ def test_muon(dev, shapes, grad_t):
     check_muon(dev, shapes, grad_t)
 
 
+@pytest.mark.parametrize("shapes", [[(9, 520, 2100)], [(50, 300, 520)], [(50, 520, 300), (33, 33)]], ids=str)
+def test_muon_large_tiles(dev, shapes):
+    """Enough tiles of 256 x 256, of either product, that a round of them is not split."""
+    check_muon(dev, shapes, BF16)
+
+
 @pytest.mark.parametrize("shapes", [[(64, 64)], [(128, 512)], [(600, 256)], [(3, 100, 60)]], ids=str)
 def test_muon_strong_directions(dev, shapes):
     check_muon(dev, shapes, F32, kind="strong")
