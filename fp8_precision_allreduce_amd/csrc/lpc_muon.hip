@@ -346,14 +346,201 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPla
             [&](uint32_t q, uint32_t p) { update_tile<Last, Small>(x, w, from, s, q, p, lds); });
 }
 
+// ---------------------------------------------------------------------------
+// matrices of a shorter side of at most 32: in two launches.  With U short x long, every X is R U / |u| with R a polynomial of
+// U U^T: the first launch sums that up, in 64 bits and a part of it per workgroup; in the second each workgroup finds R, 32 x 32 in
+// FP32, and applies it to its part of U.  All of its products are FP32 matrix instructions, so that the update is good to
+// about 1e-4 of itself (R is up to 3.4445^5 = 485 where a singular value is small); rounding to fp16 does not average out
+// over so few rows.  Four matrices of 16 x 1152: 169 us with the tiles' 17 launches.
+// ---------------------------------------------------------------------------
+
+typedef double f64x4_t __attribute__((ext_vector_type(4)));
+constexpr uint32_t kSide = kMuonSmall, kPitch = kSide + 1, kBlockCols = 128, kPerLane = kSide * kBlockCols / kChunkLanes;
+
+// A workgroup's part of U's long side, in blocks of 128.
+struct Strip {
+    uint32_t side, length, begin, end;
+    bool tall;
+
+    __device__ __forceinline__ Strip(const MuonMatrix& x, uint32_t index)
+        : side(min(x.rows, x.cols)), length(max(x.rows, x.cols)), begin(index * x.span), end(min(length, begin + x.span)), tall(x.rows > x.cols) {}
+    // the lane's n-th element of the block from k0 on: its place in the matrix and in the block; false: none
+    __device__ __forceinline__ bool place(int n, uint32_t k0, size_t* at, uint32_t* i, uint32_t* k) const {
+        const uint32_t e = n * kChunkLanes + threadIdx.x;
+        *k = tall ? e / side : e % kBlockCols;
+        *i = tall ? e - *k * side : e / kBlockCols;
+        *at = tall ? (size_t)(k0 + *k) * side + *i : (size_t)*i * length + k0 + *k;
+        return *i < side && *k < kBlockCols && k0 + *k < end;
+    }
+};
+
+__device__ __forceinline__ float element(const float* p, size_t i) { return p[i]; }
+__device__ __forceinline__ float element(const uint16_t* p, size_t i) { return bf16lo(p[i]); }
+
+template <typename Grad>
+__global__ __launch_bounds__(kChunkLanes) void muon_small_sums_kernel(MuonPlan plan, uint8_t* space, const float* grad_scale, MuonScalars s) {
+    __shared__ float u[kBlockCols][kPitch];
+    const MuonPiece piece = plan.smalls[blockIdx.x];
+    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const Strip strip(x, piece.index);
+    const Grad* grad = static_cast<const Grad*>(x.grad);
+    const float scale = grad_scale ? grad_scale[0] : 1.0f;
+    const uint32_t wave = threadIdx.x >> 6, l16 = threadIdx.x & 15, l4 = (threadIdx.x & 63) >> 4;
+    const uint32_t ti = wave / 2 * 16 + l16, tj = wave % 2 * 16 + l16;
+    f64x4_t sum = {};
+    for (uint32_t k0 = strip.begin; k0 < strip.end; k0 += kBlockCols) {
+        float g[kPerLane], m[kPerLane];
+        size_t at;
+        uint32_t i, k;
+#pragma unroll
+        for (int n = 0; n < (int)kPerLane; ++n) {
+            const bool in = strip.place(n, k0, &at, &i, &k);
+            g[n] = in ? element(grad, at) * scale : 0.0f;
+            m[n] = in ? x.m[at] * s.beta : 0.0f;
+        }
+        for (uint32_t e = threadIdx.x; e < kBlockCols * kPitch; e += kChunkLanes) (&u[0][0])[e] = 0.0f;
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < (int)kPerLane; ++n) {
+            if (!strip.place(n, k0, &at, &i, &k)) continue;
+            const float now = m[n] + g[n] * s.rest;
+            x.m[at] = now;
+            u[k][i] = s.nesterov ? g[n] * s.rest + now * s.beta : now;
+        }
+        __syncthreads();
+#pragma unroll 8
+        for (uint32_t c = 0; c < kBlockCols; c += 4)
+            sum = __builtin_amdgcn_mfma_f64_16x16x4f64((double)u[c + l4][ti], (double)u[c + l4][tj], sum, 0, 0, 0);
+        __syncthreads();
+    }
+    double* out = reinterpret_cast<double*>(space + x.space) + (size_t)piece.index * kSide * kSide;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[(wave / 2 * 16 + l4 + 4 * e) * kSide + tj] = sum[e];
+}
+
+// to = a b of matrices [32][kPitch] that are symmetric: the wavefront's 16 x 16 of it
+__device__ __forceinline__ f32x4_t small_product(const float (*a)[kPitch], const float (*b)[kPitch]) {
+    const uint32_t wave = threadIdx.x >> 6, l16 = threadIdx.x & 15, l4 = (threadIdx.x & 63) >> 4;
+    f32x4_t sum = {};
+#pragma unroll
+    for (uint32_t c = 0; c < kSide; c += 4)
+        sum = __builtin_amdgcn_mfma_f32_16x16x4f32(a[wave / 2 * 16 + l16][c + l4], b[wave % 2 * 16 + l16][c + l4], sum, 0, 0, 0);
+    return sum;
+}
+
+template <typename Grad>
+__global__ __launch_bounds__(kChunkLanes) void muon_small_update_kernel(MuonPlan plan, uint8_t* space, const float* grad_scale, int iterations,
+                                                                        MuonScalars s) {
+    __shared__ float a[kSide][kPitch], p[kSide][kPitch], r[kSide][kPitch], t[kSide][kPitch], u[kBlockCols][kPitch], o[kBlockCols][kPitch];
+    __shared__ double diagonal[kSide];
+    const MuonPiece piece = plan.smalls[blockIdx.x];
+    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const Strip strip(x, piece.index);
+    const Grad* grad = static_cast<const Grad*>(x.grad);
+    const float scale = grad_scale ? grad_scale[0] : 1.0f;
+    const uint32_t wave = threadIdx.x >> 6, l16 = threadIdx.x & 15, l4 = (threadIdx.x & 63) >> 4;
+
+    constexpr int kSums = kSide * kSide / kChunkLanes;
+    const double* sums = reinterpret_cast<const double*>(space + x.space) + threadIdx.x;
+    const uint32_t strips = (strip.length + x.span - 1) / x.span;
+    double gram[kSums] = {};
+#pragma unroll 4
+    for (uint32_t c = 0; c < strips; ++c)
+#pragma unroll
+        for (int n = 0; n < kSums; ++n) gram[n] += sums[((size_t)c * kSums + n) * kChunkLanes];
+#pragma unroll
+    for (int n = 0; n < kSums; ++n) {
+        const uint32_t e = n * kChunkLanes + threadIdx.x;
+        if (e % (kSide + 1) == 0) diagonal[e / (kSide + 1)] = gram[n];
+    }
+    __syncthreads();
+    double norm2 = 0.0;
+    for (uint32_t d = 0; d < kSide; ++d) norm2 += diagonal[d];
+    const double inverse = norm2 > 0.0 ? 1.0 / norm2 : 0.0, by = sqrt(inverse);
+#pragma unroll
+    for (int n = 0; n < kSums; ++n) {
+        const uint32_t e = n * kChunkLanes + threadIdx.x;
+        a[e / kSide][e % kSide] = (float)(gram[n] * inverse);
+    }
+    __syncthreads();
+    const uint32_t row = wave / 2 * 16 + 4 * l4, col = wave % 2 * 16 + l16;  // of four sums, below one another
+    for (int n = 0; n < iterations; ++n) {
+        const f32x4_t square = small_product(a, a);  // P = a + b A + c A A
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[row + e][col] = (row + e == col ? kA : 0.0f) + kB * a[row + e][col] + kC * square[e];
+        __syncthreads();
+        const f32x4_t next = n ? small_product(p, r) : f32x4_t{};
+        const bool more = n + 1 < iterations;
+        const f32x4_t half = more ? small_product(p, a) : f32x4_t{};
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r[row + e][col] = n ? next[e] : p[row + e][col];
+            t[row + e][col] = half[e];
+        }
+        __syncthreads();
+        const f32x4_t whole = more ? small_product(p, t) : f32x4_t{};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[row + e][col] = whole[e];
+        __syncthreads();
+    }
+
+    const float rate = s.lr * x.scale;
+    for (uint32_t k0 = strip.begin; k0 < strip.end; k0 += kBlockCols) {
+        float param[kPerLane];
+        size_t at;
+        uint32_t i, k;
+        for (uint32_t e = threadIdx.x; e < kBlockCols * kPitch; e += kChunkLanes) (&u[0][0])[e] = 0.0f;
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < (int)kPerLane; ++n) {
+            const bool in = strip.place(n, k0, &at, &i, &k);
+            param[n] = in ? x.param[at] : 0.0f;
+            if (!in) continue;
+            const float m = x.m[at];
+            u[k][i] = (float)((double)(s.nesterov ? element(grad, at) * scale * s.rest + m * s.beta : m) * by);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+            for (int tk = 0; tk < 2; ++tk) {
+                const uint32_t k1 = (2 * wave + tk) * 16 + l16;
+                f32x4_t v = {};
+#pragma unroll
+                for (uint32_t c = 0; c < kSide; c += 4) v = __builtin_amdgcn_mfma_f32_16x16x4f32(r[ti * 16 + l16][c + l4], u[k1][c + l4], v, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[k1][ti * 16 + 4 * l4 + e] = v[e];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < (int)kPerLane; ++n) {
+            if (!strip.place(n, k0, &at, &i, &k)) continue;
+            const float now = param[n] * s.keep - o[k][i] * rate;
+            x.param[at] = now;
+            if (x.copy) x.copy[at] = (uint16_t)pack_bf16x2(now, now);
+        }
+        __syncthreads();
+    }
+}
+
 }  // namespace
 
 hipError_t launch_muon(const MuonPlan& plan, const MuonCounts& n, int grad_bf16, int iterations, const MuonScalars& s, const float* grad_scale,
                        void* space, hipStream_t stream) {
     uint8_t* w = static_cast<uint8_t*>(space);
     const dim3 lanes(kTileWaves * 64), few(kChunkLanes);
-    hipError_t e = grad_bf16 ? enqueue(muon_momentum_kernel<uint16_t>, dim3(n.chunks), few, stream, plan, w, grad_scale, s)
-                             : enqueue(muon_momentum_kernel<float>, dim3(n.chunks), few, stream, plan, w, grad_scale, s);
+    hipError_t e = hipSuccess;
+    if (n.smalls != 0) {
+        e = grad_bf16 ? enqueue(muon_small_sums_kernel<uint16_t>, dim3(n.smalls), few, stream, plan, w, grad_scale, s)
+                      : enqueue(muon_small_sums_kernel<float>, dim3(n.smalls), few, stream, plan, w, grad_scale, s);
+        if (e == hipSuccess)
+            e = grad_bf16 ? enqueue(muon_small_update_kernel<uint16_t>, dim3(n.smalls), few, stream, plan, w, grad_scale, iterations, s)
+                          : enqueue(muon_small_update_kernel<float>, dim3(n.smalls), few, stream, plan, w, grad_scale, iterations, s);
+    }
+    if (n.chunks == 0 || e != hipSuccess) return e;
+    e = grad_bf16 ? enqueue(muon_momentum_kernel<uint16_t>, dim3(n.chunks), few, stream, plan, w, grad_scale, s)
+                  : enqueue(muon_momentum_kernel<float>, dim3(n.chunks), few, stream, plan, w, grad_scale, s);
     if (e == hipSuccess)
         e = grad_bf16 ? enqueue(muon_start_kernel<uint16_t>, dim3(n.chunks), few, stream, plan, w, grad_scale, s)
                       : enqueue(muon_start_kernel<float>, dim3(n.chunks), few, stream, plan, w, grad_scale, s);

@@ -203,8 +203,12 @@ hipError_t launch_gemm_mxfp4(const uint8_t* x, const uint8_t* xs, size_t rows, s
 constexpr size_t kMuonChunk = 16384;
 constexpr size_t kMuonTile = 256;  // outputs along a side of a tile of its products
 
+constexpr size_t kMuonSmall = 32;  // shorter sides up to this go without tiles
+// of such a matrix's longer side, a workgroup takes whole blocks of 128, of 64 workgroups at most
+inline size_t muon_span(size_t length) { return (length + 128 * 64 - 1) / (128 * 64) * 128; }
+
 // A plan is the matrices, then the pieces of each kind of launch: which matrix, and the chunk's number within it, or the tile's
-// row and column (16 bits each) in its square products, of which those above the diagonal are left out, or in the matrix.
+// row and column (16 bits each) in its square products, of which those above the diagonal are left out, or in the matrix; of a small matrix, the number of the span.
 struct MuonMatrix {
     float* param;
     const void* grad;
@@ -214,7 +218,7 @@ struct MuonMatrix {
     uint32_t rows, cols;
     uint32_t ldx, lda;  // elements between rows of X, and of A and B
     float scale;
-    uint32_t unused;
+    uint32_t span;      // of a small matrix: muon_span()
 };
 static_assert(sizeof(MuonMatrix) % 16 == 0, "pieces start aligned");
 struct MuonPiece {
@@ -222,10 +226,10 @@ struct MuonPiece {
 };
 struct MuonPlan {
     const MuonMatrix* matrices;
-    const MuonPiece *chunks, *squares, *updates;
+    const MuonPiece *chunks, *squares, *updates, *smalls;
 };
 struct MuonCounts {
-    uint32_t chunks, squares, updates;
+    uint32_t chunks, squares, updates, smalls;
 };
 struct MuonScalars {
     float beta, rest, keep, lr;

@@ -74,15 +74,20 @@ constexpr size_t kMuonPad = 64;  // elements that rows of its workspace are padd
 size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 
 struct MuonSizes {
-    size_t chunks, squares, updates, space;  // of one matrix
+    size_t chunks, squares, updates, smalls, space;  // of one matrix
 };
 
 MuonSizes muon_sizes(size_t rows, size_t cols) {
-    const size_t s = rows < cols ? rows : cols, side = (s + lpc::kMuonTile - 1) / lpc::kMuonTile;
+    const size_t s = rows < cols ? rows : cols, length = rows < cols ? cols : rows;
+    if (s <= lpc::kMuonSmall) {
+        const size_t smalls = (length + lpc::muon_span(length) - 1) / lpc::muon_span(length);
+        return {0, 0, 0, smalls, smalls * lpc::kMuonSmall * lpc::kMuonSmall * sizeof(double)};
+    }
+    const size_t side = (s + lpc::kMuonTile - 1) / lpc::kMuonTile;
     const size_t chunks = (rows * cols + lpc::kMuonChunk - 1) / lpc::kMuonChunk;
     const size_t tiles = ((rows + lpc::kMuonTile - 1) / lpc::kMuonTile) * ((cols + lpc::kMuonTile - 1) / lpc::kMuonTile);
     const size_t bytes = 6 * rows * up(cols, kMuonPad) + 4 * s * up(s, kMuonPad) + 8 * chunks;
-    return {chunks, side * (side + 1) / 2, tiles, up(bytes, 128)};
+    return {chunks, side * (side + 1) / 2, tiles, 0, up(bytes, 128)};
 }
 
 // false: refused
@@ -96,14 +101,15 @@ bool muon_work(const lpc_muon_tensor* t, int count, lpc_muon_work* w) {
         w->chunks += t[i].batch * m.chunks;
         w->squares += t[i].batch * m.squares;
         w->updates += t[i].batch * m.updates;
+        w->smalls += t[i].batch * m.smalls;
         w->workspace_bytes += t[i].batch * m.space;  // below 2^24 pieces of 2^23 bytes
-        if (w->chunks > kMaxPieces || w->squares > kMaxPieces || w->updates > kMaxPieces) return false;
+        if (w->chunks > kMaxPieces || w->squares > kMaxPieces || w->updates > kMaxPieces || w->smalls > kMaxPieces) return false;
     }
     return true;
 }
 
 size_t muon_plan_size(const lpc_muon_work& w) {
-    return w.matrices * sizeof(lpc::MuonMatrix) + up((w.chunks + w.squares + w.updates) * sizeof(lpc::MuonPiece), 16);
+    return w.matrices * sizeof(lpc::MuonMatrix) + up((w.chunks + w.squares + w.updates + w.smalls) * sizeof(lpc::MuonPiece), 16);
 }
 
 }  // namespace
@@ -361,10 +367,11 @@ lpc_status lpc_muon_plan(const lpc_muon_tensor* tensors, int count, lpc_dtype gr
     if (plan_bytes < muon_plan_size(w)) return LPC_ERR_SHAPE;
     memset(plan, 0, muon_plan_size(w));
     uint8_t* matrices = static_cast<uint8_t*>(plan);
-    uint8_t* pieces[3];  // chunks, squares, updates
+    uint8_t* pieces[4];  // chunks, squares, updates, smalls
     pieces[0] = matrices + w.matrices * sizeof(lpc::MuonMatrix);
     pieces[1] = pieces[0] + w.chunks * sizeof(lpc::MuonPiece);
     pieces[2] = pieces[1] + w.squares * sizeof(lpc::MuonPiece);
+    pieces[3] = pieces[2] + w.updates * sizeof(lpc::MuonPiece);
     uint32_t at = 0;
     uint64_t space = 0;
     for (int i = 0; i < count; ++i) {
@@ -385,6 +392,7 @@ lpc_status lpc_muon_plan(const lpc_muon_tensor* tensors, int count, lpc_dtype gr
             m.ldx = (uint32_t)up(t.cols, kMuonPad);
             m.lda = (uint32_t)up(t.rows < t.cols ? t.rows : t.cols, kMuonPad);
             m.scale = (float)t.scale;
+            m.span = sizes.smalls ? (uint32_t)lpc::muon_span(t.rows < t.cols ? t.cols : t.rows) : 0;
             memcpy(matrices + at * sizeof(m), &m, sizeof(m));
             space += sizes.space;
             const auto add = [&](int kind, size_t index) {
@@ -392,6 +400,10 @@ lpc_status lpc_muon_plan(const lpc_muon_tensor* tensors, int count, lpc_dtype gr
                 memcpy(pieces[kind], &piece, sizeof(piece));
                 pieces[kind] += sizeof(piece);
             };
+            if (sizes.smalls) {
+                for (size_t j = 0; j < sizes.smalls; ++j) add(3, j);
+                continue;
+            }
             for (size_t j = 0; j < sizes.chunks; ++j) add(0, j);
             for (size_t q = 0; q * lpc::kMuonTile < side; ++q)
                 for (size_t p = 0; p <= q; ++p) add(1, q << 16 | p);
@@ -411,7 +423,7 @@ lpc_status lpc_muon_step(const void* plan, const lpc_muon_work* work, lpc_dtype 
     if (work->matrices == 0) return LPC_OK;
     if (!plan || !workspace) return LPC_ERR_NULL;
     if (misaligned(plan) || misaligned(workspace) || misaligned4(grad_scale)) return LPC_ERR_ALIGN;
-    if (work->matrices > kMaxPieces || work->chunks > kMaxPieces || work->squares > kMaxPieces || work->updates > kMaxPieces ||
+    if (work->matrices > kMaxPieces || work->chunks > kMaxPieces || work->squares > kMaxPieces || work->updates > kMaxPieces || work->smalls > kMaxPieces ||
         workspace_bytes < work->workspace_bytes || !(beta >= 0.0 && beta < 1.0) || iterations < 1 ||
         iterations > LPC_MUON_MAX_ITERATIONS)
         return LPC_ERR_SHAPE;
@@ -421,7 +433,8 @@ lpc_status lpc_muon_step(const void* plan, const lpc_muon_work* work, lpc_dtype 
     p.chunks = reinterpret_cast<const lpc::MuonPiece*>(b + work->matrices * sizeof(lpc::MuonMatrix));
     p.squares = p.chunks + work->chunks;
     p.updates = p.squares + work->squares;
-    const lpc::MuonCounts n{(uint32_t)work->chunks, (uint32_t)work->squares, (uint32_t)work->updates};
+    p.smalls = p.updates + work->updates;
+    const lpc::MuonCounts n{(uint32_t)work->chunks, (uint32_t)work->squares, (uint32_t)work->updates, (uint32_t)work->smalls};
     const lpc::MuonScalars s{(float)beta, (float)(1.0 - beta), (float)(1.0 - lr * weight_decay), (float)lr, nesterov != 0};
     return hip_status(lpc::launch_muon(p, n, grad_t == LPC_BF16, iterations, s, grad_scale, workspace, stream));
 }

@@ -55,7 +55,7 @@ class _MuonTensor(ctypes.Structure):
 
 
 class _MuonWork(ctypes.Structure):
-    _fields_ = [(f, ctypes.c_size_t) for f in ("matrices", "chunks", "squares", "updates", "workspace_bytes")]
+    _fields_ = [(f, ctypes.c_size_t) for f in ("matrices", "chunks", "squares", "updates", "smalls", "workspace_bytes")]
 
 
 _vp, _sz, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int

@@ -321,7 +321,7 @@ typedef struct {
 /* What a step of a plan launches; lpc_muon_plan writes it and lpc_muon_step
  * takes it as it is.                                                         */
 typedef struct {
-    size_t matrices, chunks, squares, updates;
+    size_t matrices, chunks, squares, updates, smalls;
     size_t workspace_bytes;
 } lpc_muon_work;
 

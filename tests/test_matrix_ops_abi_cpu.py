@@ -82,7 +82,7 @@ def test_mxfp4_errors(L):  # noqa: F811
 def plan(L, rows, grad=F32):  # noqa: F811
     t = (lpc._MuonTensor * max(len(rows), 1))(*[lpc._MuonTensor(*r) for r in rows])
     size = L.lpc_muon_plan_bytes(t, len(rows))
-    host, work = (ctypes.c_uint8 * max(size, 1))(), lpc._MuonWork(9, 9, 9, 9, 9)
+    host, work = (ctypes.c_uint8 * max(size, 1))(), lpc._MuonWork(9, 9, 9, 9, 9, 9)
     return L.lpc_muon_plan(t, len(rows), grad, host, size, ctypes.byref(work)), work, bytes(host[:size])
 
 
@@ -95,7 +95,8 @@ def test_muon_plan(L):  # noqa: F811
     st, work, data = plan(L, [row, (A, A, A, A, 1, 1, 1, 1.0)])
     assert st == OK and work.matrices == 3 and len(data) % 16 == 0
     # X's halves twice and once, [300, 128]; A and B, [100, 128]; a sum for each of two chunks
-    assert work.workspace_bytes >= 2 * (3 * 300 * 128 * 2 + 2 * 100 * 128 * 2 + 2 * 8)
+    # and 32 x 32 sums in 64 bits of the small one
+    assert work.workspace_bytes >= 2 * (3 * 300 * 128 * 2 + 2 * 100 * 128 * 2 + 2 * 8) + 8192
     for i in range(3):
         assert plan(L, [row[:i] + (None,) + row[i + 1:]])[0] == NULL
         assert plan(L, [row[:i] + (B,) + row[i + 1:]])[0] == ALIGN
@@ -104,7 +105,7 @@ def test_muon_plan(L):  # noqa: F811
     side = 1 << 20
     for bad in ((1, side + 1, 4), (1, 4, side + 1), (1, side, side), (1 << 40, 4, 4), ((1 << 64) - 1, 4, 4), (1, (1 << 64) - 1, 4)):
         t = (lpc._MuonTensor * 1)(lpc._MuonTensor(A, A, A, None, *bad, 1.0))
-        work = lpc._MuonWork(9, 9, 9, 9, 9)
+        work = lpc._MuonWork(9, 9, 9, 9, 9, 9)
         assert L.lpc_muon_plan_bytes(t, 1) == 0
         assert L.lpc_muon_plan(t, 1, F32, (ctypes.c_uint8 * 64)(), 64, ctypes.byref(work)) == SHAPE and work.matrices == 0, bad
     t, work = (lpc._MuonTensor * 1)(lpc._MuonTensor(*row)), lpc._MuonWork()
@@ -131,7 +132,7 @@ def test_muon_step_errors(L):  # noqa: F811
     assert f(*replaced(ok, _0=B)) == ALIGN and f(*replaced(ok, _9=B)) == ALIGN and f(*replaced(ok, _8=A + 2)) == ALIGN
     for bad in (dict(_4=1.0), dict(_4=-0.1), dict(_4=float("nan")), dict(_7=0), dict(_7=-1), dict(_7=11), dict(_10=work.workspace_bytes - 1)):
         assert f(*replaced(ok, **bad)) == SHAPE, bad
-    for field in ("matrices", "chunks", "squares", "updates"):
+    for field in ("matrices", "chunks", "squares", "updates", "smalls"):
         odd = lpc._MuonWork.from_buffer_copy(work)
         setattr(odd, field, (1 << 24) + 1)
         assert f(*replaced(ok, _1=ctypes.byref(odd))) == SHAPE, field
