@@ -31,30 +31,63 @@ __device__ __forceinline__ Operand operand(const uint16_t* first, uint32_t ld, u
     return {reinterpret_cast<const uint8_t*>(first), (size_t)ld * 2, n, nullptr};
 }
 
-// Outputs [q0, + nq) x [p0, + np) of group g (== groups: rows past the last group, whose sums are empty).  product, dgrad: q0 is
-// a row of x; wgrad: a row of dw[g], and rows [r0, r1) are the group's.
+// The operands of outputs [q0, + nq) x [p0, + np) of group g (== groups: rows past the last group, whose sums are empty).
+// product, dgrad: q0 is a row of x; wgrad: a row of dw[g], and rows [r0, r1) are the group's.
+template <int M, typename Out>
+struct Part {
+    Operand q, p;
+    Contraction k;
+    Out* out;
+    uint32_t nq, np, ldo;
+
+    __device__ __forceinline__ Part(const Gemm16Args& a, uint32_t g, uint32_t q0, uint32_t rows_q, uint32_t p0, uint32_t most_p, uint32_t r0, uint32_t r1)
+        : nq(rows_q), np(min(most_p, outputs_p<M>(a) - p0)), ldo(outputs_p<M>(a)) {
+        k = contraction(M == kWgrad ? r1 - r0 : g == a.groups ? 0 : M == kProduct ? a.k : a.n);
+        const size_t matrix = (size_t)(g == a.groups ? 0 : g) * a.n * a.k;
+        if constexpr (M == kProduct) {
+            q = operand(a.q + (size_t)q0 * a.k, a.k, nq);
+            p = operand(a.p + matrix + (size_t)p0 * a.k, a.k, np);
+        } else if constexpr (M == kDgrad) {
+            q = operand(a.q + (size_t)q0 * a.n, a.n, nq);
+            p = operand(a.p + matrix + p0, a.k, np);
+        } else {
+            q = operand(a.q + (size_t)r0 * a.n + q0, a.n, nq);
+            p = operand(a.p + (size_t)r0 * a.k + p0, a.k, np);
+        }
+        out = static_cast<Out*>(a.out) + (M == kWgrad ? matrix : 0) + (size_t)q0 * ldo + p0;
+    }
+};
+
 template <int M, typename Out, typename S>
 __device__ __forceinline__ void tile(const Gemm16Args& a, uint32_t g, uint32_t q0, uint32_t nq, uint32_t p0, uint32_t r0, uint32_t r1,
                                      uint8_t* lds) {
-    const uint32_t np = min(S::BP, outputs_p<M>(a) - p0);
-    const uint32_t length = M == kWgrad ? r1 - r0 : g == a.groups ? 0 : M == kProduct ? a.k : a.n;
-    const size_t matrix = (size_t)(g == a.groups ? 0 : g) * a.n * a.k;
-    Operand q, p;
-    if constexpr (M == kProduct) {
-        q = operand(a.q + (size_t)q0 * a.k, a.k, nq);
-        p = operand(a.p + matrix + (size_t)p0 * a.k, a.k, np);
-    } else if constexpr (M == kDgrad) {
-        q = operand(a.q + (size_t)q0 * a.n, a.n, nq);
-        p = operand(a.p + matrix + p0, a.k, np);
-    } else {
-        q = operand(a.q + (size_t)r0 * a.n + q0, a.n, nq);
-        p = operand(a.p + (size_t)r0 * a.k + p0, a.k, np);
-    }
+    const Part<M, Out> t(a, g, q0, nq, p0, S::BP, r0, r1);
     f32x4_t acc[S::AQ][S::AP];
-    tile_sums<MmaBf16, kFormQ<M>, kFormP<M>, S>(q, p, contraction(length), lds, acc);
-    const uint32_t ldo = outputs_p<M>(a);
-    Out* out = static_cast<Out*>(a.out) + (M == kWgrad ? matrix : 0) + (size_t)q0 * ldo + p0;
-    store_tile<Out, S>(acc, out, ldo, nq, np, lds);
+    tile_sums<MmaBf16, kFormQ<M>, kFormP<M>, S>(t.q, t.p, t.k, lds, acc);
+    store_tile<Out, S>(acc, t.out, t.ldo, t.nq, t.np, lds);
+}
+
+template <int M, typename Out, typename S>
+__global__ __launch_bounds__(kNarrowWaves * 64) void gemm16_narrow_kernel(Gemm16Args a) {
+    __shared__ __attribute__((aligned(128))) uint8_t lds[S::kBytes];
+    const uint32_t tiles_p = (outputs_p<M>(a) + S::BP - 1) / S::BP;
+    GroupTile g;
+    uint32_t q0, nq, tp;
+    if constexpr (M == kWgrad) {
+        const uint32_t n = (uint32_t)xcd_tile();
+        g = find_group(a.counts, a.groups, a.rows, 1, blockIdx.y);
+        q0 = n / tiles_p * S::BQ;
+        nq = min(S::BQ, a.n - q0);
+        tp = n % tiles_p;
+    } else {
+        if (!find_even(a.counts, a.groups, a.rows, S::BQ, tiles_p, &g, &tp)) return;
+        q0 = g.row;
+        nq = g.rows;
+    }
+    const Part<M, Out> t(a, g.group, q0, nq, tp * S::BP, S::BP, g.row, g.row + g.rows);
+    narrow_tile<MmaBf16, kFormQ<M>, kFormP<M>, S>(t.q, t.p, t.k, lds, [&](uint32_t q, uint32_t p, const f32x4_t& v) {
+        if (q < t.nq && p < t.np) store4(v, t.out + (size_t)q * t.ldo + p, t.np - p, t.ldo % 4 == 0);
+    });
 }
 
 using Large = LargeOf<false>;
@@ -105,15 +138,51 @@ hipError_t launch_wgrad(const Gemm16Args& a, hipStream_t stream) {
     return enqueue(gemm16_wgrad_kernel<Out, S>, dim3((uint32_t)wgs, a.groups), dim3(kTileWaves * 64), stream, a);
 }
 
+template <int M, typename Out, int QF, int PF, int Depth>
+hipError_t launch_narrow(const Gemm16Args& a, hipStream_t stream) {
+    using S = NarrowOf<QF, PF, Depth, false>;
+    const uint64_t tiles_q = M == kWgrad ? (a.n + (uint64_t)S::BQ - 1) / S::BQ : most_tiles(a.counts, a.groups, a.rows, S::BQ);
+    const uint64_t tiles = tiles_q * ((outputs_p<M>(a) + (uint64_t)S::BP - 1) / S::BP), wgs = M == kWgrad ? tiles : even_workgroups(tiles);
+    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    return enqueue(gemm16_narrow_kernel<M, Out, S>, dim3((uint32_t)wgs, M == kWgrad ? a.groups : 1), dim3(kNarrowWaves * 64), stream, a);
+}
+
+// By the number of workgroups, one to a CU and 256 CUs.  Times in us with the weights in HBM, of 32 x 32 / 64 x 32 / 64 x 64
+// outputs / large and small tiles:
+//   up to 32 rows a group    32 x 32: 8192 x 8192, 1 row 27.7 / 29.6 / 34.9 / 60.5, 32 rows 28.9 / 30.1 / 36.7 / 59.9; over 8
+//                            weights of 7168 x 2048, 32 rows 45 / 46 / 43 / 59, 256 rows 63 / 73 / 71 / 75; over 32, 32 rows
+//                            41 / 42 / 34 / 55 and 1024 rows 250 / 253 / 198 / 227
+//   more than 384 of 64 x 64 tiles: 8192 x 8192, 256 rows 154 / 101 / 82 / 74; 2048 x 2048 x 2048 89 / 56 / 49 / 22
+//   more than 128            64 x 64: 128 rows 82 / 56 / 45 / 75; 777 rows over 3 weights of 1160 x 1000 17 / 13 / 9.7 / 16
+//   more than 128 of 64 x 32 64 x 32: 64 rows 44 / 35 / 43 / 63
+//   otherwise                32 x 32
+// The gradients, 64 x 64 / tiles: up to 256 of 64 x 64, 1024 x 1024 x 1024 10.2 / 12.5 (rows) and 9.8 / 13.1 (weights); more, 777
+// rows as above 15.4 / 14.6 and 18 / 11.5.  The weights' are large tiles where there are more than 128 of these, else small
+// ones: 2048 rows, 4096 x 2048 55 / 46, 4096 x 4096 69 / 89.
+template <int M, typename Out>
+hipError_t launch(const Gemm16Args& a, hipStream_t stream) {
+    const uint64_t wide = (outputs_p<M>(a) + 63ull) / 64;
+    if constexpr (M == kWgrad) {
+        if ((a.n + 63ull) / 64 * wide * a.groups <= 256) return launch_narrow<M, Out, 4, 4, 2>(a, stream);
+        return wgrad_tiles<Large>(a) * a.groups <= 128 ? launch_wgrad<Out, Small>(a, stream) : launch_wgrad<Out, Large>(a, stream);
+    } else {
+        const uint64_t high = most_tiles(a.counts, a.groups, a.rows, 64);
+        if constexpr (M == kDgrad) {
+            return high * wide <= 256 ? launch_narrow<M, Out, 4, 4, 2>(a, stream) : launch_rows<M, Out>(a, stream);
+        } else {
+            if (a.rows > 32ull * a.groups) {
+                if (high * wide > 384) return launch_rows<M, Out>(a, stream);
+                if (high * wide > 128) return launch_narrow<M, Out, 4, 4, 2>(a, stream);
+                if (high * ((a.n + 31ull) / 32) > 128) return launch_narrow<M, Out, 4, 2, 2>(a, stream);
+            }
+            return launch_narrow<M, Out, 2, 2, 3>(a, stream);
+        }
+    }
+}
+
 template <int M>
 hipError_t launch(const Gemm16Args& a, int out_bf16, hipStream_t stream) {
-    if constexpr (M == kWgrad) {
-        const bool small = wgrad_tiles<Large>(a) * a.groups <= 128;
-        if (small) return out_bf16 ? launch_wgrad<uint16_t, Small>(a, stream) : launch_wgrad<float, Small>(a, stream);
-        return out_bf16 ? launch_wgrad<uint16_t, Large>(a, stream) : launch_wgrad<float, Large>(a, stream);
-    } else {
-        return out_bf16 ? launch_rows<M, uint16_t>(a, stream) : launch_rows<M, float>(a, stream);
-    }
+    return out_bf16 ? launch<M, uint16_t>(a, stream) : launch<M, float>(a, stream);
 }
 
 }  // namespace

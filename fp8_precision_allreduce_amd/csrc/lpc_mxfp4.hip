@@ -84,16 +84,43 @@ struct Mxfp4Args {
 using Large = LargeOf<true>;
 using Small = SmallOf<true>;
 
-// outputs [q0, + nq) x [p0, + np) of group g (== groups: rows past the last one, whose sums are empty)
+// The operands of outputs [q0, + nq) x [p0, + np) of group g (== groups: rows past the last one, whose sums are empty).
+template <typename Out>
+struct Part {
+    Operand q, p;
+    Contraction k;
+    Out* out;
+    uint32_t nq, np;
+
+    __device__ __forceinline__ Part(const Mxfp4Args& a, uint32_t g, uint32_t q0, uint32_t rows_q, uint32_t p0, uint32_t most_p)
+        : nq(rows_q), np(min(most_p, a.n - p0)) {
+        const uint32_t row = a.k / 2, scale_row = a.k / 32;
+        const size_t first = (size_t)(g == a.groups ? 0 : g) * a.n + p0;
+        k = contraction(g == a.groups ? 0 : row / 2);
+        q = {a.x + (size_t)q0 * row, row, nq, a.xs + (size_t)q0 * scale_row};
+        p = {a.w + first * row, row, np, a.ws + first * scale_row};
+        out = static_cast<Out*>(a.out) + (size_t)q0 * a.n + p0;
+    }
+};
+
 template <typename Out, typename S>
 __device__ __forceinline__ void tile(const Mxfp4Args& a, uint32_t g, uint32_t q0, uint32_t nq, uint32_t p0, uint8_t* lds) {
-    const uint32_t np = min(S::BP, a.n - p0), row = a.k / 2, scale_row = a.k / 32;
-    const size_t first = (size_t)(g == a.groups ? 0 : g) * a.n + p0;
-    const Operand q{a.x + (size_t)q0 * row, row, nq, a.xs + (size_t)q0 * scale_row};
-    const Operand p{a.w + first * row, row, np, a.ws + first * scale_row};
+    const Part<Out> t(a, g, q0, nq, p0, S::BP);
     f32x4_t acc[S::AQ][S::AP];
-    tile_sums<MmaMxfp4, kAlong, kAlong, S>(q, p, contraction(g == a.groups ? 0 : row / 2), lds, acc);
-    store_tile<Out, S>(acc, static_cast<Out*>(a.out) + (size_t)q0 * a.n + p0, a.n, nq, np, lds);
+    tile_sums<MmaMxfp4, kAlong, kAlong, S>(t.q, t.p, t.k, lds, acc);
+    store_tile<Out, S>(acc, t.out, a.n, t.nq, t.np, lds);
+}
+
+template <typename Out, typename S>
+__global__ __launch_bounds__(kNarrowWaves * 64) void mxfp4_narrow_kernel(Mxfp4Args a) {
+    __shared__ __attribute__((aligned(128))) uint8_t lds[S::kBytes];
+    GroupTile g;
+    uint32_t tp;
+    if (!find_even(a.counts, a.groups, a.rows, S::BQ, (a.n + S::BP - 1) / S::BP, &g, &tp)) return;
+    const Part<Out> t(a, g.group, g.row, g.rows, tp * S::BP, S::BP);
+    narrow_tile<MmaMxfp4, kAlong, kAlong, S>(t.q, t.p, t.k, lds, [&](uint32_t q, uint32_t p, const f32x4_t& v) {
+        if (q < t.nq && p < t.np) store4(v, t.out + (size_t)q * a.n + p, t.np - p, a.n % 4 == 0);
+    });
 }
 
 // large tiles, and small ones where these fill the chip better
@@ -120,6 +147,35 @@ hipError_t launch_tiled(const Mxfp4Args& a, hipStream_t stream) {
     return enqueue(mxfp4_kernel<Out>, dim3((uint32_t)wgs), dim3(kTileWaves * 64), stream, a);
 }
 
+template <typename Out, int QF, int PF, int Depth>
+hipError_t launch_narrow(const Mxfp4Args& a, hipStream_t stream) {
+    using S = NarrowOf<QF, PF, Depth, true>;
+    const uint64_t wgs = even_workgroups(most_tiles(a.counts, a.groups, a.rows, S::BQ) * ((a.n + (uint64_t)S::BP - 1) / S::BP));
+    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    return enqueue(mxfp4_narrow_kernel<Out, S>, dim3((uint32_t)wgs), dim3(kNarrowWaves * 64), stream, a);
+}
+
+// By the number of workgroups, one to a CU and 256 CUs.  Times in us with the weights in HBM, of 32 x 32 / 64 x 32 / 64 x 64
+// outputs / large and small tiles:
+//   up to 32 rows a group    32 x 32: 8192 x 8192, 1 row 9.2 / 9.9 / 12.8 / 25, 32 rows 10.7 / 11.2 / 14.8 / 28; over 8 weights of
+//                            7168 x 2048, 32 rows 15.6 / 18.3 / 15.9 / 26, 256 rows 21.5 / 30 / 29 / 35; over 32, 1024 rows
+//                            76 / 99 / 79 / 86
+//   more than 256 of 64 x 64 tiles: 8192 x 8192, 256 rows 47 / 44 / 33 / 35; 1216 x 1152 x 1000 - / - / 13.2 / 8.9; 2048 x 2048 x
+//                            2048 27 / 31 / 23 / 11.8
+//   more than 128            64 x 64: 128 rows 27 / 24 / 18.7 / 36; 777 x 1152 x 1001 7.7 / 8.8 / 7.4 / 12.6
+//   more than 128 of 64 x 32 64 x 32: 64 rows 16.4 / 14.9 / 18.5 / 31
+//   otherwise                32 x 32
+template <typename Out>
+hipError_t launch(const Mxfp4Args& a, hipStream_t stream) {
+    if (a.rows > 32ull * a.groups) {
+        const uint64_t high = most_tiles(a.counts, a.groups, a.rows, 64), wide = (a.n + 63ull) / 64;
+        if (high * wide > 256) return launch_tiled<Out>(a, stream);
+        if (high * wide > 128) return launch_narrow<Out, 4, 4, 2>(a, stream);
+        if (high * ((a.n + 31ull) / 32) > 128) return launch_narrow<Out, 4, 2, 2>(a, stream);
+    }
+    return launch_narrow<Out, 2, 2, 2>(a, stream);
+}
+
 }  // namespace
 
 hipError_t launch_mx_quantize(const void* x, int in_bf16, size_t n, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
@@ -141,7 +197,7 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, siz
 hipError_t launch_gemm_mxfp4(const uint8_t* x, const uint8_t* xs, size_t rows, size_t k, const uint8_t* w, const uint8_t* ws, size_t n,
                              int groups, const int32_t* counts, void* out, int out_bf16, hipStream_t stream) {
     const Mxfp4Args a{x, xs, w, ws, counts, out, (uint32_t)groups, (uint32_t)rows, (uint32_t)n, (uint32_t)k};
-    return out_bf16 ? launch_tiled<uint16_t>(a, stream) : launch_tiled<float>(a, stream);
+    return out_bf16 ? launch<uint16_t>(a, stream) : launch<float>(a, stream);
 }
 
 }  // namespace lpc

@@ -87,7 +87,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
-// 16 (4) bytes a lane from base + off to LDS at `to` + 16 (4) lane.  The compiler does not
+// 16 (4) bytes a lane from base + off, or from an address of its own, to LDS at `to` + 16 (4) lane.  The compiler does not
 // count these loads: lds_arrived() waits until at most `Left` of them are on their way.  M0 is read one wait state after it
 // is written, and is named as overwritten, so that no use of it by the compiler is carried across (the warning says that it
 // is not saved either).
@@ -98,6 +98,9 @@ __device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint3
 }
 __device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base) : "m0");
+}
+__device__ __forceinline__ void load_lds4_at(const void* from, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "m0");
 }
 #pragma clang diagnostic pop
 template <int Left>
@@ -536,6 +539,129 @@ __device__ __forceinline__ void tile_sums(const Operand& q_, const Operand& p_, 
 }
 
 // ---------------------------------------------------------------------------
+// narrow: 16 QF x 16 PF outputs per workgroup for few rows or few outputs.  Its four wavefronts take every fourth slab, each
+// through stages of LDS of its own that asynchronous loads fill Depth - 1 slabs ahead, and never wait for each other; their
+// sums are joined through LDS, in the wavefronts' order.
+// ---------------------------------------------------------------------------
+
+constexpr int kNarrowWaves = 4;
+
+// One wavefront's loads of all B rows (columns: 64) of an operand's slab; places in LDS are those of Loads.
+template <int F, int B>
+struct NarrowLoads {
+    static constexpr int N = B / 8;
+    const uint8_t* base;
+    size_t ld, step;
+    uint32_t off[F == kAlong ? 1 : 2], lr, n, count;
+
+    __device__ __forceinline__ NarrowLoads(const Operand& o, const Contraction& k, uint32_t lane)
+        : base(o.base), ld(o.ld), step(F == kAlong ? kSlab : kSlabRows * o.ld), lr(lane >> 3), n(o.n), count(k.count) {
+        static_assert(F == kAlong || B == 64, "columns of one run");
+        if constexpr (F == kAlong) {
+            off[0] = ((lane & 7) ^ lr) * 16;
+        } else {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) off[part] = min(((lane & 7) ^ (2 * ((lr >> 1 & 1) + 2 * part))) * 16, (o.n - 8) * 2);
+        }
+    }
+    // load i: rows (contraction rows) 8 i .. + 7
+    __device__ __forceinline__ void load(int i, uint32_t slab, bool last, uint32_t to) const {
+        const uint32_t row = min(8u * i, (F == kAlong ? n : last ? count : kSlabRows) - 1);
+        const uint32_t in = min(lr, (F == kAlong ? n : last ? count : kSlabRows) - 1 - row);
+        const uint32_t piece = F == kAlong ? (last ? min(off[0], (2 * count - 1) / 16 * 16) : off[0]) : off[F == kAlong ? 0 : i & 1];
+        load_lds16(base + slab * step + row * ld, in * (uint32_t)ld + piece, to + i * 1024);
+    }
+};
+
+template <int QF_, int PF_, int Depth_, bool Scaled>
+struct NarrowOf {
+    static constexpr int QF = QF_, PF = PF_, Depth = Depth_;
+    static constexpr uint32_t BQ = 16 * QF, BP = 16 * PF;
+    static constexpr uint32_t kStage = (BQ + BP) * (kSlab + (Scaled ? 8 : 0));
+    static constexpr uint32_t kRing = kNarrowWaves * Depth * kStage, kSums = kNarrowWaves * QF * PF * 1024;
+    static constexpr uint32_t kBytes = kRing > kSums ? kRing : kSums;
+    static constexpr bool kScaled = Scaled;
+    static_assert(!Scaled || (BQ + BP) % 32 == 0, "exponent bytes of 32 rows by one load");
+};
+
+// Calls store(row, column, sums) for each lane's four neighbouring outputs of each fragment of the tile, by one of the wavefronts.
+template <typename Mma, int FQ, int FP, typename S, typename Store>
+__device__ __forceinline__ void narrow_tile(const Operand& q_, const Operand& p_, const Contraction& k_, uint8_t* lds, Store store) {
+    constexpr int QF = S::QF, PF = S::PF, Depth = S::Depth;
+    constexpr uint32_t BQ = S::BQ, BP = S::BP;
+    constexpr int SLoads = Mma::kScaled ? (BQ + BP) / 32 : 0, kLoads = (BQ + BP) / 8 + SLoads, kAhead = (Depth - 1) * kLoads;
+    static_assert(Mma::kScaled == S::kScaled, "stages with exponent bytes");
+    const Operand q = scalar(q_), p = scalar(p_);
+    const Contraction k{scalar(k_.slabs), scalar(k_.count)};
+    const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    uint8_t* ring = lds + wave * Depth * S::kStage;
+    const NarrowLoads<FQ, BQ> lq(q, k, lane);
+    const NarrowLoads<FP, BP> lp(p, k, lane);
+    const bool cuts = k.count != kSlabRows;
+    // exponent bytes, 2 lanes a row, 32 rows of both operands together: each lane has an address of its own
+    const uint8_t* from[SLoads + 1];
+#pragma unroll
+    for (int n = 0; n < SLoads; ++n) {
+        const uint32_t row = n * 32 + lane / 2;
+        from[n] = (row < BQ ? q.scale + min(row, q.n - 1) * (q.ld / 16) : p.scale + min(row - BQ, p.n - 1) * (p.ld / 16)) + (lane & 1) * 4;
+    }
+    auto load_slab = [&](uint32_t c, uint32_t stage) {
+        const uint32_t to = lds_address(ring) + stage * S::kStage;
+        const bool last = cuts && c + 1 == k.slabs;
+#pragma unroll
+        for (uint32_t i = 0; i < BQ / 8; ++i) lq.load(i, c, last, to);
+#pragma unroll
+        for (uint32_t i = 0; i < BP / 8; ++i) lp.load(i, c, last, to + BQ * kSlab);
+#pragma unroll
+        for (int n = 0; n < SLoads; ++n) load_lds4_at(from[n] + c * 8 - (last ? (lane & 1) * 4 : 0), to + (BQ + BP) * kSlab + n * 256);
+    };
+
+    f32x4_t acc[QF][PF];
+    clear(acc);
+    const uint32_t mine = wave < k.slabs ? (k.slabs - wave + kNarrowWaves - 1) / kNarrowWaves : 0;  // slabs
+#pragma unroll
+    for (uint32_t d = 0; d + 1 < Depth; ++d)
+        if (d < mine) load_slab(wave + d * kNarrowWaves, d);
+    const Reader<FQ> rq(lane);
+    const Reader<FP> rp(lane);
+    uint32_t stage = 0;
+    for (uint32_t i = 0; i < mine; ++i) {
+        // into the stage that was read last; those reads are in registers
+        if (i + Depth - 1 < mine) {
+            load_slab(wave + (i + Depth - 1) * kNarrowWaves, stage == 0 ? Depth - 1 : stage - 1);
+            lds_arrived<kAhead>();
+        } else {
+            lds_arrived<0>();
+        }
+        const uint8_t* s = ring + stage * S::kStage;
+        const uint8_t* bytes = s + (BQ + BP) * kSlab;
+        Fragments<Mma, FQ, QF> qv;
+        Fragments<Mma, FP, PF> pv;
+        pv.read(rp, s + BQ * kSlab, 0, bytes + BQ * 8, lane);
+        if (cuts && wave + i * kNarrowWaves + 1 == k.slabs) pv.cut(lane, k.count);
+        qv.read(rq, s, 0, bytes, lane);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        multiply<Mma>(acc, qv, pv);
+        stage = stage + 1 == Depth ? 0 : stage + 1;
+    }
+
+    __syncthreads();
+    f32x4_t(*sums)[QF * PF][64] = reinterpret_cast<f32x4_t(*)[QF * PF][64]>(lds);
+#pragma unroll
+    for (int i = 0; i < QF; ++i)
+#pragma unroll
+        for (int j = 0; j < PF; ++j) sums[wave][i * PF + j][lane] = acc[i][j];
+    __syncthreads();
+    for (uint32_t f = wave; f < QF * PF; f += kNarrowWaves) {
+        f32x4_t v = sums[0][f][lane];
+#pragma unroll
+        for (int n = 1; n < kNarrowWaves; ++n) v += sums[n][f][lane];
+        store(f / PF * 16 + l16, f % PF * 16 + 4 * l4, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // stores
 // ---------------------------------------------------------------------------
 
@@ -554,6 +680,13 @@ __device__ __forceinline__ void store_some(const f32x4_t& v, Out* o, uint32_t le
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i)
         if (i < left) o[i] = t[i];
+}
+
+// four of them where all exist and are aligned, else `left`
+template <typename Out>
+__device__ __forceinline__ void store4(const f32x4_t& v, Out* o, uint32_t left, bool wide) {
+    if (wide) pack4(v, o);
+    else store_some(v, o, left);
 }
 
 // Stores a tile's sums to out (its first row and column), ldo elements between rows, nq x np of them.  After tile_sums by
@@ -669,11 +802,26 @@ uint64_t shares(uint64_t most_tiles) {
     return kXcds * ((most_tiles + kXcds - 1) / kXcds + kMostSplit * (Parts - 1));
 }
 
-// Tiles of T rows that any counts can make of `rows` rows in `groups` groups and the rows past them: every group and the
-// rest may end in a short tile.
+// Tiles of T rows that any counts can make of `rows` rows in `groups` groups and the rows past them: a group without rows has
+// none, and each of the others may end in a short one.
 inline uint64_t most_tiles(const int32_t* counts, uint32_t groups, uint32_t rows, uint32_t T) {
-    return (rows + (uint64_t)T - 1) / T + (counts ? groups : 0);
+    const uint64_t parts = counts ? (groups < rows ? groups + 1ull : rows) : 1;
+    return (rows + parts * (T - 1)) / T;
 }
+
+// One of the tiles of T rows by outputs that there are (no more than the launch has workgroups), spread evenly over the XCDs,
+// each of which has a run of them.  false: none is left.
+__device__ __forceinline__ bool find_even(const int32_t* counts, uint32_t groups, uint32_t rows, uint32_t T, uint32_t tiles_p, GroupTile* w,
+                                          uint32_t* tp) {
+    const TileScan tiles(counts, groups, rows, T);
+    const uint32_t all = tiles.all * tiles_p, rest = all % kXcds, x = blockIdx.x % kXcds, k = blockIdx.x / kXcds;
+    if (k >= all / kXcds + (x < rest)) return false;
+    const uint32_t n = x * (all / kXcds) + min(x, rest) + k;
+    *w = tiles.find(n / tiles_p);
+    *tp = n % tiles_p;
+    return true;
+}
+inline uint64_t even_workgroups(uint64_t tiles) { return (tiles + kXcds - 1) / kXcds * kXcds; }
 
 // The group with the z-th most rows, for up to 64 groups: their tiles take times that differ as their rows do, and the
 // long ones come first, so that short ones fill the end.
