@@ -675,7 +675,13 @@ class AdamW:
              self.state_bits, step, lr, beta1, beta2, eps, weight_decay, p.optional(grad_scale, "grad_scale", _F32, 1))
 
 
-_BF = (torch.bfloat16,)
+_b2, _BF = torch.bfloat16, (torch.bfloat16,)
+
+
+def _usual_counts(counts, device):
+    return counts is None or (counts.dtype is _i4 and counts.is_contiguous() and counts.get_device() == device)
+
+
 MX = 32  # elements of a microscaled block
 
 
@@ -694,6 +700,17 @@ def _expect2(t, what, shape):
 def lpc_gemm_bf16(x, w, out, counts=None, stream=None):
     """out [rows, n] (fp32 or bf16) = x [rows, k] times w [groups, n, k] (or [n, k]) transposed, bf16; counts [groups] int32:
     rows of each group."""
+    try:  # the usual call in one expression, as in lpc_gemm_fp8
+        (rows, k), (n, kw), device = x.shape, w.shape[-2:], x.get_device()
+        groups = 1 if counts is None else counts.numel()
+        usual = (stream is None and device >= 0 and kw == k and out.shape == (rows, n) and w.numel() == groups * n * k and w.dim() < 4
+                 and x.dtype is _b2 and w.dtype is _b2 and x.is_contiguous() and w.is_contiguous() and out.is_contiguous()
+                 and w.get_device() == device and out.get_device() == device and _usual_counts(counts, device))
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if usual:
+        return _run("lpc_gemm_bf16", device, None, x.data_ptr(), rows, k, w.data_ptr(), n, groups,
+                    None if counts is None else counts.data_ptr(), out.data_ptr(), _dtype(out))
     (rows, k), groups = _shape2(x, "x"), _groups(counts)
     n, kw = _grouped_weight(w, groups)
     if kw != k:
@@ -708,6 +725,17 @@ def lpc_gemm_bf16(x, w, out, counts=None, stream=None):
 def lpc_gemm_bf16_dgrad(dy, w, dx, counts=None, stream=None):
     """dx [rows, k] (fp32 or bf16) = dy [rows, n] times w [groups, n, k] (or [n, k]), bf16: the gradient of lpc_gemm_bf16's
     rows."""
+    try:  # the usual call in one expression, as in lpc_gemm_fp8
+        (rows, n), (nw, k), device = dy.shape, w.shape[-2:], dy.get_device()
+        groups = 1 if counts is None else counts.numel()
+        usual = (stream is None and device >= 0 and nw == n and dx.shape == (rows, k) and w.numel() == groups * n * k and w.dim() < 4
+                 and dy.dtype is _b2 and w.dtype is _b2 and dy.is_contiguous() and w.is_contiguous() and dx.is_contiguous()
+                 and w.get_device() == device and dx.get_device() == device and _usual_counts(counts, device))
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if usual:
+        return _run("lpc_gemm_bf16_dgrad", device, None, dy.data_ptr(), rows, n, w.data_ptr(), k, groups,
+                    None if counts is None else counts.data_ptr(), dx.data_ptr(), _dtype(dx))
     (rows, n), groups = _shape2(dy, "dy"), _groups(counts)
     nw, k = _grouped_weight(w, groups)
     if nw != n:
@@ -722,6 +750,17 @@ def lpc_gemm_bf16_dgrad(dy, w, dx, counts=None, stream=None):
 def lpc_gemm_bf16_wgrad(dy, x, dw, counts=None, stream=None):
     """dw [groups, n, k] (or [n, k]; fp32 or bf16) = each group's rows of dy [rows, n] transposed times those of x [rows, k],
     bf16: the gradient of lpc_gemm_bf16's weights."""
+    try:  # the usual call in one expression, as in lpc_gemm_fp8
+        (rows, n), (nw, k), device = dy.shape, dw.shape[-2:], dy.get_device()
+        groups = 1 if counts is None else counts.numel()
+        usual = (stream is None and device >= 0 and nw == n and x.shape == (rows, k) and dw.numel() == groups * n * k and dw.dim() < 4
+                 and dy.dtype is _b2 and x.dtype is _b2 and dy.is_contiguous() and x.is_contiguous() and dw.is_contiguous()
+                 and x.get_device() == device and dw.get_device() == device and _usual_counts(counts, device))
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if usual:
+        return _run("lpc_gemm_bf16_wgrad", device, None, dy.data_ptr(), n, x.data_ptr(), k, rows, groups,
+                    None if counts is None else counts.data_ptr(), dw.data_ptr(), _dtype(dw))
     (rows, n), groups = _shape2(dy, "dy"), _groups(counts)
     _expect2(x, "x", (rows, _grouped_weight(dw, groups, "dw")[1]))
     if dw.shape[-2] != n:
@@ -734,6 +773,15 @@ def lpc_gemm_bf16_wgrad(dy, x, dw, counts=None, stream=None):
 
 def lpc_quantize_mxfp4(x, codes, scales, stream=None):
     """E2M1 codes (two to a byte) and exponent bytes, one per 32 elements, of x (fp32 or bf16, a multiple of 32 elements)."""
+    try:  # the usual call in one expression, as in lpc_gemm_fp8
+        n, device = x.numel(), x.get_device()
+        usual = (stream is None and device >= 0 and codes.numel() * 2 == n and scales.numel() == n // MX and codes.dtype is _u8
+                 and scales.dtype is _u8 and x.is_contiguous() and codes.is_contiguous() and scales.is_contiguous()
+                 and codes.get_device() == device and scales.get_device() == device)
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if usual:
+        return _run("lpc_quantize_mxfp4", device, None, x.data_ptr(), _dtype(x), n, codes.data_ptr(), scales.data_ptr())
     p = _Args()
     address, n = p(x, "x", _FB, 0), x.numel()
     args = (address, _dtype(x), n, p(codes, "codes", _U8, n // 2, True), p(scales, "scales", _U8, n // MX, True))
@@ -751,6 +799,20 @@ def lpc_dequantize_mxfp4(codes, scales, out, stream=None):
 def lpc_gemm_mxfp4(x, xs, w, ws, out, counts=None, stream=None):
     """out [rows, n] (fp32 or bf16) = x [rows, k] times w [groups, n, k] (or [n, k]) transposed, held as E2M1 codes x [rows, k/2],
     w [groups, n, k/2] with exponent bytes xs [rows, k/32], ws [groups, n, k/32]; counts [groups] int32: rows of each group."""
+    try:  # the usual call in one expression, as in lpc_gemm_fp8
+        (rows, half), (n, hw), device = x.shape, w.shape[-2:], x.get_device()
+        groups, blocks = 1 if counts is None else counts.numel(), half // 16
+        usual = (stream is None and device >= 0 and hw == half and out.shape == (rows, n) and w.numel() == groups * n * half and w.dim() < 4
+                 and xs.numel() == rows * blocks and ws.numel() == groups * n * blocks
+                 and x.dtype is _u8 and w.dtype is _u8 and xs.dtype is _u8 and ws.dtype is _u8
+                 and x.is_contiguous() and w.is_contiguous() and xs.is_contiguous() and ws.is_contiguous() and out.is_contiguous()
+                 and w.get_device() == device and xs.get_device() == device and ws.get_device() == device
+                 and out.get_device() == device and _usual_counts(counts, device))
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if usual:
+        return _run("lpc_gemm_mxfp4", device, None, x.data_ptr(), xs.data_ptr(), rows, 2 * half, w.data_ptr(), ws.data_ptr(), n, groups,
+                    None if counts is None else counts.data_ptr(), out.data_ptr(), _dtype(out))
     (rows, half), groups = _shape2(x, "x"), _groups(counts)
     n, hw = _grouped_weight(w, groups)
     if hw != half:

@@ -163,7 +163,8 @@ def test_bf16_wgrad_groups(dev, rows, k, n, counts, dtype):
     check_wgrad(dev, rows, k, n, counts, dtype)
 
 
-@pytest.mark.parametrize("rows,k,n,counts", [(2100, 1152, 1160, None), (3001, 648, 1304, [5, 1500, 0, 900]), (4500, 520, 2048, None)])
+@pytest.mark.parametrize("rows,k,n,counts", [(2100, 1152, 1160, None), (3001, 648, 1304, [5, 1500, 0, 900]), (4500, 520, 2048, None),
+                                             (3000, 264, 3016, None), (3500, 264, 3016, [1100, 300, 1700]), (300, 3848, 2056, None)])
 def test_bf16_large(dev, rows, k, n, counts):
     """More tiles than one round of the chip's CUs in some of them; every form."""
     check_product(dev, rows, k, n - 1, counts, BF16)
@@ -299,7 +300,7 @@ def check_mxfp4(dev, rows, k, n, counts, dtype):
 
 
 MXFP4 = [(1, 128, 1), (1, 8192, 512), (2, 384, 130), (15, 1152, 127), (16, 256, 128), (17, 640, 1000), (33, 896, 257),
-         (64, 2048, 384), (65, 1152, 129), (129, 128, 255), (257, 640, 300), (300, 1152, 1000), (777, 512, 513), (2100, 1152, 1153)]
+         (64, 2048, 384), (65, 1152, 129), (129, 128, 255), (257, 640, 300), (300, 1152, 1000), (777, 512, 513), (2100, 1152, 1153), (3000, 256, 3001)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
