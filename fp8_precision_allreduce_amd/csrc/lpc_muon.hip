@@ -40,31 +40,55 @@ __device__ __forceinline__ Space space_of(const MuonMatrix& m, uint8_t* w) {
 
 constexpr uint32_t kChunkLanes = 256;
 
-typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint16_t u16x4u_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x8_t __attribute__((ext_vector_type(8)));
+// a tensor's matrices start at any element
+typedef float f32x8u_t __attribute__((ext_vector_type(8), aligned(4)));
+typedef uint16_t u16x8u_t __attribute__((ext_vector_type(8), aligned(2)));
 
-// four elements from i on, fewer at a matrix's end (0 for the others); matrices of a tensor start at any element
-__device__ __forceinline__ f32x4_t load4(const float* p, size_t i, size_t n) {
-    if (i + 4 <= n) return *reinterpret_cast<const f32x4u_t*>(p + i);
-    f32x4_t v = {};
+// A workgroup's chunk of X: runs of 8 elements of its rows, which are padded to whole runs (to ldx, with zeros).
+struct Runs {
+    uint32_t width;  // runs of a row
+    uint32_t row, run;
+    uint32_t all;    // of the chunk
+
+    __device__ __forceinline__ Runs(const MuonMatrix& x, uint32_t chunk) : width(x.ldx / 8) {
+        const uint64_t first = (uint64_t)chunk * (kMuonChunk / 8), end = (uint64_t)x.rows * width;
+        row = (uint32_t)(first / width);
+        run = (uint32_t)(first - (uint64_t)row * width);
+        all = (uint32_t)min(end - first, (uint64_t)(kMuonChunk / 8));
+    }
+    // run i's row, first column and how many of its elements there are in the matrix
+    __device__ __forceinline__ void place(const MuonMatrix& x, uint32_t i, uint32_t* r, uint32_t* col, uint32_t* left) const {
+        const uint32_t n = run + i, more = n / width;
+        *r = row + more;
+        *col = (n - more * width) * 8;
+        *left = *col < x.cols ? min(x.cols - *col, 8u) : 0;
+    }
+};
+
+__device__ __forceinline__ f32x8_t load8(const float* p, uint32_t left) {
+    if (left == 8) return *reinterpret_cast<const f32x8u_t*>(p);
+    f32x8_t v = {};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = i + e < n ? p[i + e] : 0.0f;
+    for (uint32_t e = 0; e < 8; ++e)
+        if (e < left) v[e] = p[e];
     return v;
 }
-__device__ __forceinline__ f32x4_t load4(const uint16_t* p, size_t i, size_t n) {
-    f32x4_t v = {};
-    if (i + 4 <= n) {
-        const u16x4u_t h = *reinterpret_cast<const u16x4u_t*>(p + i);
+__device__ __forceinline__ f32x8_t load8(const uint16_t* p, uint32_t left) {
+    f32x8_t v = {};
+    if (left == 8) {
+        const u16x8u_t h = *reinterpret_cast<const u16x8u_t*>(p);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = bf16lo(h[e]);
+        for (int e = 0; e < 8; ++e) v[e] = bf16lo(h[e]);
         return v;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = i + e < n ? bf16lo(p[i + e]) : 0.0f;
+    for (uint32_t e = 0; e < 8; ++e)
+        if (e < left) v[e] = bf16lo(p[e]);
     return v;
 }
 
-__device__ __forceinline__ f32x4_t update_of(f32x4_t m, f32x4_t g, const MuonScalars& s) {
+__device__ __forceinline__ f32x8_t update_of(f32x8_t m, f32x8_t g, const MuonScalars& s) {
     return s.nesterov ? g * s.rest + m * s.beta : m;
 }
 
@@ -85,23 +109,27 @@ __global__ __launch_bounds__(kChunkLanes) void muon_momentum_kernel(MuonPlan pla
     __shared__ double lds[kChunkLanes / 64];
     const MuonPiece piece = plan.chunks[blockIdx.x];
     const MuonMatrix& x = plan.matrices[piece.matrix];
-    const size_t n = (size_t)x.rows * x.cols;
+    const Runs runs(x, piece.index);
     const Grad* grad = static_cast<const Grad*>(x.grad);
     const float scale = grad_scale ? grad_scale[0] : 1.0f;
     double sum = 0.0;
-    for (size_t i = (size_t)piece.index * kMuonChunk + threadIdx.x * 4; i < min(n, ((size_t)piece.index + 1) * kMuonChunk); i += kChunkLanes * 4) {
-        const f32x4_t g = load4(grad, i, n) * scale;
-        const f32x4_t m = load4(x.m, i, n) * s.beta + g * s.rest;
-        if (i + 4 <= n) {
-            *reinterpret_cast<f32x4u_t*>(x.m + i) = m;
+#pragma unroll 2
+    for (uint32_t i = threadIdx.x; i < runs.all; i += kChunkLanes) {
+        uint32_t row, col, left;
+        runs.place(x, i, &row, &col, &left);
+        if (left == 0) continue;
+        const size_t at = (size_t)row * x.cols + col;
+        const f32x8_t g = load8(grad + at, left) * scale, m = load8(x.m + at, left) * s.beta + g * s.rest;
+        if (left == 8) {
+            *reinterpret_cast<f32x8u_t*>(x.m + at) = m;
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (i + e < n) x.m[i + e] = m[e];
+            for (uint32_t e = 0; e < 8; ++e)
+                if (e < left) x.m[at + e] = m[e];
         }
-        const f32x4_t u = update_of(m, g, s);
+        const f32x8_t u = update_of(m, g, s);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum += (double)u[e] * (double)u[e];
+        for (int e = 0; e < 8; ++e) sum += (double)u[e] * (double)u[e];
     }
     const double all = workgroup_sum(sum, lds);
     if (threadIdx.x == 0) space_of(x, space).partial[piece.index] = all;
@@ -114,30 +142,29 @@ __global__ __launch_bounds__(kChunkLanes) void muon_start_kernel(MuonPlan plan, 
     const MuonPiece piece = plan.chunks[blockIdx.x];
     const MuonMatrix& x = plan.matrices[piece.matrix];
     const Space w = space_of(x, space);
-    const size_t n = (size_t)x.rows * x.cols;
-    const uint32_t chunks = (uint32_t)((n + kMuonChunk - 1) / kMuonChunk);
+    const Runs runs(x, piece.index);
+    const uint32_t chunks = (uint32_t)(((uint64_t)x.rows * x.ldx + kMuonChunk - 1) / kMuonChunk);
     double sum = 0.0;
     for (uint32_t c = threadIdx.x; c < chunks; c += kChunkLanes) sum += w.partial[c];
     const double norm = sqrt(workgroup_sum(sum, lds)), by = norm > 0.0 ? (double)kHeld / norm : 0.0;
     const Grad* grad = static_cast<const Grad*>(x.grad);
     const float scale = grad_scale ? grad_scale[0] : 1.0f;
-    for (size_t i = (size_t)piece.index * kMuonChunk + threadIdx.x * 4; i < min(n, ((size_t)piece.index + 1) * kMuonChunk); i += kChunkLanes * 4) {
-        const f32x4_t u = update_of(load4(x.m, i, n), load4(grad, i, n) * scale, s);
-        uint32_t row = (uint32_t)(i / x.cols), col = (uint32_t)(i - (size_t)row * x.cols);
+#pragma unroll 2
+    for (uint32_t i = threadIdx.x; i < runs.all; i += kChunkLanes) {
+        uint32_t row, col, left;
+        runs.place(x, i, &row, &col, &left);
+        const size_t at = (size_t)row * x.cols + col, to = (size_t)row * x.ldx + col;
+        f16x8_t high = {}, low = {};
+        if (left != 0) {
+            const f32x8_t u = update_of(load8(x.m + at, left), load8(grad + at, left) * scale, s);
+            f32x8_t v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (i + e >= n) break;
-            const float v = (float)((double)u[e] * by);
-            const _Float16 high = (_Float16)v;
-            const size_t at = (size_t)row * x.ldx + col;
-            w.high[0][at] = high;
-            w.low[at] = (_Float16)((v - (float)high) * kLow);
-            if (++col == x.cols) {
-                for (size_t z = at + 1; col < x.ldx; ++col, ++z) w.high[0][z] = w.low[z] = (_Float16)0.0f;
-                col = 0;
-                ++row;
-            }
+            for (int e = 0; e < 8; ++e) v[e] = (float)((double)u[e] * by);
+            high = __builtin_convertvector(v, f16x8_t);
+            low = __builtin_convertvector((v - __builtin_convertvector(high, f32x8_t)) * kLow, f16x8_t);
         }
+        *reinterpret_cast<f16x8_t*>(w.high[0] + to) = high;
+        *reinterpret_cast<f16x8_t*>(w.low + to) = low;
     }
 }
 
@@ -153,42 +180,88 @@ __device__ __forceinline__ Operand operand(const _Float16* first, uint32_t ld, u
     return {reinterpret_cast<const uint8_t*>(first), (size_t)ld * 2, n, nullptr};
 }
 
-// f(sums, row, column) for each of a lane's four neighbouring elements of a tile
-template <typename S, typename F>
-__device__ __forceinline__ void each_place(f32x4_t (&acc)[S::AQ][S::AP], F f) {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t q = S::q0(wave) + (lane & 15), p = S::p0(wave) + 4 * (lane >> 4);
-#pragma unroll
-    for (int i = 0; i < S::AQ; ++i)
-#pragma unroll
-        for (int j = 0; j < S::AP; ++j) f(acc[i][j], q + 16 * i, p + 16 * j);
+__device__ __forceinline__ f16x8_t low_of(const f32x8_t& v, const f16x8_t& high) {
+    return __builtin_convertvector((v - __builtin_convertvector(high, f32x8_t)) * kLow, f16x8_t);
 }
 
-__device__ __forceinline__ f32x4_t halves(const _Float16* p) { return __builtin_convertvector(*reinterpret_cast<const f16x4_t*>(p), f32x4_t); }
+// Zeros from column `np` of a matrix on.
+__device__ __forceinline__ void cut_columns(f32x8_t& v, uint32_t p, uint32_t np) {
+#pragma unroll
+    for (uint32_t e = 0; e < 8; ++e)
+        if (p + e >= np) v[e] = 0.0f;
+}
 
-// Stores a tile's sums with rows and columns exchanged: nq columns, np rows from out on.  Through LDS like store_tile.
-template <typename S>
-__device__ __forceinline__ void store_turned(const f32x4_t (&acc)[S::AQ][S::AP], _Float16* out, size_t ldo, uint32_t nq, uint32_t np, uint8_t* lds) {
-    constexpr int FS = S::AQ < 4 ? S::AQ : 4;
-    constexpr uint32_t kPitch = 16 * FS * 2 + 16, kLanes = 2 * FS;
-    static_assert(kTileWaves * S::PW * kPitch <= S::kBytes, "LDS for the outputs");
+// Goes through a tile's sums in runs of 8 columns of one row, nq x np of them (np a multiple of 64): load(q, p) brings what a run
+// needs, use(q, p, sums, that) ends it.  Sums reach the lanes of their runs through LDS, 32 rows at a time, so that everything
+// else is read and written whole lines at a time; loads are under way while those of the rows before are used.  A wavefront has a
+// part of LDS of its own; rows are 16 bytes further apart than they are long, which spreads them over the banks.
+template <typename S, typename Load, typename Use>
+__device__ __forceinline__ void each_run(const f32x4_t (&acc)[S::AQ][S::AP], uint32_t nq, uint32_t np, uint8_t* lds, Load load, Use use) {
+    constexpr uint32_t kPitchF = S::PW * 4 + 16, kRows = 32, kSteps = kRows / 8;
+    static_assert(S::PW == 64 && kTileWaves * kRows * kPitchF <= S::kBytes, "8 lanes a row");
     const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    uint8_t* own = lds + wave * S::PW * kPitch;
+    const uint32_t q0 = S::q0(wave) + lane / 8, p = S::p0(wave) + lane % 8 * 8;
+    if (S::p0(wave) >= np) return;
+    uint8_t* own = lds + wave * kRows * kPitchF;
+    using Loaded = decltype(load(0u, 0u));
+    Loaded next[kSteps];
+    auto bring = [&](int f) {
+#pragma unroll
+        for (uint32_t r = 0; r < kSteps; ++r)
+            if (q0 + f * 16 + r * 8 < nq) next[r] = load(q0 + f * 16 + r * 8, p);
+    };
+    bring(0);
+#pragma unroll
+    for (int f = 0; f < S::AQ; f += 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < S::AP; ++j) *reinterpret_cast<f32x4_t*>(own + (16 * i + l16) * kPitchF + (16 * j + 4 * l4) * 4) = acc[f + i][j];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        Loaded now[kSteps];
+        f32x8_t v[kSteps];
+#pragma unroll
+        for (uint32_t r = 0; r < kSteps; ++r) {
+            now[r] = next[r];
+            const f32x4_t* at = reinterpret_cast<const f32x4_t*>(own + (r * 8 + lane / 8) * kPitchF + lane % 8 * 32);
+            v[r] = __builtin_shufflevector(at[0], at[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+        if (f + 2 < S::AQ) bring(f + 2);
+#pragma unroll
+        for (uint32_t r = 0; r < kSteps; ++r)
+            if (q0 + f * 16 + r * 8 < nq) use(q0 + f * 16 + r * 8, p, v[r], now[r]);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+}
+
+// Stores value(sums, q, p) of a tile with rows and columns exchanged: nq columns, np rows from out on.  Through LDS like each_run.
+template <typename S, typename Value>
+__device__ __forceinline__ void store_turned(const f32x4_t (&acc)[S::AQ][S::AP], _Float16* out, size_t ldo, uint32_t nq, uint32_t np, uint8_t* lds,
+                                             Value value) {
+    constexpr int FS = S::AQ < 4 ? S::AQ : 4;
+    constexpr uint32_t kPitchH = 16 * FS * 2 + 16, kLanes = 2 * FS;
+    static_assert(kTileWaves * S::PW * kPitchH <= S::kBytes, "LDS for the outputs");
+    const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    uint8_t* own = lds + wave * S::PW * kPitchH;
 #pragma unroll
     for (int f = 0; f < S::AQ; f += FS) {
 #pragma unroll
         for (int i = 0; i < FS; ++i)
 #pragma unroll
-            for (int j = 0; j < S::AP; ++j)
+            for (int j = 0; j < S::AP; ++j) {
+                const uint32_t q = S::q0(wave) + 16 * (f + i) + l16, p = S::p0(wave) + 16 * j + 4 * l4;
+                const f32x4_t v = value(acc[f + i][j], q, p);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<_Float16*>(own + (16 * j + 4 * l4 + e) * kPitch + (16 * i + l16) * 2) = (_Float16)acc[f + i][j][e];
+                    *reinterpret_cast<_Float16*>(own + (16 * j + 4 * l4 + e) * kPitchH + (16 * i + l16) * 2) = (_Float16)v[e];
+            }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
         for (uint32_t r = 0; r < S::PW; r += 64 / kLanes) {
             const uint32_t row = r + lane / kLanes, col = lane % kLanes;
-            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + row * kPitch + col * 16);
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + row * kPitchH + col * 16);
             const uint32_t p = S::p0(wave) + row, q = S::q0(wave) + f * 16 + col * 8;
             if (q < nq && p < np) *reinterpret_cast<u32x4_t*>(out + p * ldo + q) = v;
         }
@@ -213,18 +286,24 @@ __device__ __forceinline__ void square_tile(const MuonMatrix& x, const Space& w,
         tile_sums<MmaF16, kAlong, kAlong, S>(operand(w.high[from] + (size_t)q0 * x.ldx, x.ldx, nq),
                                              operand(w.high[from] + (size_t)p0 * x.ldx, x.ldx, np), contraction(x.cols), lds, acc);
     }
-    each_place<S>(acc, [&](f32x4_t& v, uint32_t q, uint32_t p) {
-        v = v * (1.0f / kHeld);
-        if (Second) v = v * kC + (q < nq && p < np ? halves(w.a + (size_t)(q0 + q) * x.lda + p0 + p) : f32x4_t{}) * kB;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (q >= nq || p + e >= np) v[e] = 0.0f;
-    });
     _Float16* out = Second ? w.b : w.a;
-    store_tile<_Float16, S>(acc, out + (size_t)q0 * x.lda + p0, x.lda, nq, min(S::BP, x.lda - p0), lds);
+    const _Float16* a = w.a + (size_t)q0 * x.lda + p0;
+    each_run<S>(acc, nq, min(S::BP, x.lda - p0), lds,
+                [&](uint32_t q, uint32_t p) { return Second ? *reinterpret_cast<const f16x8_t*>(a + (size_t)q * x.lda + p) : f16x8_t{}; },
+                [&](uint32_t q, uint32_t p, f32x8_t v, const f16x8_t& now) {
+                    v = v * (1.0f / kHeld);
+                    if (Second) v = v * kC + __builtin_convertvector(now, f32x8_t) * kB;
+                    cut_columns(v, p, np);
+                    *reinterpret_cast<f16x8_t*>(out + (size_t)(q0 + q) * x.lda + p0 + p) = __builtin_convertvector(v, f16x8_t);
+                });
     if (q0 == p0) return;
     __syncthreads();  // the wavefronts' parts of LDS are others now
-    store_turned<S>(acc, out + (size_t)p0 * x.lda + q0, x.lda, min(S::BQ, x.lda - q0), np, lds);
+    store_turned<S>(acc, out + (size_t)p0 * x.lda + q0, x.lda, min(S::BQ, x.lda - q0), np, lds, [&](f32x4_t v, uint32_t q, uint32_t p) {
+        v = v * (1.0f / kHeld);
+        if (q >= nq || p >= np) return f32x4_t{};
+        if (Second) v = v * kC + __builtin_convertvector(*reinterpret_cast<const f16x4_t*>(a + (size_t)q * x.lda + p), f32x4_t) * kB;
+        return v;
+    });
 }
 
 // Rows from q0 and columns from p0 of X = a X + B X (tall: X B); Last: of the parameters with it.
@@ -240,43 +319,49 @@ __device__ __forceinline__ void update_tile(const MuonMatrix& x, const Space& w,
     else
         tile_sums<MmaF16, kAlong, kAcross, S>(operand(w.b + (size_t)q0 * x.lda, x.lda, nq), operand(high + p0, x.ldx, min(S::BP, x.ldx - p0)),
                                               contraction(x.rows), lds, acc);
-    each_place<S>(acc, [&](f32x4_t& v, uint32_t q, uint32_t p) {
-        if (q >= nq || p >= np) {
-            v = f32x4_t{};
-            return;
-        }
-        const size_t at = (size_t)(q0 + q) * x.ldx + p0 + p;
-        v = v * (1.0f / kHeld) + (halves(high + at) + halves(w.low + at) * (1.0f / kLow)) * kA;
+    struct Halves {
+        f16x8_t high, low;
+    };
+    const size_t first = (size_t)q0 * x.ldx + p0;
+    const float rate = s.lr * x.scale * (1.0f / kHeld);
+    each_run<S>(acc, nq, min(S::BP, x.ldx - p0), lds,
+                [&](uint32_t q, uint32_t p) {
+                    const size_t at = first + (size_t)q * x.ldx + p;
+                    return Halves{*reinterpret_cast<const f16x8_t*>(high + at), *reinterpret_cast<const f16x8_t*>(w.low + at)};
+                },
+                [&](uint32_t q, uint32_t p, f32x8_t v, const Halves& now) {
+                    v = v * (1.0f / kHeld) + (__builtin_convertvector(now.high, f32x8_t) + __builtin_convertvector(now.low, f32x8_t) * (1.0f / kLow)) * kA;
+                    if (!Last) {
+                        cut_columns(v, p, np);
+                        const size_t at = first + (size_t)q * x.ldx + p;
+                        const f16x8_t h = __builtin_convertvector(v, f16x8_t);
+                        *reinterpret_cast<f16x8_t*>(w.high[1 - from] + at) = h;
+                        *reinterpret_cast<f16x8_t*>(w.low + at) = low_of(v, h);
+                        return;
+                    }
+                    const size_t at = (size_t)(q0 + q) * x.cols + p0 + p;
+                    if (p + 8 <= np) {
+                        const f32x8u_t param = *reinterpret_cast<const f32x8u_t*>(x.param + at);
+                        const f32x8_t value = f32x8_t(param) * s.keep - v * rate;
+                        *reinterpret_cast<f32x8u_t*>(x.param + at) = value;
+                        if (x.copy) {
+                            u16x8u_t c;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (p + e >= np) v[e] = 0.0f;
-        if (Last) {
-            const size_t out = (size_t)(q0 + q) * x.cols + p0 + p;
-            const float rate = s.lr * x.scale * (1.0f / kHeld);
-            if (p + 4 <= np) {
-                const f32x4_t now = *reinterpret_cast<const f32x4u_t*>(x.param + out) * s.keep - v * rate;
-                *reinterpret_cast<f32x4u_t*>(x.param + out) = now;
-                if (x.copy) {
-                    const u32x2_t c = {pack_bf16x2(now[0], now[1]), pack_bf16x2(now[2], now[3])};
-                    *reinterpret_cast<u16x4u_t*>(x.copy + out) = __builtin_bit_cast(u16x4u_t, c);
-                }
-            } else {
-#pragma unroll
-                for (uint32_t e = 0; e < 4; ++e) {
-                    if (p + e >= np) break;
-                    const float now = x.param[out + e] * s.keep - v[e] * rate;
-                    x.param[out + e] = now;
-                    if (x.copy) x.copy[out + e] = (uint16_t)pack_bf16x2(now, now);
-                }
-            }
-        }
-    });
-    if (Last) return;
-    const uint32_t wide = min(S::BP, x.ldx - p0);
-    const size_t at = (size_t)q0 * x.ldx + p0;
-    store_tile<_Float16, S>(acc, w.high[1 - from] + at, x.ldx, nq, wide, lds);
-    each_place<S>(acc, [&](f32x4_t& v, uint32_t, uint32_t) { v = (v - __builtin_convertvector(__builtin_convertvector(v, f16x4_t), f32x4_t)) * kLow; });
-    store_tile<_Float16, S>(acc, w.low + at, x.ldx, nq, wide, lds);
+                            for (int e = 0; e < 8; e += 2) {
+                                const uint32_t two = pack_bf16x2(value[e], value[e + 1]);
+                                c[e] = (uint16_t)two;
+                                c[e + 1] = (uint16_t)(two >> 16);
+                            }
+                            *reinterpret_cast<u16x8u_t*>(x.copy + at) = c;
+                        }
+                        return;
+                    }
+                    for (uint32_t e = 0; p + e < np; ++e) {
+                        const float value = x.param[at + e] * s.keep - v[e] * rate;
+                        x.param[at + e] = value;
+                        if (x.copy) x.copy[at + e] = (uint16_t)pack_bf16x2(value, value);
+                    }
+                });
 }
 
 // Which of `all` large tiles, and which part of it, a workgroup takes: each XCD has a run of them, and where its last round would

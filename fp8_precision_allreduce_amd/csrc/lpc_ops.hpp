@@ -199,7 +199,7 @@ hipError_t launch_gemm_mxfp4(const uint8_t* x, const uint8_t* xs, size_t rows, s
                              const uint8_t* ws, size_t n, int groups, const int32_t* counts, void* out, int out_bf16,
                              hipStream_t stream);
 
-// elements of a matrix that one workgroup of the matrix optimizer's elementwise kernels takes
+// elements of a matrix, its rows padded, that one workgroup of the matrix optimizer's elementwise kernels takes
 constexpr size_t kMuonChunk = 16384;
 constexpr size_t kMuonTile = 256;  // outputs along a side of a tile of its products
 

@@ -84,7 +84,7 @@ MuonSizes muon_sizes(size_t rows, size_t cols) {
         return {0, 0, 0, smalls, smalls * lpc::kMuonSmall * lpc::kMuonSmall * sizeof(double)};
     }
     const size_t side = (s + lpc::kMuonTile - 1) / lpc::kMuonTile;
-    const size_t chunks = (rows * cols + lpc::kMuonChunk - 1) / lpc::kMuonChunk;
+    const size_t chunks = (rows * up(cols, kMuonPad) + lpc::kMuonChunk - 1) / lpc::kMuonChunk;
     const size_t tiles = ((rows + lpc::kMuonTile - 1) / lpc::kMuonTile) * ((cols + lpc::kMuonTile - 1) / lpc::kMuonTile);
     const size_t bytes = 6 * rows * up(cols, kMuonPad) + 4 * s * up(s, kMuonPad) + 8 * chunks;
     return {chunks, side * (side + 1) / 2, tiles, 0, up(bytes, 128)};
