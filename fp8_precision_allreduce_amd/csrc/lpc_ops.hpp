@@ -203,6 +203,7 @@ hipError_t launch_gemm_mxfp4(const uint8_t* x, const uint8_t* xs, size_t rows, s
 constexpr size_t kMuonChunk = 16384;
 constexpr size_t kMuonTile = 256;  // outputs along a side of a tile of its products
 
+constexpr size_t kMuonBand = 6;     // rows of tiles of a matrix that follow each other
 constexpr size_t kMuonSmall = 32;  // shorter sides up to this go without tiles
 // of such a matrix's longer side, a workgroup takes whole blocks of 128, of 64 workgroups at most
 inline size_t muon_span(size_t length) { return (length + 128 * 64 - 1) / (128 * 64) * 128; }

@@ -407,8 +407,11 @@ lpc_status lpc_muon_plan(const lpc_muon_tensor* tensors, int count, lpc_dtype gr
             for (size_t j = 0; j < sizes.chunks; ++j) add(0, j);
             for (size_t q = 0; q * lpc::kMuonTile < side; ++q)
                 for (size_t p = 0; p <= q; ++p) add(1, q << 16 | p);
-            for (size_t q = 0; q * lpc::kMuonTile < t.rows; ++q)
-                for (size_t p = 0; p * lpc::kMuonTile < t.cols; ++p) add(2, q << 16 | p);
+            // bands of rows of tiles, column after column: neighbours in the list run at the same time on one XCD and share operands
+            const size_t tall = (t.rows + lpc::kMuonTile - 1) / lpc::kMuonTile;
+            for (size_t band = 0; band < tall; band += lpc::kMuonBand)
+                for (size_t p = 0; p * lpc::kMuonTile < t.cols; ++p)
+                    for (size_t q = band; q < tall && q < band + lpc::kMuonBand; ++q) add(2, q << 16 | p);
         }
     }
     *work = w;
