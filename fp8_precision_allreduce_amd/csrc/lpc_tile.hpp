@@ -267,14 +267,17 @@ __device__ __forceinline__ void end_slot() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Exponent bytes come for four slabs at a time, 32 bytes of each row, into one of two buffers behind the stages: a slab's 8 bytes
+// of each row by themselves were 512 lines for 4 KB, as many as of the codes (16,384 x 7168 x 4096 over 8 groups 314 us against 281).
+constexpr uint32_t kScaleSlabs = 4, kScaleRun = 8 * kScaleSlabs;
+
 // Large: two wavefronts along q and four along p, each with 128 x 64 outputs in two phases of 64 x 64.
 template <bool Scaled>
 struct LargeOf {
     static constexpr int WavesQ = 2, F = 4, Phases = 2, PF = 4, AQ = F * Phases, AP = PF;  // fragments of 16 x 16
     static constexpr uint32_t QW = 128, PW = 64, BQ = 256, BP = 256, Stages = 2;
-    static constexpr uint32_t kScaleBytes = Scaled ? 8 * (BQ + BP) : 0;  // 8 exponent bytes a row and slab
-    static constexpr uint32_t kStage = (BQ + BP) * kSlab + kScaleBytes;
-    static constexpr uint32_t kBytes = Stages * kStage;
+    static constexpr uint32_t kStage = (BQ + BP) * kSlab;
+    static constexpr uint32_t kBytes = Stages * kStage + (Scaled ? 2 * kScaleRun * (BQ + BP) : 0);
     static constexpr bool kScaled = Scaled, kPair = false;
     static __device__ __forceinline__ uint32_t q0(uint32_t wave) { return wave % 2 * QW; }
     static __device__ __forceinline__ uint32_t p0(uint32_t wave) { return wave / 2 * PW; }
@@ -286,9 +289,8 @@ template <bool Scaled>
 struct SmallOf {
     static constexpr int F = 4, PF = 4, AQ = 2, AP = 4;
     static constexpr uint32_t QW = 32, PW = 64, BQ = 128, BP = 128, Stages = 4;
-    static constexpr uint32_t kScaleBytes = Scaled ? 8 * (BQ + BP) : 0;
-    static constexpr uint32_t kStage = (BQ + BP) * kSlab + kScaleBytes;
-    static constexpr uint32_t kBytes = Stages * kStage;
+    static constexpr uint32_t kStage = (BQ + BP) * kSlab;
+    static constexpr uint32_t kBytes = Stages * kStage + (Scaled ? 2 * kScaleRun * (BQ + BP) : 0);
     static constexpr bool kScaled = Scaled, kPair = true;
     static __device__ __forceinline__ uint32_t q0(uint32_t wave) { return wave % 2 * 64 + wave / 4 * QW; }
     static __device__ __forceinline__ uint32_t p0(uint32_t wave) { return wave % 4 / 2 * PW; }
@@ -298,50 +300,60 @@ struct SmallOf {
 template <typename S, int FQ, int FP>
 struct SlabLoads {
     static constexpr int QLoads = S::BQ / 64, PLoads = S::BP / 64;
-    // exponent bytes: 2 lanes a row, 32 rows a load; a wavefront does SLoads of the (BQ + BP) / 32
-    static constexpr int SLoads = S::kScaled ? (S::BQ + S::BP) / 32 / kTileWaves : 0;
-    static constexpr int kLoads = SLoads + PLoads + QLoads;
+    // exponent bytes of four slabs: 8 lanes a row, 8 rows a load
+    static constexpr int SLoads = S::kScaled ? (S::BQ + S::BP) / 8 / kTileWaves : 0;
+    static constexpr int kLoads = PLoads + QLoads;
     Loads<FQ, QLoads> q;
     Loads<FP, PLoads> p;
-    const uint8_t* sbase[SLoads + 1];
-    uint32_t soff[SLoads + 1];
-    uint32_t slabs, wave, lane;
+    const uint8_t* sbase[2];
+    uint32_t soff[SLoads + 1], scales, slabs, wave, lane, row_bytes;
     bool cuts;
 
-    __device__ __forceinline__ SlabLoads(const Operand& oq, const Operand& op, const Contraction& k, uint32_t w, uint32_t l)
-        : q(oq, k, w, l), p(op, k, w, l), slabs(k.slabs), wave(w), lane(l), cuts(k.count != kSlabRows) {
+    __device__ __forceinline__ SlabLoads(const Operand& oq, const Operand& op, const Contraction& k, uint32_t w, uint32_t l, uint32_t lds)
+        : q(oq, k, w, l), p(op, k, w, l), sbase{oq.scale, op.scale}, scales(lds + S::Stages * S::kStage), slabs(k.slabs), wave(w), lane(l),
+          row_bytes((uint32_t)(oq.ld / 16)), cuts(k.count != kSlabRows) {
         q.settle();
         p.settle();
 #pragma unroll
         for (int n = 0; n < SLoads; ++n) {
-            const uint32_t part = n * kTileWaves + wave;  // 32 rows of Q, then of P
-            const bool of_q = part < S::BQ / 32;
-            const Operand& o = of_q ? oq : op;
-            const uint32_t row = (of_q ? part : part - S::BQ / 32) * 32 + lane / 2;
-            sbase[n] = o.scale;
-            soff[n] = min(row, o.n - 1) * (uint32_t)(o.ld / 16) + (lane & 1) * 4;
+            const uint32_t row = (n * kTileWaves + wave) * 8 + lane / 8;  // of Q, then of P
+            soff[n] = (n < SLoads / 2 ? min(row, oq.n - 1) : min(row - S::BQ, op.n - 1)) * row_bytes;
             asm volatile("" : "+v"(soff[n]));
         }
     }
 
-    // load n of slab c: exponent bytes, P, the even loads of Q, the odd ones
+    // the buffer of slab c's exponent bytes
+    __device__ __forceinline__ uint32_t scales_of(uint32_t c) const { return S::Stages * S::kStage + c / kScaleSlabs % 2 * (kScaleRun * (S::BQ + S::BP)); }
+    // whether slab c's loads bring exponent bytes
+    static __device__ __forceinline__ bool with_scales(uint32_t c) { return S::kScaled && c % kScaleSlabs == 0; }
+
+    // load n of slab c: P, the even loads of Q, the odd ones
     __device__ __forceinline__ void load(int n, uint32_t c, uint32_t to) const {
         const bool last = c + 1 == slabs && cuts;
-        if (n < SLoads) {
-            // in a short slab the second half's bytes are those of the first once more
-            load_lds4(sbase[n] + c * 8, soff[n] - (last ? (lane & 1) * 4 : 0), to + (S::BQ + S::BP) * kSlab + (n * kTileWaves + wave) * 256);
-        } else if (n < SLoads + PLoads) {
-            const int i = n - SLoads;
-            p.load(i, c, last, to + S::BQ * kSlab + i * 8192 + wave * 1024);
+        if (n < PLoads) {
+            p.load(n, c, last, to + S::BQ * kSlab + n * 8192 + wave * 1024);
         } else {
-            const int m = n - SLoads - PLoads, i = m < QLoads / 2 ? 2 * m : 2 * (m - QLoads / 2) + 1;
+            const int m = n - PLoads, i = m < QLoads / 2 ? 2 * m : 2 * (m - QLoads / 2) + 1;
             q.load(i, c, last, to + i * 8192 + wave * 1024);
         }
     }
     __device__ __forceinline__ void range(int from, int upto, uint32_t c, uint32_t to) const {
+        if (from == 0 && with_scales(c)) {
+            // past a row's end its last four bytes are repeated: what they scale is zeros
+            const uint32_t in = min(lane % 8 * 4, row_bytes - 4 - c * 8);
+            const uint32_t at = scales - S::Stages * S::kStage + scales_of(c);
+#pragma unroll
+            for (int n = 0; n < SLoads; ++n) load_lds4(sbase[n < SLoads / 2 ? 0 : 1] + c * 8, soff[n] + in, at + (n * kTileWaves + wave) * 256);
+        }
 #pragma unroll
         for (int n = 0; n < kLoads; ++n)
             if (n >= from && n < upto) load(n, c, to);
+    }
+    // Waits until only `Slabs` slabs' loads are on their way, of which one brings exponent bytes or none does.
+    template <int Slabs>
+    static __device__ __forceinline__ void arrived(bool scaled) {
+        if (S::kScaled && scaled) lds_arrived<Slabs * kLoads + SLoads>();
+        else lds_arrived<Slabs * kLoads>();
     }
 };
 
@@ -350,13 +362,15 @@ template <typename Mma, int F, int N>
 struct Fragments {
     Fragment f[N];
     int s[N] = {};
+    // bytes: the first row's exponent bytes, Pitch apart
+    template <uint32_t Pitch>
     __device__ __forceinline__ void read(const Reader<F>& r, const uint8_t* at, uint32_t first, const uint8_t* bytes, uint32_t lane) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             f[i] = r.read(at, first + i);
             if constexpr (Mma::kScaled) {
                 // the exponent bytes of the lane's codes: of 8 in a row, lane / 16 of each half's four
-                const i32x2_t v = *reinterpret_cast<const i32x2_t*>(bytes + (16 * i + (lane & 15)) * 8);
+                const i32x2_t v = *reinterpret_cast<const i32x2_t*>(bytes + (16 * i + (lane & 15)) * Pitch);
                 s[i] = (int)__builtin_amdgcn_perm((uint32_t)v[1], (uint32_t)v[0], (lane >> 4) * 0x0101 + 0x0400);
             }
         }
@@ -405,19 +419,18 @@ __device__ __forceinline__ void large_sums(const Operand& q, const Operand& p, c
     const uint32_t lane = threadIdx.x & 63, slabs = k.slabs;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const uint32_t group = wave / 4, wq = S::q0(wave), wp = S::p0(wave);
-    const SlabLoads<S, FQ, FP> loads(q, p, k, wave, lane);
-    // scales, P and the Q of phase 0 come early, the Q of phase 1 late
+    const SlabLoads<S, FQ, FP> loads(q, p, k, wave, lane, lds_address(lds));
+    // exponent bytes, P and the Q of phase 0 come early, the Q of phase 1 late
     constexpr int kLoads = loads.kLoads, kEarly = kLoads - loads.QLoads / 2;
     const uint32_t to[2] = {lds_address(lds), lds_address(lds) + S::kStage};
-    // before the first reads of a part of slab c
+    // until one slab's loads are on their way, the early ones of slab c among them
     auto arrived = [&](uint32_t c) {
-        if (c + 1 < slabs) lds_arrived<kLoads>();
+        if (c < slabs) loads.template arrived<1>(loads.with_scales(c));
         else lds_arrived<0>();
     };
     loads.range(0, kLoads, 0, to[0]);
     if (slabs > 1) loads.range(0, kEarly, 1, to[1]);
-    if (slabs > 1) lds_arrived<kLoads>();  // what is left: the late ones of slab 0 and the early ones of slab 1
-    else lds_arrived<0>();
+    arrived(1);  // what is left: the late ones of slab 0 and the early ones of slab 1
     end_slot();
     if (group == 1) end_slot();
     const Reader<FQ> rq(lane);
@@ -425,29 +438,23 @@ __device__ __forceinline__ void large_sums(const Operand& q, const Operand& p, c
     for (uint32_t b = 0; b < slabs; ++b) {
         const uint32_t at = b & 1;
         const uint8_t* s = lds + at * S::kStage;
-        const uint8_t* bytes = s + (BQ + S::BP) * kSlab;
+        const uint8_t* bytes = lds + loads.scales_of(b) + b % kScaleSlabs * 8;
         Fragments<Mma, FP, S::PF> pv;
 #pragma unroll
         for (int ph = 0; ph < 2; ++ph) {
             Fragments<Mma, FQ, S::F> qv;
             if (ph == 0) {
-                pv.read(rp, s + BQ * kSlab + wp / 64 * 8192, 0, bytes + (BQ + wp) * 8, lane);
+                pv.template read<kScaleRun>(rp, s + BQ * kSlab + wp / 64 * 8192, 0, bytes + (BQ + wp) * kScaleRun, lane);
                 if (loads.cuts && b + 1 == slabs) pv.cut(lane, k.count);
             }
-            qv.read(rq, s + wq / 64 * 8192, ph * S::F, bytes + (wq + 64 * ph) * 8, lane);
+            qv.template read<kScaleRun>(rq, s + wq / 64 * 8192, ph * S::F, bytes + (wq + 64 * ph) * kScaleRun, lane);
             __builtin_amdgcn_sched_barrier(0);
             if (ph == 0 && b + 1 < slabs) loads.range(kEarly, kLoads, b + 1, to[0] + to[1] - to[at]);
             if (ph == 1 && b + 2 < slabs) loads.range(0, kEarly, b + 2, to[at]);
-            if (group == 1) {
-                if (ph == 0) arrived(b);
-                else if (b + 1 < slabs) arrived(b + 1);
-            }
+            if (group == 1 && (ph == 0 || b + 1 < slabs)) arrived(b + 1 + ph);
             end_slot();
             multiply<Mma>(acc + ph * S::F, qv, pv);
-            if (group == 0) {
-                if (ph == 0) arrived(b);
-                else if (b + 1 < slabs) arrived(b + 1);
-            }
+            if (group == 0 && (ph == 0 || b + 1 < slabs)) arrived(b + 1 + ph);
             end_slot();
         }
     }
@@ -462,7 +469,7 @@ __device__ __forceinline__ void small_sums(const Operand& q, const Operand& p, c
     const uint32_t lane = threadIdx.x & 63, slabs = k.slabs;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const uint32_t group = wave / 4, wq = wave % 2 * 64, wp = wave % 4 / 2 * 64;
-    const SlabLoads<S, FQ, FP> loads(q, p, k, wave, lane);
+    const SlabLoads<S, FQ, FP> loads(q, p, k, wave, lane, lds_address(lds));
     constexpr int kLoads = loads.kLoads;
     f32x4_t acc[S::F][S::PF];
     clear(acc);
@@ -473,8 +480,8 @@ __device__ __forceinline__ void small_sums(const Operand& q, const Operand& p, c
     };
     // slab c, where those up to c + 2 have been started
     auto arrived = [&](uint32_t c) {
-        if (c + 2 < slabs) lds_arrived<2 * kLoads>();
-        else if (c + 1 < slabs) lds_arrived<kLoads>();
+        if (c + 2 < slabs) loads.template arrived<2>(loads.with_scales(c + 1) || loads.with_scales(c + 2));
+        else if (c + 1 < slabs) loads.template arrived<1>(loads.with_scales(c + 1));
         else lds_arrived<0>();
     };
     load_next(0);
@@ -494,12 +501,12 @@ __device__ __forceinline__ void small_sums(const Operand& q, const Operand& p, c
     }
     for (uint32_t b = group; b < slabs; b += 2) {
         const uint8_t* s = lds + b % S::Stages * S::kStage;
-        const uint8_t* bytes = s + (BQ + S::BP) * kSlab;
+        const uint8_t* bytes = lds + loads.scales_of(b) + b % kScaleSlabs * 8;
         Fragments<Mma, FP, S::PF> pv;
         Fragments<Mma, FQ, S::F> qv;
-        pv.read(rp, s + BQ * kSlab + wp / 64 * 8192, 0, bytes + (BQ + wp) * 8, lane);
+        pv.template read<kScaleRun>(rp, s + BQ * kSlab + wp / 64 * 8192, 0, bytes + (BQ + wp) * kScaleRun, lane);
         if (loads.cuts && b + 1 == slabs) pv.cut(lane, k.count);
-        qv.read(rq, s + wq / 64 * 8192, 0, bytes + wq * 8, lane);
+        qv.template read<kScaleRun>(rq, s + wq / 64 * 8192, 0, bytes + wq * kScaleRun, lane);
         __builtin_amdgcn_sched_barrier(0);
         slot(b);
         end_slot();
@@ -638,9 +645,9 @@ __device__ __forceinline__ void narrow_tile(const Operand& q_, const Operand& p_
         const uint8_t* bytes = s + (BQ + BP) * kSlab;
         Fragments<Mma, FQ, QF> qv;
         Fragments<Mma, FP, PF> pv;
-        pv.read(rp, s + BQ * kSlab, 0, bytes + BQ * 8, lane);
+        pv.template read<8>(rp, s + BQ * kSlab, 0, bytes + BQ * 8, lane);
         if (cuts && wave + i * kNarrowWaves + 1 == k.slabs) pv.cut(lane, k.count);
-        qv.read(rq, s, 0, bytes, lane);
+        qv.template read<8>(rq, s, 0, bytes, lane);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         multiply<Mma>(acc, qv, pv);
         stage = stage + 1 == Depth ? 0 : stage + 1;
