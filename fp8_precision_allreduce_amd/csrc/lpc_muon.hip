@@ -448,14 +448,19 @@ constexpr uint32_t kSide = kMuonSmall, kPitch = kSide + 1, kBlockCols = 128, kPe
 // A workgroup's part of U's long side, in blocks of 128.
 struct Strip {
     uint32_t side, length, begin, end;
+    float over;  // 1 / side
     bool tall;
 
     __device__ __forceinline__ Strip(const MuonMatrix& x, uint32_t index)
-        : side(min(x.rows, x.cols)), length(max(x.rows, x.cols)), begin(index * x.span), end(min(length, begin + x.span)), tall(x.rows > x.cols) {}
-    // the lane's n-th element of the block from k0 on: its place in the matrix and in the block; false: none
+        : side(min(x.rows, x.cols)), length(max(x.rows, x.cols)), begin(index * x.span), end(min(length, begin + x.span)), over(1.0f / (float)side),
+          tall(x.rows > x.cols) {}
+    // whether any lane has an n-th element of a block
+    __device__ __forceinline__ bool any(int n) const { return n * kChunkLanes < side * kBlockCols; }
+    // the lane's n-th element of the block from k0 on: its place in the matrix and in the block; false: none.  e / side of less than
+    // 2^12 is exact as a product with the reciprocal, half a unit up.
     __device__ __forceinline__ bool place(int n, uint32_t k0, size_t* at, uint32_t* i, uint32_t* k) const {
         const uint32_t e = n * kChunkLanes + threadIdx.x;
-        *k = tall ? e / side : e % kBlockCols;
+        *k = tall ? (uint32_t)(((float)e + 0.5f) * over) : e % kBlockCols;
         *i = tall ? e - *k * side : e / kBlockCols;
         *at = tall ? (size_t)(k0 + *k) * side + *i : (size_t)*i * length + k0 + *k;
         return *i < side && *k < kBlockCols && k0 + *k < end;
@@ -475,14 +480,14 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_sums_kernel(MuonPlan p
     const float scale = grad_scale ? grad_scale[0] : 1.0f;
     const uint32_t wave = threadIdx.x >> 6, l16 = threadIdx.x & 15, l4 = (threadIdx.x & 63) >> 4;
     const uint32_t ti = wave / 2 * 16 + l16, tj = wave % 2 * 16 + l16;
-    f64x4_t sum = {};
+    f64x4_t sums[4] = {};  // each of their instructions waits for the one before
     for (uint32_t k0 = strip.begin; k0 < strip.end; k0 += kBlockCols) {
         float g[kPerLane], m[kPerLane];
         size_t at;
         uint32_t i, k;
 #pragma unroll
         for (int n = 0; n < (int)kPerLane; ++n) {
-            const bool in = strip.place(n, k0, &at, &i, &k);
+            const bool in = strip.any(n) && strip.place(n, k0, &at, &i, &k);
             g[n] = in ? element(grad, at) * scale : 0.0f;
             m[n] = in ? x.m[at] * s.beta : 0.0f;
         }
@@ -490,30 +495,38 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_sums_kernel(MuonPlan p
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < (int)kPerLane; ++n) {
-            if (!strip.place(n, k0, &at, &i, &k)) continue;
+            if (!strip.any(n) || !strip.place(n, k0, &at, &i, &k)) continue;
             const float now = m[n] + g[n] * s.rest;
             x.m[at] = now;
             u[k][i] = s.nesterov ? g[n] * s.rest + now * s.beta : now;
         }
         __syncthreads();
-#pragma unroll 8
-        for (uint32_t c = 0; c < kBlockCols; c += 4)
-            sum = __builtin_amdgcn_mfma_f64_16x16x4f64((double)u[c + l4][ti], (double)u[c + l4][tj], sum, 0, 0, 0);
+#pragma unroll 2
+        for (uint32_t c = 0; c < kBlockCols; c += 16)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                sums[n] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)u[c + 4 * n + l4][ti], (double)u[c + 4 * n + l4][tj], sums[n], 0, 0, 0);
         __syncthreads();
     }
+    const f64x4_t sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
     double* out = reinterpret_cast<double*>(space + x.space) + (size_t)piece.index * kSide * kSide;
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[(wave / 2 * 16 + l4 + 4 * e) * kSide + tj] = sum[e];
 }
 
-// to = a b of matrices [32][kPitch] that are symmetric: the wavefront's 16 x 16 of it
-__device__ __forceinline__ f32x4_t small_product(const float (*a)[kPitch], const float (*b)[kPitch]) {
+// a b of matrices [32][kPitch] that are symmetric and zeros past `side`: the wavefront's 16 x 16 of it.  Two sums, as each of their
+// instructions waits for the one before.
+__device__ __forceinline__ f32x4_t small_product(const float (*a)[kPitch], const float (*b)[kPitch], uint32_t side) {
     const uint32_t wave = threadIdx.x >> 6, l16 = threadIdx.x & 15, l4 = (threadIdx.x & 63) >> 4;
-    f32x4_t sum = {};
+    const float *row = a[wave / 2 * 16 + l16] + l4, *col = b[wave % 2 * 16 + l16] + l4;
+    f32x4_t sum[2] = {};
 #pragma unroll
-    for (uint32_t c = 0; c < kSide; c += 4)
-        sum = __builtin_amdgcn_mfma_f32_16x16x4f32(a[wave / 2 * 16 + l16][c + l4], b[wave % 2 * 16 + l16][c + l4], sum, 0, 0, 0);
-    return sum;
+    for (uint32_t half = 0; half < 2; ++half) {
+        if (half && side <= 16) break;
+#pragma unroll
+        for (uint32_t c = half * 16; c < half * 16 + 16; c += 4) sum[c / 4 % 2] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[c], col[c], sum[c / 4 % 2], 0, 0, 0);
+    }
+    return sum[0] + sum[1];
 }
 
 template <typename Grad>
@@ -553,13 +566,13 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_update_kernel(MuonPlan
     __syncthreads();
     const uint32_t row = wave / 2 * 16 + 4 * l4, col = wave % 2 * 16 + l16;  // of four sums, below one another
     for (int n = 0; n < iterations; ++n) {
-        const f32x4_t square = small_product(a, a);  // P = a + b A + c A A
+        const f32x4_t square = small_product(a, a, strip.side);  // P = a + b A + c A A
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[row + e][col] = (row + e == col ? kA : 0.0f) + kB * a[row + e][col] + kC * square[e];
         __syncthreads();
-        const f32x4_t next = n ? small_product(p, r) : f32x4_t{};
+        const f32x4_t next = n ? small_product(p, r, strip.side) : f32x4_t{};
         const bool more = n + 1 < iterations;
-        const f32x4_t half = more ? small_product(p, a) : f32x4_t{};
+        const f32x4_t half = more ? small_product(p, a, strip.side) : f32x4_t{};
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -567,7 +580,7 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_update_kernel(MuonPlan
             t[row + e][col] = half[e];
         }
         __syncthreads();
-        const f32x4_t whole = more ? small_product(p, t) : f32x4_t{};
+        const f32x4_t whole = more ? small_product(p, t, strip.side) : f32x4_t{};
 #pragma unroll
         for (int e = 0; e < 4; ++e) a[row + e][col] = whole[e];
         __syncthreads();
@@ -575,19 +588,21 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_update_kernel(MuonPlan
 
     const float rate = s.lr * x.scale;
     for (uint32_t k0 = strip.begin; k0 < strip.end; k0 += kBlockCols) {
-        float param[kPerLane];
+        float param[kPerLane], value[kPerLane];
         size_t at;
         uint32_t i, k;
         for (uint32_t e = threadIdx.x; e < kBlockCols * kPitch; e += kChunkLanes) (&u[0][0])[e] = 0.0f;
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < (int)kPerLane; ++n) {
-            const bool in = strip.place(n, k0, &at, &i, &k);
+            const bool in = strip.any(n) && strip.place(n, k0, &at, &i, &k);
             param[n] = in ? x.param[at] : 0.0f;
-            if (!in) continue;
-            const float m = x.m[at];
-            u[k][i] = (float)((double)(s.nesterov ? element(grad, at) * scale * s.rest + m * s.beta : m) * by);
+            const float m = in ? x.m[at] : 0.0f, g = in ? element(grad, at) * scale : 0.0f;
+            value[n] = (float)((double)(s.nesterov ? g * s.rest + m * s.beta : m) * by);
         }
+#pragma unroll
+        for (int n = 0; n < (int)kPerLane; ++n)
+            if (strip.any(n) && strip.place(n, k0, &at, &i, &k)) u[k][i] = value[n];
         __syncthreads();
 #pragma unroll
         for (int ti = 0; ti < 2; ++ti)
@@ -603,7 +618,7 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_update_kernel(MuonPlan
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < (int)kPerLane; ++n) {
-            if (!strip.place(n, k0, &at, &i, &k)) continue;
+            if (!strip.any(n) || !strip.place(n, k0, &at, &i, &k)) continue;
             const float now = param[n] * s.keep - o[k][i] * rate;
             x.param[at] = now;
             if (x.copy) x.copy[at] = (uint16_t)pack_bf16x2(now, now);
