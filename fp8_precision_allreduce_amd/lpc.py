@@ -871,8 +871,9 @@ class Muon:
         _call("lpc_muon_plan", table, count, self.grad_dtype, host.data_ptr() if size else None, size, ctypes.byref(self._work))
         self._plan = self._space = None
         if self._work.matrices:
-            self._plan = host.to("cuda:%d" % self.device)
-            self._space = torch.empty(self._work.workspace_bytes, dtype=torch.uint8, device=self._plan.device)
+            # the copy of the plan ends after all earlier work of this stream, which may have used what is the workspace now
+            self._space = torch.empty(self._work.workspace_bytes, dtype=torch.uint8, device="cuda:%d" % self.device)
+            self._plan = host.to(self._space.device)
         # streams after whose work plan and workspace may be handed out again when this object goes
         self._streams = {torch._C._cuda_getCurrentRawStream(self.device)} if self._work.matrices else set()
 

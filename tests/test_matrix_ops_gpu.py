@@ -124,7 +124,8 @@ DENSE = [(1, 8, 1), (1, 64, 16), (1, 4096, 1000), (2, 72, 5), (15, 136, 127), (1
          (64, 1032, 384), (127, 56, 129), (128, 64, 128), (129, 200, 255), (300, 1152, 1001), (777, 520, 513), (1030, 328, 768)]
 GROUPED = [(1, 256, 96, [0, 1, 0]), (40, 392, 136, [0, 17, 0, 20]), (300, 640, 264, [128, 0, 172]), (300, 72, 128, [0, 0, 0]),
            (513, 896, 304, [256, 1, 255, 1]), (500, 384, 256, [-3, 200, 1000, 5]), (200, 128, 64, [50]),
-           (700, 1160, 640, [3, 0, 500, 7, 40]), (90, 64, 72, [1] * 70 + [3])]
+           (700, 1160, 640, [3, 0, 500, 7, 40]), (90, 64, 72, [1] * 70 + [3]),
+           (300, 200, 208, [4] * 70)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
