@@ -21,17 +21,30 @@ namespace {
 constexpr float kHeld = 1024.0f, kLow = 2048.0f;  // what X, A and B are held times; and what a low half is held times besides
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 
+// The plan does not change during a launch and a workgroup's part of it is the same for all lanes: read by scalar loads.
+typedef uint32_t u32x16_t __attribute__((ext_vector_type(16)));
+template <typename V, typename T>
+__device__ __forceinline__ T scalar_load(const T* p) {
+    static_assert(sizeof(V) == sizeof(T), "as a vector");
+    return __builtin_bit_cast(T, *reinterpret_cast<const __attribute__((address_space(4))) V*>(reinterpret_cast<uintptr_t>(p)));
+}
+__device__ __forceinline__ MuonPiece piece_of(const MuonPiece* pieces, uint32_t i) { return scalar_load<u32x2_t>(pieces + i); }
+__device__ __forceinline__ MuonMatrix matrix_of(const MuonPlan& plan, const MuonPiece& piece) {
+    return scalar_load<u32x16_t>(plan.matrices + piece.matrix);
+}
+
 // one matrix's parts of the workspace; all start at multiples of 128 bytes and their rows' ends are zeros
 struct Space {
-    _Float16 *high[2], *low, *a, *b;
+    _Float16 *high0, *high1, *low, *a, *b;
     double* partial;
+    __device__ __forceinline__ _Float16* high(uint32_t n) const { return n ? high1 : high0; }
 };
 
 __device__ __forceinline__ Space space_of(const MuonMatrix& m, uint8_t* w) {
     w += m.space;
     const size_t x = (size_t)m.rows * m.ldx * 2, s = (size_t)min(m.rows, m.cols) * m.lda * 2;
     _Float16* h = reinterpret_cast<_Float16*>(w);
-    return {{h, reinterpret_cast<_Float16*>(w + x)}, reinterpret_cast<_Float16*>(w + 2 * x), reinterpret_cast<_Float16*>(w + 3 * x),
+    return {h, reinterpret_cast<_Float16*>(w + x), reinterpret_cast<_Float16*>(w + 2 * x), reinterpret_cast<_Float16*>(w + 3 * x),
             reinterpret_cast<_Float16*>(w + 3 * x + s), reinterpret_cast<double*>(w + 3 * x + 2 * s)};
 }
 
@@ -108,8 +121,8 @@ __device__ __forceinline__ double workgroup_sum(double v, double* lds) {
 template <typename Grad>
 __global__ __launch_bounds__(kChunkLanes) void muon_momentum_kernel(MuonPlan plan, uint8_t* space, const float* grad_scale, MuonScalars s) {
     __shared__ double lds[kChunkLanes / 64];
-    const MuonPiece piece = plan.chunks[blockIdx.x];
-    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const MuonPiece piece = piece_of(plan.chunks, blockIdx.x);
+    const MuonMatrix x = matrix_of(plan, piece);
     const Runs runs(x, piece.index);
     const Grad* grad = static_cast<const Grad*>(x.grad);
     const float scale = grad_scale ? grad_scale[0] : 1.0f;
@@ -140,8 +153,8 @@ __global__ __launch_bounds__(kChunkLanes) void muon_momentum_kernel(MuonPlan pla
 template <typename Grad>
 __global__ __launch_bounds__(kChunkLanes) void muon_start_kernel(MuonPlan plan, uint8_t* space, const float* grad_scale, MuonScalars s) {
     __shared__ double lds[kChunkLanes / 64];
-    const MuonPiece piece = plan.chunks[blockIdx.x];
-    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const MuonPiece piece = piece_of(plan.chunks, blockIdx.x);
+    const MuonMatrix x = matrix_of(plan, piece);
     const Space w = space_of(x, space);
     const Runs runs(x, piece.index);
     const uint32_t chunks = (uint32_t)(((uint64_t)x.rows * x.ldx + kMuonChunk - 1) / kMuonChunk);
@@ -164,7 +177,7 @@ __global__ __launch_bounds__(kChunkLanes) void muon_start_kernel(MuonPlan plan, 
             high = __builtin_convertvector(v, f16x8_t);
             low = __builtin_convertvector((v - __builtin_convertvector(high, f32x8_t)) * kLow, f16x8_t);
         }
-        *reinterpret_cast<f16x8_t*>(w.high[0] + to) = high;
+        *reinterpret_cast<f16x8_t*>(w.high0 + to) = high;
         *reinterpret_cast<f16x8_t*>(w.low + to) = low;
     }
 }
@@ -281,11 +294,11 @@ __device__ __forceinline__ void square_tile(const MuonMatrix& x, const Space& w,
                                              contraction(s), lds, acc);
     } else if (x.rows > x.cols) {
         // columns up to ldx hold zeros, so that pieces of 8 are whole
-        tile_sums<MmaF16, kAcross, kAcross, S>(operand(w.high[from] + q0, x.ldx, min(S::BQ, x.ldx - q0)),
-                                               operand(w.high[from] + p0, x.ldx, min(S::BP, x.ldx - p0)), contraction(x.rows), lds, acc);
+        tile_sums<MmaF16, kAcross, kAcross, S>(operand(w.high(from) + q0, x.ldx, min(S::BQ, x.ldx - q0)),
+                                               operand(w.high(from) + p0, x.ldx, min(S::BP, x.ldx - p0)), contraction(x.rows), lds, acc);
     } else {
-        tile_sums<MmaF16, kAlong, kAlong, S>(operand(w.high[from] + (size_t)q0 * x.ldx, x.ldx, nq),
-                                             operand(w.high[from] + (size_t)p0 * x.ldx, x.ldx, np), contraction(x.cols), lds, acc);
+        tile_sums<MmaF16, kAlong, kAlong, S>(operand(w.high(from) + (size_t)q0 * x.ldx, x.ldx, nq),
+                                             operand(w.high(from) + (size_t)p0 * x.ldx, x.ldx, np), contraction(x.cols), lds, acc);
     }
     _Float16* out = Second ? w.b : w.a;
     const _Float16* a = w.a + (size_t)q0 * x.lda + p0;
@@ -313,7 +326,7 @@ template <bool Last, typename S>
 __device__ __forceinline__ void update_tile(const MuonMatrix& x, const Space& w, uint32_t from, uint32_t lows, const MuonScalars& s, uint32_t q0,
                                             uint32_t p0, uint8_t* lds) {
     const uint32_t nq = min(S::BQ, x.rows - q0), np = min(S::BP, x.cols - p0);
-    const _Float16* high = w.high[from];
+    const _Float16* high = w.high(from);
     f32x4_t acc[S::AQ][S::AP];
     if (x.rows > x.cols)
         tile_sums<MmaF16, kAlong, kAlong, S>(operand(high + (size_t)q0 * x.ldx, x.ldx, nq), operand(w.b + (size_t)p0 * x.lda, x.lda, np),
@@ -337,7 +350,7 @@ __device__ __forceinline__ void update_tile(const MuonMatrix& x, const Space& w,
                         cut_columns(v, p, np);
                         const size_t at = first + (size_t)q * x.ldx + p;
                         const f16x8_t h = __builtin_convertvector(v, f16x8_t);
-                        *reinterpret_cast<f16x8_t*>(w.high[1 - from] + at) = h;
+                        *reinterpret_cast<f16x8_t*>(w.high(1 - from) + at) = h;
                         if (lows & 2) *reinterpret_cast<f16x8_t*>(w.low + at) = low_of(v, h);
                         return;
                     }
@@ -411,8 +424,8 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_square_kernel(MuonPla
     __shared__ __attribute__((aligned(128))) uint8_t lds[kLdsBytes];
     Turn t;
     if (!find_turn(all, &t)) return;
-    const MuonPiece piece = plan.squares[t.tile];
-    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const MuonPiece piece = piece_of(plan.squares, t.tile);
+    const MuonMatrix x = matrix_of(plan, piece);
     const Space w = space_of(x, space);
     const uint32_t s = min(x.rows, x.cols);
     do_turn(piece, t.part, s, s, [&](uint32_t q, uint32_t p) { square_tile<Second, Large>(x, w, from, q, p, lds); },
@@ -427,8 +440,8 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPla
     __shared__ __attribute__((aligned(128))) uint8_t lds[kLdsBytes];
     Turn t;
     if (!find_turn(all, &t)) return;
-    const MuonPiece piece = plan.updates[t.tile];
-    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const MuonPiece piece = piece_of(plan.updates, t.tile);
+    const MuonMatrix x = matrix_of(plan, piece);
     const Space w = space_of(x, space);
     do_turn(piece, t.part, x.rows, x.cols, [&](uint32_t q, uint32_t p) { update_tile<Last, Large>(x, w, from, lows, s, q, p, lds); },
             [&](uint32_t q, uint32_t p) { update_tile<Last, Small>(x, w, from, lows, s, q, p, lds); });
@@ -473,8 +486,8 @@ __device__ __forceinline__ float element(const uint16_t* p, size_t i) { return b
 template <typename Grad>
 __global__ __launch_bounds__(kChunkLanes) void muon_small_sums_kernel(MuonPlan plan, uint8_t* space, const float* grad_scale, MuonScalars s) {
     __shared__ float u[kBlockCols][kPitch];
-    const MuonPiece piece = plan.smalls[blockIdx.x];
-    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const MuonPiece piece = piece_of(plan.smalls, blockIdx.x);
+    const MuonMatrix x = matrix_of(plan, piece);
     const Strip strip(x, piece.index);
     const Grad* grad = static_cast<const Grad*>(x.grad);
     const float scale = grad_scale ? grad_scale[0] : 1.0f;
@@ -534,8 +547,8 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_update_kernel(MuonPlan
                                                                         MuonScalars s) {
     __shared__ float a[kSide][kPitch], p[kSide][kPitch], r[kSide][kPitch], t[kSide][kPitch], u[kBlockCols][kPitch], o[kBlockCols][kPitch];
     __shared__ double diagonal[kSide];
-    const MuonPiece piece = plan.smalls[blockIdx.x];
-    const MuonMatrix& x = plan.matrices[piece.matrix];
+    const MuonPiece piece = piece_of(plan.smalls, blockIdx.x);
+    const MuonMatrix x = matrix_of(plan, piece);
     const Strip strip(x, piece.index);
     const Grad* grad = static_cast<const Grad*>(x.grad);
     const float scale = grad_scale ? grad_scale[0] : 1.0f;
