@@ -66,10 +66,10 @@ struct Runs {
     uint32_t all;    // of the chunk
 
     __device__ __forceinline__ Runs(const MuonMatrix& x, uint32_t chunk) : width(x.ldx / 8) {
-        const uint64_t first = (uint64_t)chunk * (kMuonChunk / 8), end = (uint64_t)x.rows * width;
+        const uint64_t first = (uint64_t)chunk * (x.span / 8), end = (uint64_t)x.rows * width;
         row = (uint32_t)(first / width);
         run = (uint32_t)(first - (uint64_t)row * width);
-        all = (uint32_t)min(end - first, (uint64_t)(kMuonChunk / 8));
+        all = (uint32_t)min(end - first, (uint64_t)(x.span / 8));
     }
     // run i's row, first column and how many of its elements there are in the matrix
     __device__ __forceinline__ void place(const MuonMatrix& x, uint32_t i, uint32_t* r, uint32_t* col, uint32_t* left) const {
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(kChunkLanes) void muon_start_kernel(MuonPlan plan, 
     const MuonMatrix x = matrix_of(plan, piece);
     const Space w = space_of(x, space);
     const Runs runs(x, piece.index);
-    const uint32_t chunks = (uint32_t)(((uint64_t)x.rows * x.ldx + kMuonChunk - 1) / kMuonChunk);
+    const uint32_t chunks = (uint32_t)(((uint64_t)x.rows * x.ldx + x.span - 1) / x.span);
     double sum = 0.0;
     for (uint32_t c = threadIdx.x; c < chunks; c += kChunkLanes) sum += w.partial[c];
     const double norm = sqrt(workgroup_sum(sum, lds)), by = norm > 0.0 ? (double)kHeld / norm : 0.0;

@@ -74,27 +74,29 @@ constexpr size_t kMuonPad = 64;  // elements that rows of its workspace are padd
 size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 
 struct MuonSizes {
-    size_t chunks, squares, updates, smalls, space;  // of one matrix
+    size_t chunks, squares, updates, smalls, space, span;  // of one matrix
 };
 
 MuonSizes muon_sizes(size_t rows, size_t cols) {
     const size_t s = rows < cols ? rows : cols, length = rows < cols ? cols : rows;
     if (s <= lpc::kMuonSmall) {
         const size_t smalls = (length + lpc::muon_span(length) - 1) / lpc::muon_span(length);
-        return {0, 0, 0, smalls, smalls * lpc::kMuonSmall * lpc::kMuonSmall * sizeof(double)};
+        return {0, 0, 0, smalls, smalls * lpc::kMuonSmall * lpc::kMuonSmall * sizeof(double), lpc::muon_span(length)};
     }
     const size_t side = (s + lpc::kMuonTile - 1) / lpc::kMuonTile;
-    const size_t chunks = (rows * up(cols, kMuonPad) + lpc::kMuonChunk - 1) / lpc::kMuonChunk;
+    const size_t elements = rows * up(cols, kMuonPad), span = lpc::muon_chunk(elements), chunks = (elements + span - 1) / span;
     const size_t tiles = ((rows + lpc::kMuonTile - 1) / lpc::kMuonTile) * ((cols + lpc::kMuonTile - 1) / lpc::kMuonTile);
     const size_t bytes = 6 * rows * up(cols, kMuonPad) + 4 * s * up(s, kMuonPad) + 8 * chunks;
-    return {chunks, side * (side + 1) / 2, tiles, 0, up(bytes, 128)};
+    return {chunks, side * (side + 1) / 2, tiles, 0, up(bytes, 128), span};
 }
+
+bool empty_tensor(const lpc_muon_tensor& t) { return t.batch == 0 || t.rows == 0 || t.cols == 0; }
 
 // false: refused
 bool muon_work(const lpc_muon_tensor* t, int count, lpc_muon_work* w) {
     *w = lpc_muon_work{};
     for (int i = 0; i < count; ++i) {
-        if (t[i].batch == 0 || t[i].rows == 0 || t[i].cols == 0) continue;
+        if (empty_tensor(t[i])) continue;
         if (t[i].rows > LPC_MUON_MAX_SIDE || t[i].cols > LPC_MUON_MAX_SIDE || t[i].batch > kMaxPieces) return false;
         const MuonSizes m = muon_sizes(t[i].rows, t[i].cols);
         w->matrices += t[i].batch;
@@ -351,14 +353,13 @@ lpc_status lpc_muon_plan(const lpc_muon_tensor* tensors, int count, lpc_dtype gr
     if (count < 0) return LPC_ERR_SHAPE;
     if (count == 0) return LPC_OK;
     if (!tensors) return LPC_ERR_NULL;
-    const auto empty = [](const lpc_muon_tensor& t) { return t.batch == 0 || t.rows == 0 || t.cols == 0; };
     for (int i = 0; i < count; ++i) {
         const lpc_muon_tensor& t = tensors[i];
-        if (!empty(t) && (!t.param || !t.grad || !t.m)) return LPC_ERR_NULL;
+        if (!empty_tensor(t) && (!t.param || !t.grad || !t.m)) return LPC_ERR_NULL;
     }
     for (int i = 0; i < count; ++i) {
         const lpc_muon_tensor& t = tensors[i];
-        if (!empty(t) && any_misaligned(t.param, t.grad, t.m, t.copy)) return LPC_ERR_ALIGN;
+        if (!empty_tensor(t) && any_misaligned(t.param, t.grad, t.m, t.copy)) return LPC_ERR_ALIGN;
     }
     lpc_muon_work w;
     if (!muon_work(tensors, count, &w)) return LPC_ERR_SHAPE;
@@ -376,7 +377,7 @@ lpc_status lpc_muon_plan(const lpc_muon_tensor* tensors, int count, lpc_dtype gr
     uint64_t space = 0;
     for (int i = 0; i < count; ++i) {
         const lpc_muon_tensor& t = tensors[i];
-        if (empty(t)) continue;
+        if (empty_tensor(t)) continue;
         const MuonSizes sizes = muon_sizes(t.rows, t.cols);
         const size_t n = t.rows * t.cols, side = t.rows < t.cols ? t.rows : t.cols;
         const size_t element = grad_t == LPC_BF16 ? 2 : 4;
@@ -392,7 +393,7 @@ lpc_status lpc_muon_plan(const lpc_muon_tensor* tensors, int count, lpc_dtype gr
             m.ldx = (uint32_t)up(t.cols, kMuonPad);
             m.lda = (uint32_t)up(t.rows < t.cols ? t.rows : t.cols, kMuonPad);
             m.scale = (float)t.scale;
-            m.span = sizes.smalls ? (uint32_t)lpc::muon_span(t.rows < t.cols ? t.cols : t.rows) : 0;
+            m.span = (uint32_t)sizes.span;
             memcpy(matrices + at * sizeof(m), &m, sizeof(m));
             space += sizes.space;
             const auto add = [&](int kind, size_t index) {

@@ -103,7 +103,7 @@ def test_muon_plan(L):  # noqa: F811
     assert plan(L, [row[:3] + (B,) + row[4:]])[0] == ALIGN
     assert plan(L, [row], 5)[0] == DTYPE
     side = 1 << 20
-    for bad in ((1, side + 1, 4), (1, 4, side + 1), (1, side, side), (1 << 40, 4, 4), ((1 << 64) - 1, 4, 4), (1, (1 << 64) - 1, 4)):
+    for bad in ((1, side + 1, 4), (1, 4, side + 1), (2, side, side), (1 << 40, 4, 4), ((1 << 64) - 1, 4, 4), (1, (1 << 64) - 1, 4)):
         t = (lpc._MuonTensor * 1)(lpc._MuonTensor(A, A, A, None, *bad, 1.0))
         work = lpc._MuonWork(9, 9, 9, 9, 9, 9)
         assert L.lpc_muon_plan_bytes(t, 1) == 0
