@@ -64,10 +64,12 @@ struct MmaF16 {
 
 // E2M1 codes; ps, qs: the exponent bytes of the lane's 32 codes of half H in byte H.  In assembly, as the compiler keeps the
 // accumulators of the scaled instruction in other registers than it adds to, and then has not enough of them (it put 60 into
-// memory, and the product took 1.8 times as long).  It does not know then that a result is not there at once: wait() is
-// between the last of these instructions and whatever else touches a result.
+// memory, and the product took 1.8 times as long).  It does not know then which waits these instructions need: ready() is between
+// the last vector instruction that writes an operand and the first of these, wait() between the last of these and whatever else
+// touches a result.
 struct MmaMxfp4 {
     static constexpr bool kScaled = true;
+    static __device__ __forceinline__ void ready() { asm volatile("s_nop 1" ::: "memory"); }  // two states
     static __device__ __forceinline__ void wait() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }  // 24 states; the instruction takes up to 20
     template <int H>
     static __device__ __forceinline__ f32x4_t mul(i32x4_t p, i32x4_t q, f32x4_t c, int ps, int qs) {
@@ -384,9 +386,23 @@ struct Fragments {
     }
 };
 
+// The fragments are in the registers that the following instructions read them from.
+template <typename Mma, int F, int N>
+__device__ __forceinline__ void settle(Fragments<Mma, F, N>& v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v.f[i].h[0]), "+v"(v.f[i].h[1]), "+v"(v.s[i]));
+}
+
 // acc[i][j] += the slab's products
 template <typename Mma, int FQ, int FP, int NQ, int NP>
-__device__ __forceinline__ void multiply(f32x4_t (*acc)[NP], const Fragments<Mma, FQ, NQ>& q, const Fragments<Mma, FP, NP>& p) {
+__device__ __forceinline__ void multiply(f32x4_t (*acc)[NP], Fragments<Mma, FQ, NQ>& q, Fragments<Mma, FP, NP>& p) {
+    if constexpr (Mma::kScaled) {
+        settle(q);
+        settle(p);
+#pragma unroll
+        for (int n = 0; n < NQ * NP; ++n) asm volatile("" : "+v"(acc[n / NP][n % NP]));
+        Mma::ready();
+    }
 #pragma unroll
     for (int n = 0; n < NQ * NP; ++n) {
         f32x4_t& a = acc[n / NP][n % NP];
