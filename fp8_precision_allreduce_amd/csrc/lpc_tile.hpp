@@ -264,7 +264,8 @@ __device__ __forceinline__ void cut(Fragment& f, uint32_t lane, uint32_t count) 
 // wavefronts a SIMD have.  Measured on one card, 8192 x 8192 x 8192 in bf16: 730 us, 1.5 PFLOP/s (the library's product 667);
 // on zeros 561, so that power takes a quarter of it, and a slot 623 cycles.  In 4 bits 278 us, 4.0 PFLOP/s, and 250 on zeros: reads
 // and loads of exponent bytes are 5% of the former.  Phases over halves of a slab's contraction, whose reads are even, took
-// 749 us: loads then start 4 slots before their first read and not 6.
+// 749 us: loads then start 4 slots before their first read and not 6.  With group 1's loads one slot earlier, ahead of its products,
+// it took 841: a wavefront waits while its loads' addresses are taken, which hides behind the other group's products only.
 // ---------------------------------------------------------------------------
 
 constexpr int kTileWaves = 8;
