@@ -456,7 +456,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPla
 // U U^T: the first launch sums that up, in 64 bits and a part of it per workgroup; in the second each workgroup finds R, 32 x 32 in
 // FP32, and applies it to its part of U.  All of its products are FP32 matrix instructions, so that the update is good to
 // about 1e-4 of itself (R is up to 3.4445^5 = 485 where a singular value is small); rounding to fp16 does not average out
-// over so few rows.  Four matrices of 16 x 1152: 23.5 us, bound by latency, against 169 with the tiles' 17 launches.
+// over so few rows.  Four matrices of 16 x 1152: 22.8 to 23.5 us, bound by latency, against 169 with the tiles' 17 launches.
 // ---------------------------------------------------------------------------
 
 typedef double f64x4_t __attribute__((ext_vector_type(4)));
@@ -562,7 +562,7 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_update_kernel(MuonPlan
     const double* sums = reinterpret_cast<const double*>(space + x.space) + threadIdx.x;
     const uint32_t strips = (strip.length + x.span - 1) / x.span;
     double gram[kSums] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (uint32_t c = 0; c < strips; ++c)
 #pragma unroll
         for (int n = 0; n < kSums; ++n) gram[n] += sums[((size_t)c * kSums + n) * kChunkLanes];
