@@ -15,7 +15,7 @@
 // (singular values stay below 1.3, A's below 1.7, B's below 3) far below 65504.
 //
 // What bounds it: eight matrices of 2048 x 7168 (4.6 ms) the updates, 500 us an iteration of which 350 are products and the rest
-// moves X's halves, 8 bytes an element, between rounds of tiles that no compute hides; one of 2048 x 2048 (384 us) the chain of 15
+// moves X's halves, 8 bytes an element, between rounds of tiles that no compute hides; one of 2048 x 2048 (373 to 384 us) the chain of 15
 // products, each one round of small tiles of 23 to 27 us; nine odd ones of 1000 x 1500 and around (315 us) the same chain.
 #include "lpc_tile.hpp"
 
@@ -456,7 +456,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPla
 // U U^T: the first launch sums that up, in 64 bits and a part of it per workgroup; in the second each workgroup finds R, 32 x 32 in
 // FP32, and applies it to its part of U.  All of its products are FP32 matrix instructions, so that the update is good to
 // about 1e-4 of itself (R is up to 3.4445^5 = 485 where a singular value is small); rounding to fp16 does not average out
-// over so few rows.  Four matrices of 16 x 1152: 22.8 to 23.5 us, bound by latency, against 169 with the tiles' 17 launches.
+// over so few rows.  Four matrices of 16 x 1152: 23.3 us, bound by latency, against 169 with the tiles' 17 launches.
 // ---------------------------------------------------------------------------
 
 typedef double f64x4_t __attribute__((ext_vector_type(4)));
