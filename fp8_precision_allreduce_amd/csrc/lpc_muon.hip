@@ -23,7 +23,7 @@ namespace lpc {
 namespace {
 
 constexpr float kHeld = 1024.0f, kLow = 2048.0f;  // what X, A and B are held times; and what a low half is held times besides
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr double kA = 3.4445, kB = -4.7750, kC = 2.0315;
 
 // The plan does not change during a launch and a workgroup's part of it is the same for all lanes: read by scalar loads.
 typedef uint32_t u32x16_t __attribute__((ext_vector_type(16)));
@@ -310,7 +310,7 @@ __device__ __forceinline__ void square_tile(const MuonMatrix& x, const Space& w,
                 [&](uint32_t q, uint32_t p) { return Second ? *reinterpret_cast<const f16x8_t*>(a + (size_t)q * x.lda + p) : f16x8_t{}; },
                 [&](uint32_t q, uint32_t p, f32x8_t v, const f16x8_t& now) {
                     v = v * (1.0f / kHeld);
-                    if (Second) v = v * kC + __builtin_convertvector(now, f32x8_t) * kB;
+                    if (Second) v = v * (float)kC + __builtin_convertvector(now, f32x8_t) * (float)kB;
                     cut_columns(v, p, np);
                     *reinterpret_cast<f16x8_t*>(out + (size_t)(q0 + q) * x.lda + p0 + p) = __builtin_convertvector(v, f16x8_t);
                 });
@@ -319,7 +319,7 @@ __device__ __forceinline__ void square_tile(const MuonMatrix& x, const Space& w,
     store_turned<S>(acc, out + (size_t)p0 * x.lda + q0, x.lda, min(S::BQ, x.lda - q0), np, lds, [&](f32x4_t v, uint32_t q, uint32_t p) {
         v = v * (1.0f / kHeld);
         if (q >= nq || p >= np) return f32x4_t{};
-        if (Second) v = v * kC + __builtin_convertvector(*reinterpret_cast<const f16x4_t*>(a + (size_t)q * x.lda + p), f32x4_t) * kB;
+        if (Second) v = v * (float)kC + __builtin_convertvector(*reinterpret_cast<const f16x4_t*>(a + (size_t)q * x.lda + p), f32x4_t) * (float)kB;
         return v;
     });
 }
@@ -349,7 +349,7 @@ __device__ __forceinline__ void update_tile(const MuonMatrix& x, const Space& w,
                     return Halves{*reinterpret_cast<const f16x8_t*>(high + at), lows & 1 ? *reinterpret_cast<const f16x8_t*>(w.low + at) : f16x8_t{}};
                 },
                 [&](uint32_t q, uint32_t p, f32x8_t v, const Halves& now) {
-                    v = v * (1.0f / kHeld) + (__builtin_convertvector(now.high, f32x8_t) + __builtin_convertvector(now.low, f32x8_t) * (1.0f / kLow)) * kA;
+                    v = v * (1.0f / kHeld) + (__builtin_convertvector(now.high, f32x8_t) + __builtin_convertvector(now.low, f32x8_t) * (1.0f / kLow)) * (float)kA;
                     if (!Last) {
                         cut_columns(v, p, np);
                         const size_t at = first + (size_t)q * x.ldx + p;
@@ -453,10 +453,12 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPla
 
 // ---------------------------------------------------------------------------
 // matrices of a shorter side of at most 32: in two launches.  With U short x long, every X is R U / |u| with R a polynomial of
-// U U^T: the first launch sums that up, in 64 bits and a part of it per workgroup; in the second each workgroup finds R, 32 x 32 in
-// FP32, and applies it to its part of U.  All of its products are FP32 matrix instructions, so that the update is good to
-// about 1e-4 of itself (R is up to 3.4445^5 = 485 where a singular value is small); rounding to fp16 does not average out
-// over so few rows.  Four matrices of 16 x 1152: 23.3 us, bound by latency, against 169 with the tiles' 17 launches.
+// U U^T: the first launch sums that up, a part of it per workgroup; in the second each workgroup finds R, 32 x 32, and applies it
+// to its part of U.  All of it in 64 bits.  X itself is never formed, so that A = P A P is not kept from having negative
+// eigenvalues: where U has no direction, rounding leaves one of about 2^-53 (2^-24 in FP32), and each iteration multiplies it by
+// 3.4445^2: 1e-5 after ten of them, where FP32 passed -1 and diverged from the seventh on.  R is up to 3.4445^10 = 2e5 in directions
+// that U does not have, and that rounding U / |u| to FP32 would give it, so R takes 1 / |u| and U stays as it is.
+// Four matrices of 16 x 1152: 24.5 us, bound by latency, against 169 with the tiles' 17 launches.
 // ---------------------------------------------------------------------------
 
 typedef double f64x4_t __attribute__((ext_vector_type(4)));
@@ -531,17 +533,17 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_sums_kernel(MuonPlan p
     for (int e = 0; e < 4; ++e) out[(wave / 2 * 16 + l4 + 4 * e) * kSide + tj] = sum[e];
 }
 
-// a b of matrices [32][kPitch] that are symmetric and zeros past `side`: the wavefront's 16 x 16 of it.  Two sums, as each of their
-// instructions waits for the one before.
-__device__ __forceinline__ f32x4_t small_product(const float (*a)[kPitch], const float (*b)[kPitch], uint32_t side) {
+// a times b turned, of matrices [32][kPitch] one of which is zeros past `side`: the wavefront's 16 x 16 of it, rows l4 + 4 e.  Two
+// sums, as each of their instructions waits for the one before.
+__device__ __forceinline__ f64x4_t small_product(const double (*a)[kPitch], const double (*b)[kPitch], uint32_t side) {
     const uint32_t wave = threadIdx.x >> 6, l16 = threadIdx.x & 15, l4 = (threadIdx.x & 63) >> 4;
-    const float *row = a[wave / 2 * 16 + l16] + l4, *col = b[wave % 2 * 16 + l16] + l4;
-    f32x4_t sum[2] = {};
+    const double *row = a[wave / 2 * 16 + l16] + l4, *col = b[wave % 2 * 16 + l16] + l4;
+    f64x4_t sum[2] = {};
 #pragma unroll
     for (uint32_t half = 0; half < 2; ++half) {
         if (half && side <= 16) break;
 #pragma unroll
-        for (uint32_t c = half * 16; c < half * 16 + 16; c += 4) sum[c / 4 % 2] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[c], col[c], sum[c / 4 % 2], 0, 0, 0);
+        for (uint32_t c = half * 16; c < half * 16 + 16; c += 4) sum[c / 4 % 2] = __builtin_amdgcn_mfma_f64_16x16x4f64(row[c], col[c], sum[c / 4 % 2], 0, 0, 0);
     }
     return sum[0] + sum[1];
 }
@@ -549,8 +551,11 @@ __device__ __forceinline__ f32x4_t small_product(const float (*a)[kPitch], const
 template <typename Grad>
 __global__ __launch_bounds__(kChunkLanes) void muon_small_update_kernel(MuonPlan plan, uint8_t* space, const float* grad_scale, int iterations,
                                                                         MuonScalars s) {
-    __shared__ float a[kSide][kPitch], p[kSide][kPitch], r[kSide][kPitch], t[kSide][kPitch], u[kBlockCols][kPitch], o[kBlockCols][kPitch];
-    __shared__ double diagonal[kSide];
+    __shared__ double matrices[4][kSide][kPitch], diagonal[kSide];
+    __shared__ float u[kBlockCols][kPitch];
+    double(*a)[kPitch] = matrices[0], (*p)[kPitch] = matrices[1], (*t)[kPitch] = matrices[2], (*r)[kPitch] = matrices[3];  // r: R turned
+    float(*o)[kPitch] = reinterpret_cast<float(*)[kPitch]>(&matrices[0][0][0]);  // once only R is needed
+    static_assert(kBlockCols * sizeof(float) <= 3 * kSide * sizeof(double), "LDS for the outputs");
     const MuonPiece piece = piece_of(plan.smalls, blockIdx.x);
     const MuonMatrix x = matrix_of(plan, piece);
     const Strip strip(x, piece.index);
@@ -578,28 +583,30 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_update_kernel(MuonPlan
 #pragma unroll
     for (int n = 0; n < kSums; ++n) {
         const uint32_t e = n * kChunkLanes + threadIdx.x;
-        a[e / kSide][e % kSide] = (float)(gram[n] * inverse);
+        a[e / kSide][e % kSide] = gram[n] * inverse;
     }
     __syncthreads();
-    const uint32_t row = wave / 2 * 16 + 4 * l4, col = wave % 2 * 16 + l16;  // of four sums, below one another
+    const uint32_t row = wave / 2 * 16 + l4, col = wave % 2 * 16 + l16;  // of four sums, 4 rows apart
     for (int n = 0; n < iterations; ++n) {
-        const f32x4_t square = small_product(a, a, strip.side);  // P = a + b A + c A A
+        // P = a + b A + c A A, A = P (P A)' and R' = R' P'.  Which factor is turned matters, as rounding leaves them not quite alike: R's
+        // part from directions that U does not have to those that it has grows by 3.4445^2 an iteration, and may not be turned round.
+        const f64x4_t square = small_product(a, a, strip.side);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[row + e][col] = (row + e == col ? kA : 0.0f) + kB * a[row + e][col] + kC * square[e];
+        for (int e = 0; e < 4; ++e) p[row + 4 * e][col] = (row + 4 * e == col ? kA : 0.0) + kB * a[row + 4 * e][col] + kC * square[e];
         __syncthreads();
-        const f32x4_t next = n ? small_product(p, r, strip.side) : f32x4_t{};
+        const f64x4_t next = n ? small_product(r, p, strip.side) : f64x4_t{};
         const bool more = n + 1 < iterations;
-        const f32x4_t half = more ? small_product(p, a, strip.side) : f32x4_t{};
+        const f64x4_t half = more ? small_product(p, a, strip.side) : f64x4_t{};
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            r[row + e][col] = n ? next[e] : p[row + e][col];
-            t[row + e][col] = half[e];
+            r[row + 4 * e][col] = (n ? next[e] : p[row + 4 * e][col]) * (more ? 1.0 : by);
+            t[row + 4 * e][col] = half[e];
         }
         __syncthreads();
-        const f32x4_t whole = more ? small_product(p, t, strip.side) : f32x4_t{};
+        const f64x4_t whole = more ? small_product(p, t, strip.side) : f64x4_t{};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[row + e][col] = whole[e];
+        for (int e = 0; e < 4; ++e) a[row + 4 * e][col] = whole[e];
         __syncthreads();
     }
 
@@ -615,23 +622,30 @@ __global__ __launch_bounds__(kChunkLanes) void muon_small_update_kernel(MuonPlan
             const bool in = strip.any(n) && strip.place(n, k0, &at, &i, &k);
             param[n] = in ? x.param[at] : 0.0f;
             const float m = in ? x.m[at] : 0.0f, g = in ? element(grad, at) * scale : 0.0f;
-            value[n] = (float)((double)(s.nesterov ? g * s.rest + m * s.beta : m) * by);
+            value[n] = s.nesterov ? g * s.rest + m * s.beta : m;
         }
 #pragma unroll
         for (int n = 0; n < (int)kPerLane; ++n)
             if (strip.any(n) && strip.place(n, k0, &at, &i, &k)) u[k][i] = value[n];
         __syncthreads();
 #pragma unroll
-        for (int ti = 0; ti < 2; ++ti)
+        for (int ti = 0; ti < 2; ++ti) {
+            if (ti && strip.side <= 16) break;
 #pragma unroll
             for (int tk = 0; tk < 2; ++tk) {
                 const uint32_t k1 = (2 * wave + tk) * 16 + l16;
-                f32x4_t v = {};
+                f64x4_t v = {};
 #pragma unroll
-                for (uint32_t c = 0; c < kSide; c += 4) v = __builtin_amdgcn_mfma_f32_16x16x4f32(r[ti * 16 + l16][c + l4], u[k1][c + l4], v, 0, 0, 0);
+                for (uint32_t half = 0; half < 2; ++half) {
+                    if (half && strip.side <= 16) break;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[k1][ti * 16 + 4 * l4 + e] = v[e];
+                    for (uint32_t c = half * 16; c < half * 16 + 16; c += 4)
+                        v = __builtin_amdgcn_mfma_f64_16x16x4f64(r[c + l4][ti * 16 + l16], (double)u[k1][c + l4], v, 0, 0, 0);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[k1][ti * 16 + l4 + 4 * e] = (float)v[e];
             }
+        }
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < (int)kPerLane; ++n) {

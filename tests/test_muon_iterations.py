@@ -1,0 +1,65 @@
+"""Muon's iterations by themselves, for every number of them and for updates of full and of low rank, against 64 bits.
+
+beta 0 without Nesterov makes m = g and u = g exactly, and parameters of zeros with lr and scale 1 become -X, rounded once: what is
+compared is X alone, on the update that the kernel itself takes.
+
+a = 3.4445 is what an iteration multiplies a small singular value by, and the most that it multiplies a rounding error in a direction that
+the update does not have."""
+import numpy as np
+import pytest
+import torch
+
+from fp8_precision_allreduce_amd import lpc
+from test_matrix_ops_gpu import F32, U, Guarded, dev, orthogonal64, say  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+A = 3.4445
+
+
+def update(rows, cols, kind, seed=0):
+    """Exactly of the rank that its name says: products of small whole numbers are exact."""
+    rng = np.random.RandomState(seed)
+    short, long = min(rows, cols), max(rows, cols)
+    if kind.startswith("rank"):
+        u = rng.randint(-9, 10, (short, int(kind[4:]))).astype(float) @ rng.randint(-9, 10, (int(kind[4:]), long))
+    elif kind == "repeated":
+        u = np.repeat(rng.standard_normal(((short + 3) // 4, long)), 4, 0)[:short]
+    elif kind == "strong":  # a few directions that hide the rest
+        u = rng.standard_normal((short, 2)) @ rng.standard_normal((2, long)) + 0.003 * rng.standard_normal((short, long))
+    else:
+        u = rng.standard_normal((short, long))
+    return torch.from_numpy(u if rows <= cols else u.T.copy()).float()
+
+
+def iterated(dev, g, iterations):  # noqa: F811
+    """The kernel's X of one matrix."""
+    p, m = Guarded(g.shape, F32, dev), Guarded(g.shape, F32, dev)
+    p.t.zero_()
+    m.t.zero_()
+    lpc.Muon([p.t], [g.to(dev)], [m.t], scales=[1.0]).step(lr=1.0, beta=0.0, nesterov=False, iterations=iterations)
+    assert torch.equal(m.check().cpu(), g)
+    return -p.check().cpu().double()
+
+
+def off(got, want):
+    return float((got - want).norm() / want.norm())
+
+
+SMALL = [(4, 64), (16, 16), (16, 1152), (24, 300), (32, 130), (300, 32), (64, 4), (1152, 16), (5, 20000)]
+KINDS = ["rank1", "rank3", "repeated", "strong", "normal"]
+
+
+@pytest.mark.parametrize("iterations", range(1, 11))
+@pytest.mark.parametrize("kind", KINDS)
+def test_short_sides(dev, kind, iterations):  # noqa: F811
+    """A side of 32 and less.  All is 64 bits from u on, and X is rounded to FP32: U.  The update's 64-bit A = U U^T is off by the roundings of
+    at most 200 additions in a row, and each iteration's three products of 32 terms add 100 of what is then there: 300 2^-53 in all.
+    X = R U where R takes A's eigenvalue l = s^2 to x(s) / s, which is a^n at 0: between 0 and l it changes by a^n / l at most, so that
+    d in A changes X by d s a^n / l = d a^n / s, and where s < a^-n, as R is flat there, by d a^2n."""
+    for rows, cols in SMALL:
+        g = update(rows, cols, kind)
+        say("muon", rows, cols, kind, iterations)
+        s = torch.linalg.svdvals(g.double() / g.double().norm())
+        least = max(float(s[s > 1e-9].min()), A ** -iterations)
+        got = off(iterated(dev, g, iterations), orthogonal64(g.double(), iterations))
+        assert got <= U + 300 * 2.0 ** -53 * A ** iterations / least, (rows, cols, got)
