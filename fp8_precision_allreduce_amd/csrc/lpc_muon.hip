@@ -7,14 +7,14 @@
 // shorter side (for a tall matrix X^T X, and X B).  All three products are matrix instructions on fp16 with FP32 sums.
 //
 // Precision.  X is held as fp16 high and low halves of together 22 bits: products take the high half, the term a X both.
-// Directions of small singular values live on that term alone (B is small there), so that they keep their precision.  The last
-// two X before the update do without the low half, as what rounding adds to them is multiplied by 3.4445^2 at most: over
-// spectra of all kinds the update is off by 4e-4 to 2.3e-3 of itself (2-norm; 4e-4 to 2e-3 with all low halves).  With the
-// high half alone it was off by 4e-2 where a few strong directions hide the rest, and bf16 in its place gave 3e-1.  fp16 rather
+// Directions of small singular values live on that term alone (B is small there), so that they keep their precision.  Without the
+// low half of the last two X, as what rounding adds to them is multiplied by 3.4445^2 at most, five iterations took 2.7% less and
+// were 2 to 3 times as far off on updates of low rank or with a few strong directions (three of rank 3: 3.9e-3 of the update
+// against 8e-4, 2-norm).  With the high half alone the update was off by 4e-2 where a few strong directions hide the rest, and bf16 in its place gave 3e-1.  fp16 rather
 // than bf16 as matrices stay within known bounds: X, A and B are held times 2^10, which keeps elements of 2^-24 and up normal and the largest
 // (singular values stay below 1.3, A's below 1.7, B's below 3) far below 65504.
 //
-// What bounds it: eight matrices of 2048 x 7168 (4.6 ms) the updates, 500 us an iteration of which 350 are products and the rest
+// What bounds it: eight matrices of 2048 x 7168 (4.8 ms) the updates, 500 us an iteration of which 350 are products and the rest
 // moves X's halves, 8 bytes an element, between rounds of tiles that no compute hides; one of 2048 x 2048 (373 to 384 us) the chain of 15
 // products, each one round of small tiles of 23 to 27 us; nine odd ones of 1000 x 1500 and around (315 us) the same chain.
 #include "lpc_tile.hpp"
@@ -324,11 +324,10 @@ __device__ __forceinline__ void square_tile(const MuonMatrix& x, const Space& w,
     });
 }
 
-// Rows from q0 and columns from p0 of X = a X + B X (tall: X B); Last: of the parameters with it.  lows: whether X has a low
-// half (1) and gets one (2).
+// Rows from q0 and columns from p0 of X = a X + B X (tall: X B); Last: of the parameters with it.
 template <bool Last, typename S>
-__device__ __forceinline__ void update_tile(const MuonMatrix& x, const Space& w, uint32_t from, uint32_t lows, const MuonScalars& s, uint32_t q0,
-                                            uint32_t p0, uint8_t* lds) {
+__device__ __forceinline__ void update_tile(const MuonMatrix& x, const Space& w, uint32_t from, const MuonScalars& s, uint32_t q0, uint32_t p0,
+                                            uint8_t* lds) {
     const uint32_t nq = min(S::BQ, x.rows - q0), np = min(S::BP, x.cols - p0);
     const _Float16* high = w.high(from);
     f32x4_t acc[S::AQ][S::AP];
@@ -346,7 +345,7 @@ __device__ __forceinline__ void update_tile(const MuonMatrix& x, const Space& w,
     each_run<S>(acc, nq, min(S::BP, x.ldx - p0), lds,
                 [&](uint32_t q, uint32_t p) {
                     const size_t at = first + (size_t)q * x.ldx + p;
-                    return Halves{*reinterpret_cast<const f16x8_t*>(high + at), lows & 1 ? *reinterpret_cast<const f16x8_t*>(w.low + at) : f16x8_t{}};
+                    return Halves{*reinterpret_cast<const f16x8_t*>(high + at), *reinterpret_cast<const f16x8_t*>(w.low + at)};
                 },
                 [&](uint32_t q, uint32_t p, f32x8_t v, const Halves& now) {
                     v = v * (1.0f / kHeld) + (__builtin_convertvector(now.high, f32x8_t) + __builtin_convertvector(now.low, f32x8_t) * (1.0f / kLow)) * (float)kA;
@@ -355,7 +354,7 @@ __device__ __forceinline__ void update_tile(const MuonMatrix& x, const Space& w,
                         const size_t at = first + (size_t)q * x.ldx + p;
                         const f16x8_t h = __builtin_convertvector(v, f16x8_t);
                         *reinterpret_cast<f16x8_t*>(w.high(1 - from) + at) = h;
-                        if (lows & 2) *reinterpret_cast<f16x8_t*>(w.low + at) = low_of(v, h);
+                        *reinterpret_cast<f16x8_t*>(w.low + at) = low_of(v, h);
                         return;
                     }
                     const size_t at = (size_t)(q0 + q) * x.cols + p0 + p;
@@ -439,16 +438,15 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void muon_square_kernel(MuonPla
 }
 
 template <bool Last>
-__global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPlan plan, uint32_t all, uint8_t* space, uint32_t from,
-                                                                          uint32_t lows, MuonScalars s) {
+__global__ __launch_bounds__(kTileWaves * 64, 2) void muon_update_kernel(MuonPlan plan, uint32_t all, uint8_t* space, uint32_t from, MuonScalars s) {
     __shared__ __attribute__((aligned(128))) uint8_t lds[kLdsBytes];
     Turn t;
     if (!find_turn(all, &t)) return;
     const MuonPiece piece = piece_of(plan.updates, t.tile);
     const MuonMatrix x = matrix_of(plan, piece);
     const Space w = space_of(x, space);
-    do_turn(piece, t.part, x.rows, x.cols, [&](uint32_t q, uint32_t p) { update_tile<Last, Large>(x, w, from, lows, s, q, p, lds); },
-            [&](uint32_t q, uint32_t p) { update_tile<Last, Small>(x, w, from, lows, s, q, p, lds); });
+    do_turn(piece, t.part, x.rows, x.cols, [&](uint32_t q, uint32_t p) { update_tile<Last, Large>(x, w, from, s, q, p, lds); },
+            [&](uint32_t q, uint32_t p) { update_tile<Last, Small>(x, w, from, s, q, p, lds); });
 }
 
 // ---------------------------------------------------------------------------
@@ -679,12 +677,12 @@ hipError_t launch_muon(const MuonPlan& plan, const MuonCounts& n, int grad_bf16,
         e = grad_bf16 ? enqueue(muon_start_kernel<uint16_t>, dim3(n.chunks), few, stream, plan, w, grad_scale, s)
                       : enqueue(muon_start_kernel<float>, dim3(n.chunks), few, stream, plan, w, grad_scale, s);
     for (int i = 0; i < iterations && e == hipSuccess; ++i) {
-        const uint32_t from = i & 1, lows = (i + 3 <= iterations ? 1u : 0u) | (i + 4 <= iterations ? 2u : 0u);
+        const uint32_t from = i & 1;
         e = enqueue(muon_square_kernel<false>, dim3(turns(n.squares)), lanes, stream, plan, n.squares, w, from);
         if (e == hipSuccess) e = enqueue(muon_square_kernel<true>, dim3(turns(n.squares)), lanes, stream, plan, n.squares, w, from);
         if (e == hipSuccess)
-            e = i + 1 < iterations ? enqueue(muon_update_kernel<false>, dim3(turns(n.updates)), lanes, stream, plan, n.updates, w, from, lows, s)
-                                   : enqueue(muon_update_kernel<true>, dim3(turns(n.updates)), lanes, stream, plan, n.updates, w, from, lows, s);
+            e = i + 1 < iterations ? enqueue(muon_update_kernel<false>, dim3(turns(n.updates)), lanes, stream, plan, n.updates, w, from, s)
+                                   : enqueue(muon_update_kernel<true>, dim3(turns(n.updates)), lanes, stream, plan, n.updates, w, from, s);
     }
     return e;
 }

@@ -63,3 +63,28 @@ def test_short_sides(dev, kind, iterations):  # noqa: F811
         least = max(float(s[s > 1e-9].min()), A ** -iterations)
         got = off(iterated(dev, g, iterations), orthogonal64(g.double(), iterations))
         assert got <= U + 300 * 2.0 ** -53 * A ** iterations / least, (rows, cols, got)
+
+
+def strong_and_weak(side, other, weak, seed=0):
+    """One element of 1 and, in rows and columns of their own, a block of norm `weak` whose singular values are alike."""
+    u = torch.zeros(side, other, dtype=torch.float64)
+    block = torch.from_numpy(np.linalg.qr(np.random.RandomState(seed).standard_normal((other - 1, side - 1)))[0].T.copy())
+    u[0, 0], u[1:, 1:] = 1.0, block * (weak / (side - 1) ** 0.5)
+    return u.float()
+
+
+@pytest.mark.parametrize("turned", [False, True])
+@pytest.mark.parametrize("iterations", range(1, 7))
+def test_weak_directions_keep_22_bits(dev, iterations, turned):  # noqa: F811
+    """Longer sides than 32: X is held in 22 bits at every iteration.  What an iteration adds to a block of singular values s of 1e-3 at
+    most by products is b s^2 = 4.8e-6 of it, 2^-11 of which counts for each of the three roundings to fp16 in it.  The rest of the block
+    is a X: two halves of 11 bits leave 2^-22 of an element, and FP32's steps to it (the product by 1/1024, the low half's, their sum, by
+    a, and the sum with the product) 5 U.  The start is rounded to FP32 and to the halves, the result once."""
+    for side, other in ((40, 90), (64, 64), (130, 300)):
+        g = strong_and_weak(side, other, 1e-3 * (side - 1) ** 0.5 / A ** iterations)
+        g = g.T.contiguous() if turned else g
+        say("muon", tuple(g.shape), iterations)
+        got, want = iterated(dev, g, iterations), orthogonal64(g.double(), iterations)
+        bound = iterations * (2.0 ** -22 + 5 * U + 3 * 2.0 ** -11 * 4.8e-6) + 2.0 ** -22 + 2 * U
+        assert off(got[1:, 1:], want[1:, 1:]) <= bound, (side, other, off(got[1:, 1:], want[1:, 1:]), bound)
+        assert (got[0, 1:] == 0).all() and (got[1:, 0] == 0).all()
