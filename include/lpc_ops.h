@@ -349,10 +349,11 @@ lpc_status lpc_muon_plan(const lpc_muon_tensor *tensors, int count, lpc_dtype gr
  *   param = param (1 - lr weight_decay) - lr scale X
  * m and the parameters' last line in FP32, every operation rounded on its own;
  * |u| in 64 bits.  X is held in fp16 halves of together 22 bits and the products
- * take its high half, A and B in fp16, sums in FP32: after five iterations X is
- * off by 2.5e-3 of itself (2-norm) at most on the matrices measured, whatever
- * their singular values; where rows or cols is 32 or less, u is FP32 and all from
- * there to the last line in 64 bits.
+ * take its high half, A and B in fp16, sums in FP32.  On the matrices measured,
+ * of full and of low rank, X is off by at most 3.2e-3 of itself (2-norm) after
+ * five iterations; after ten by 7.2e-3, and by 2.2e-2 where its rank is low, as in
+ * FP32 throughout.  Where rows or cols is 32 or less, u is FP32 and all from there
+ * to the last line in 64 bits.
  *   plan   DEVICE copy of the plan;  work, grad_t as planned
  *   workspace  device memory of work->workspace_bytes, no initial contents
  *      needed; steps that overlap need one each

@@ -88,3 +88,20 @@ def test_weak_directions_keep_22_bits(dev, iterations, turned):  # noqa: F811
         bound = iterations * (2.0 ** -22 + 5 * U + 3 * 2.0 ** -11 * 4.8e-6) + 2.0 ** -22 + 2 * U
         assert off(got[1:, 1:], want[1:, 1:]) <= bound, (side, other, off(got[1:, 1:], want[1:, 1:]), bound)
         assert (got[0, 1:] == 0).all() and (got[1:, 0] == 0).all()
+
+
+@pytest.mark.parametrize("iterations", range(1, 11))
+@pytest.mark.parametrize("kind", KINDS + ["rank40"])
+def test_long_sides(dev, kind, iterations):  # noqa: F811
+    """Longer sides than 32, updates of any rank.  Products of operands in fp16 leave X of singular values of 1 off by 1.2e-3 of itself in the mean and
+    by 5.3e-3 at most (off_by in test_matrix_ops_gpu has the sum), and a later iteration multiplies that by 1.3 in the mean.  Means hold
+    where roundings are independent: not where rows are the same or one multiple of each other.  Directions that the update does not have
+    get 2^-22 of it from X's two halves at most, times a at each iteration."""
+    each = 5.3e-3 if kind in ("rank1", "repeated") else 1.2e-3
+    bound = each * sum(1.3 ** (2 * i) for i in range(iterations)) ** 0.5 + 2.0 ** -22 * A ** iterations
+    for rows, cols in ((33, 33), (40, 90), (130, 64), (128, 512), (300, 200), (450, 700)):
+        g = update(rows, cols, kind)
+        say("muon", rows, cols, kind, iterations)
+        want = orthogonal64(g.double().to(dev), iterations).cpu()
+        got = off(iterated(dev, g, iterations), want)
+        assert got <= bound, (rows, cols, got, bound)
