@@ -124,7 +124,7 @@ template <int M, typename Out>
 hipError_t launch_rows(const Gemm16Args& a, hipStream_t stream) {
     const uint64_t tiles_p = (outputs_p<M>(a) + (uint64_t)Large::BP - 1) / Large::BP;
     const uint64_t wgs = shares<Large, Small>(most_tiles(a.counts, a.groups, a.rows, Large::BQ) * tiles_p);
-    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    if (!launchable(wgs, kTileWaves)) return hipErrorInvalidConfiguration;
     return enqueue(gemm16_rows_kernel<M, Out>, dim3((uint32_t)wgs), dim3(kTileWaves * 64), stream, a);
 }
 
@@ -136,16 +136,21 @@ uint64_t wgrad_tiles(const Gemm16Args& a) {
 template <typename Out, typename S>
 hipError_t launch_wgrad(const Gemm16Args& a, hipStream_t stream) {
     const uint64_t wgs = wgrad_tiles<S>(a);
-    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    if (!launchable(wgs, kTileWaves)) return hipErrorInvalidConfiguration;
     return enqueue(gemm16_wgrad_kernel<Out, S>, dim3((uint32_t)wgs, a.groups), dim3(kTileWaves * 64), stream, a);
+}
+
+template <int M, typename S>
+uint64_t narrow_workgroups(const Gemm16Args& a) {
+    const uint64_t tiles_q = M == kWgrad ? (a.n + (uint64_t)S::BQ - 1) / S::BQ : most_tiles(a.counts, a.groups, a.rows, S::BQ);
+    const uint64_t tiles = tiles_q * ((outputs_p<M>(a) + (uint64_t)S::BP - 1) / S::BP);
+    return M == kWgrad ? tiles : even_workgroups(tiles);
 }
 
 template <int M, typename Out, int QF, int PF, int Depth>
 hipError_t launch_narrow(const Gemm16Args& a, hipStream_t stream) {
     using S = NarrowOf<QF, PF, Depth, false>;
-    const uint64_t tiles_q = M == kWgrad ? (a.n + (uint64_t)S::BQ - 1) / S::BQ : most_tiles(a.counts, a.groups, a.rows, S::BQ);
-    const uint64_t tiles = tiles_q * ((outputs_p<M>(a) + (uint64_t)S::BP - 1) / S::BP), wgs = M == kWgrad ? tiles : even_workgroups(tiles);
-    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    const uint64_t wgs = narrow_workgroups<M, S>(a);
     return enqueue(gemm16_narrow_kernel<M, Out, S>, dim3((uint32_t)wgs, M == kWgrad ? a.groups : 1), dim3(kNarrowWaves * 64), stream, a);
 }
 
@@ -157,7 +162,7 @@ hipError_t launch_narrow(const Gemm16Args& a, hipStream_t stream) {
 //   more than 384 of 64 x 64 tiles: 8192 x 8192, 256 rows 154 / 101 / 82 / 74; 2048 x 2048 x 2048 89 / 56 / 49 / 22
 //   more than 128            64 x 64: 128 rows 82 / 56 / 45 / 75; 777 rows over 3 weights of 1160 x 1000 17 / 13 / 9.7 / 16
 //   more than 128 of 64 x 32 64 x 32: 64 rows 44 / 35 / 43 / 63
-//   otherwise                32 x 32
+//   otherwise                32 x 32, and tiles where there are more of them than a launch can have (2^24)
 // The gradients, 64 x 64 / tiles: up to 256 of 64 x 64, 1024 x 1024 x 1024 10.2 / 12.5 (rows) and 9.8 / 13.1 (weights); more, 777
 // rows as above 15.4 / 14.6 and 18 / 11.5.  The weights' are large tiles where there are more than 128 of these, else small
 // ones: 2048 rows, 4096 x 2048 55 / 46, 4096 x 4096 69 / 89.
@@ -177,6 +182,7 @@ hipError_t launch(const Gemm16Args& a, hipStream_t stream) {
                 if (high * wide > 128) return launch_narrow<M, Out, 4, 4, 2>(a, stream);
                 if (high * ((a.n + 31ull) / 32) > 128) return launch_narrow<M, Out, 4, 2, 2>(a, stream);
             }
+            if (!launchable(narrow_workgroups<M, NarrowOf<2, 2, 3, false>>(a), kNarrowWaves)) return launch_rows<M, Out>(a, stream);
             return launch_narrow<M, Out, 2, 2, 3>(a, stream);
         }
     }

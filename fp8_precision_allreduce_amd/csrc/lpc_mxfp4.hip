@@ -151,15 +151,19 @@ template <typename Out>
 hipError_t launch_tiled(const Mxfp4Args& a, hipStream_t stream) {
     const uint64_t tiles_p = (a.n + (uint64_t)Large::BP - 1) / Large::BP;
     const uint64_t wgs = shares<Large, Small>(most_tiles(a.counts, a.groups, a.rows, Large::BQ) * tiles_p);
-    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    if (!launchable(wgs, kTileWaves)) return hipErrorInvalidConfiguration;
     return enqueue(mxfp4_kernel<Out>, dim3((uint32_t)wgs), dim3(kTileWaves * 64), stream, a);
+}
+
+template <typename S>
+uint64_t narrow_workgroups(const Mxfp4Args& a) {
+    return even_workgroups(most_tiles(a.counts, a.groups, a.rows, S::BQ) * ((a.n + (uint64_t)S::BP - 1) / S::BP));
 }
 
 template <typename Out, int QF, int PF, int Depth>
 hipError_t launch_narrow(const Mxfp4Args& a, hipStream_t stream) {
     using S = NarrowOf<QF, PF, Depth, true>;
-    const uint64_t wgs = even_workgroups(most_tiles(a.counts, a.groups, a.rows, S::BQ) * ((a.n + (uint64_t)S::BP - 1) / S::BP));
-    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
+    const uint64_t wgs = narrow_workgroups<S>(a);
     return enqueue(mxfp4_narrow_kernel<Out, S>, dim3((uint32_t)wgs), dim3(kNarrowWaves * 64), stream, a);
 }
 
@@ -172,7 +176,7 @@ hipError_t launch_narrow(const Mxfp4Args& a, hipStream_t stream) {
 //                            2048 27 / 31 / 23 / 11.8
 //   more than 128            64 x 64: 128 rows 27 / 24 / 18.7 / 36; 777 x 1152 x 1001 7.7 / 8.8 / 7.4 / 12.6
 //   more than 128 of 64 x 32 64 x 32: 64 rows 16.4 / 14.9 / 18.5 / 31
-//   otherwise                32 x 32
+//   otherwise                32 x 32, and tiles where there are more of them than a launch can have (2^24)
 template <typename Out>
 hipError_t launch(const Mxfp4Args& a, hipStream_t stream) {
     if (a.rows > 32ull * a.groups) {
@@ -181,6 +185,7 @@ hipError_t launch(const Mxfp4Args& a, hipStream_t stream) {
         if (high * wide > 128) return launch_narrow<Out, 4, 4, 2>(a, stream);
         if (high * ((a.n + 31ull) / 32) > 128) return launch_narrow<Out, 4, 2, 2>(a, stream);
     }
+    if (!launchable(narrow_workgroups<NarrowOf<2, 2, 2, true>>(a), kNarrowWaves)) return launch_tiled<Out>(a, stream);
     return launch_narrow<Out, 2, 2, 2>(a, stream);
 }
 

@@ -828,6 +828,9 @@ __device__ __forceinline__ bool find_share(const int32_t* counts, uint32_t group
     return s->p0 < s->p1;
 }
 
+// whether one launch can have that many workgroups: lanes along x are counted in 32 bits
+constexpr bool launchable(uint64_t wgs, uint32_t waves) { return wgs < (1ull << 32) / (waves * 64); }
+
 // workgroups that cover what any counts make of `most_tiles` tiles: up to kMostSplit tiles of every XCD are split
 template <typename L, typename Small>
 uint64_t shares(uint64_t most_tiles) {

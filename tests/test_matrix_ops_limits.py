@@ -1,0 +1,48 @@
+"""The matrix operators at what a launch can hold."""
+import pytest
+import torch
+
+from fp8_precision_allreduce_amd import lpc
+from test_matrix_ops_gpu import BF16, MX, dev, mx_oracle, near, randn, say  # noqa: F401
+
+
+def room(gib):
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip("needs %d GiB of device memory" % gib)
+
+
+def columns(n):
+    return torch.tensor([0, 1, 255, 256, n // 2 - 1, n // 2, n - 257, n - 2, n - 1])
+
+
+@pytest.mark.gpu
+def test_bf16_few_rows_and_many_outputs(dev):  # noqa: F811
+    """More tiles of 32 x 32 than a launch can have."""
+    room(40)
+    rows, n, k, counts = 64, (1 << 27) + 5, 8, [33, 31]
+    say("bf16", rows, n, k)
+    x, w = randn(rows, k, seed=1).to(BF16), torch.randn(2, n, k, device=dev).to(BF16)
+    out = torch.full((rows, n), 7.0, dtype=BF16, device=dev)
+    lpc.lpc_gemm_bf16(x.to(dev), w, out, counts=torch.tensor(counts, dtype=torch.int32, device=dev))
+    at = columns(n)
+    for g, (a, b) in enumerate(((0, 33), (33, 64))):
+        xd, wd = x[a:b].double(), w[g, at.to(dev)].cpu().double()
+        near(out[a:b, at.to(dev)], xd @ wd.t(), xd.abs() @ wd.abs().t(), k, BF16, "group %d" % g)
+
+
+@pytest.mark.gpu
+def test_mxfp4_few_rows_and_many_outputs(dev):  # noqa: F811
+    room(60)
+    rows, n, k, counts = 64, (1 << 27) + 5, 128, [33, 31]
+    say("mxfp4", rows, n, k)
+    xc, xs, x = mx_oracle(randn(rows, k, seed=1))
+    at = columns(n)
+    wc, ws, w = mx_oracle(randn(2, len(at), k, seed=2))
+    codes = torch.zeros(2, n, k // 2, dtype=torch.uint8, device=dev)
+    scales = torch.zeros(2, n, k // MX, dtype=torch.uint8, device=dev)
+    codes[:, at.to(dev)], scales[:, at.to(dev)] = wc.to(dev), ws.to(dev)
+    out = torch.full((rows, n), 7.0, dtype=BF16, device=dev)
+    lpc.lpc_gemm_mxfp4(xc.to(dev), xs.to(dev), codes, scales, out, counts=torch.tensor(counts, dtype=torch.int32, device=dev))
+    for g, (a, b) in enumerate(((0, 33), (33, 64))):
+        near(out[a:b, at.to(dev)], x[a:b] @ w[g].t(), x[a:b].abs() @ w[g].abs().t(), k, BF16, "group %d" % g)
+    assert not out[:, 1000:2000].any()
