@@ -28,6 +28,9 @@ bool bad_dtype(lpc_dtype t) { return t != LPC_F32 && t != LPC_BF16; }
 
 lpc_status hip_status(hipError_t e) { return e == hipSuccess ? LPC_OK : LPC_ERR_HIP; }
 
+// of a launcher that finds what no launch can have before it makes any
+lpc_status launch_status(hipError_t e) { return e == hipErrorInvalidConfiguration ? LPC_ERR_SHAPE : hip_status(e); }
+
 constexpr size_t kMaxDim = (size_t)1 << 31;
 
 // a x b elements, both below 2^31
@@ -287,7 +290,7 @@ lpc_status lpc_gemm_bf16(const uint16_t* x, size_t rows, size_t k, const uint16_
     if (any_null(x, w) || !out || missing_counts(groups, counts)) return LPC_ERR_NULL;
     if (any_misaligned(x, w, out) || misaligned4(counts)) return LPC_ERR_ALIGN;
     if (k == 0 || k % 8 || bad_product(rows, n, k, groups)) return LPC_ERR_SHAPE;
-    return hip_status(lpc::launch_gemm16(x, rows, k, w, n, groups, counts, out, out_t == LPC_BF16, stream));
+    return launch_status(lpc::launch_gemm16(x, rows, k, w, n, groups, counts, out, out_t == LPC_BF16, stream));
 }
 
 lpc_status lpc_gemm_bf16_dgrad(const uint16_t* dy, size_t rows, size_t n, const uint16_t* w, size_t k, int groups,
@@ -297,7 +300,7 @@ lpc_status lpc_gemm_bf16_dgrad(const uint16_t* dy, size_t rows, size_t n, const 
     if (any_null(dy, w) || !dx || missing_counts(groups, counts)) return LPC_ERR_NULL;
     if (any_misaligned(dy, w, dx) || misaligned4(counts)) return LPC_ERR_ALIGN;
     if (n == 0 || n % 8 || k % 8 || bad_product(rows, n, k, groups)) return LPC_ERR_SHAPE;
-    return hip_status(lpc::launch_gemm16_dgrad(dy, rows, n, w, k, groups, counts, dx, out_t == LPC_BF16, stream));
+    return launch_status(lpc::launch_gemm16_dgrad(dy, rows, n, w, k, groups, counts, dx, out_t == LPC_BF16, stream));
 }
 
 lpc_status lpc_gemm_bf16_wgrad(const uint16_t* dy, size_t n, const uint16_t* x, size_t k, size_t rows, int groups,
@@ -307,7 +310,7 @@ lpc_status lpc_gemm_bf16_wgrad(const uint16_t* dy, size_t n, const uint16_t* x, 
     if (!dw || missing_counts(groups, counts) || (rows != 0 && any_null(dy, x))) return LPC_ERR_NULL;
     if (any_misaligned(dy, x, dw) || misaligned4(counts)) return LPC_ERR_ALIGN;
     if (n % 8 || k % 8 || bad_product(rows, n, k, groups)) return LPC_ERR_SHAPE;
-    return hip_status(lpc::launch_gemm16_wgrad(dy, n, x, k, rows, groups, counts, dw, out_t == LPC_BF16, stream));
+    return launch_status(lpc::launch_gemm16_wgrad(dy, n, x, k, rows, groups, counts, dw, out_t == LPC_BF16, stream));
 }
 
 lpc_status lpc_quantize_mxfp4(const void* x, lpc_dtype in, size_t n, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
@@ -336,7 +339,7 @@ lpc_status lpc_gemm_mxfp4(const uint8_t* x, const uint8_t* xs, size_t rows, size
     if (any_null(x, xs, w, ws) || !out || missing_counts(groups, counts)) return LPC_ERR_NULL;
     if (any_misaligned(x, xs, w, ws, out) || misaligned4(counts)) return LPC_ERR_ALIGN;
     if (k == 0 || k % LPC_BLOCK || bad_product(rows, n, k, groups)) return LPC_ERR_SHAPE;
-    return hip_status(lpc::launch_gemm_mxfp4(x, xs, rows, k, w, ws, n, groups, counts, out, out_t == LPC_BF16, stream));
+    return launch_status(lpc::launch_gemm_mxfp4(x, xs, rows, k, w, ws, n, groups, counts, out, out_t == LPC_BF16, stream));
 }
 
 size_t lpc_muon_plan_bytes(const lpc_muon_tensor* tensors, int count) {

@@ -235,8 +235,10 @@ lpc_status lpc_adamw_step(const void *plan, size_t chunks, lpc_dtype grad_t, int
  *      count is taken as 0, groups end at `rows`, rows past the last group give
  *      zeros; may be NULL when groups == 1
  *   k a positive multiple of 8; any n; k, n < LPC_MAX_ROW, rows < 2^31,
- *   groups in 1..LPC_MAX_GROUPS, each matrix at most LPC_MAX_MATRIX elements
- *   (else LPC_ERR_SHAPE).  rows == 0 or n == 0: LPC_OK, no work.             */
+ *   groups in 1..LPC_MAX_GROUPS, each matrix at most LPC_MAX_MATRIX elements,
+ *   and of the result at most 2^23 - 512 tiles of 256 x 256, where each group's rows
+ *   count as whole tiles (else LPC_ERR_SHAPE).  rows == 0 or n == 0: LPC_OK, no
+ *   work.                                                                    */
 lpc_status lpc_gemm_bf16(const uint16_t *x, size_t rows, size_t k,
                          const uint16_t *w, size_t n, int groups, const int32_t *counts,
                          void *out, lpc_dtype out_t, hipStream_t stream);
@@ -253,8 +255,9 @@ lpc_status lpc_gemm_bf16_dgrad(const uint16_t *dy, size_t rows, size_t n,
 /* Gradient of the weights: dw[g, j, i] = sum over the rows r of group g of
  * dy[r, j] * x[r, i]; zeros for a group without rows.
  *   dy [rows, n], x [rows, k] bf16; dw [groups, n, k] of type out_t
- *   n and k multiples of 8 (else LPC_ERR_SHAPE).  n == 0 or k == 0: LPC_OK, no
- *   work; rows == 0 writes zeros (dy and x may then be NULL).                */
+ *   n and k multiples of 8 (else LPC_ERR_SHAPE), the rest as above, with the
+ *   tiles of each dw[g] by itself.  n == 0 or k == 0: LPC_OK, no work; rows == 0
+ *   writes zeros (dy and x may then be NULL).                                */
 lpc_status lpc_gemm_bf16_wgrad(const uint16_t *dy, size_t n, const uint16_t *x, size_t k,
                                size_t rows, int groups, const int32_t *counts,
                                void *dw, lpc_dtype out_t, hipStream_t stream);

@@ -1,9 +1,25 @@
-"""The matrix operators at what a launch can hold."""
+"""The matrix operators at what a launch can hold: calls past it are refused before anything runs, and those below it run."""
 import pytest
 import torch
 
 from fp8_precision_allreduce_amd import lpc
 from test_matrix_ops_gpu import BF16, MX, dev, mx_oracle, near, randn, say  # noqa: F401
+from test_ops_abi_cpu import A, HIP, L, SHAPE  # noqa: F401
+from test_ops_abi_cpu import BF16 as BF16_T
+
+MOST = (1 << 23) - 512  # tiles of 256 x 256
+
+
+def test_products_past_a_launch(L):  # noqa: F811
+    """No device here: a call that passes the checks comes to LPC_ERR_HIP."""
+    product = lambda rows, n, k: L.lpc_gemm_bf16(A, rows, k, A, n, 1, None, A, BF16_T, None)  # noqa: E731
+    dgrad = lambda rows, n, k: L.lpc_gemm_bf16_dgrad(A, rows, n, A, k, 1, None, A, BF16_T, None)  # noqa: E731
+    wgrad = lambda n, k: L.lpc_gemm_bf16_wgrad(A, n, A, k, 8, 1, None, A, BF16_T, None)  # noqa: E731
+    mxfp4 = lambda rows, n, k: L.lpc_gemm_mxfp4(A, A, rows, k, A, A, n, 1, None, A, BF16_T, None)  # noqa: E731
+    assert product(MOST * 256, 1, 8) == HIP and product((1 << 31) - 1, 1, 8) == SHAPE
+    assert dgrad(MOST * 256, 8, 8) == HIP and dgrad((1 << 31) - 1, 8, 8) == SHAPE
+    assert wgrad(1 << 20, 1 << 18) == HIP and wgrad(1 << 20, 1 << 19) == SHAPE
+    assert mxfp4(MOST * 256, 1, 128) == HIP and mxfp4((1 << 31) - 1, 1, 128) == SHAPE
 
 
 def room(gib):
