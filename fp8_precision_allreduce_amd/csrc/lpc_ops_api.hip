@@ -70,8 +70,9 @@ bool bad_product(size_t rows, size_t n, size_t k, int groups) {
     return n >= LPC_MAX_ROW || k >= LPC_MAX_ROW || bad_groups(groups) || too_many(rows, k) || too_many(n, k) || too_many(rows, n) || n * k > LPC_MAX_MATRIX / (size_t)groups;
 }
 
-// pieces of a matrix optimizer's plan, of each kind
-constexpr size_t kMaxPieces = (size_t)1 << 24;
+// A matrix optimizer's plan has what its launches can hold, whose lanes are counted in 32 bits: workgroups of 256 for chunks and
+// small matrices, of 512 for tiles, up to 384 of which more than there are tiles where these are split.
+constexpr size_t kMaxPieces = ((size_t)1 << 24) - 1, kMaxTiles = ((size_t)1 << 23) - 512;
 constexpr size_t kMuonPad = 64;  // elements that rows of its workspace are padded to
 
 size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
@@ -93,6 +94,10 @@ MuonSizes muon_sizes(size_t rows, size_t cols) {
     return {chunks, side * (side + 1) / 2, tiles, 0, up(bytes, 128), span};
 }
 
+bool too_much_work(const lpc_muon_work& w) {
+    return w.matrices > kMaxPieces || w.chunks > kMaxPieces || w.smalls > kMaxPieces || w.squares > kMaxTiles || w.updates > kMaxTiles;
+}
+
 bool empty_tensor(const lpc_muon_tensor& t) { return t.batch == 0 || t.rows == 0 || t.cols == 0; }
 
 // false: refused
@@ -108,7 +113,7 @@ bool muon_work(const lpc_muon_tensor* t, int count, lpc_muon_work* w) {
         w->updates += t[i].batch * m.updates;
         w->smalls += t[i].batch * m.smalls;
         w->workspace_bytes += t[i].batch * m.space;  // below 2^24 tiles of 2^20 bytes
-        if (w->chunks > kMaxPieces || w->squares > kMaxPieces || w->updates > kMaxPieces || w->smalls > kMaxPieces) return false;
+        if (too_much_work(*w)) return false;
     }
     return true;
 }
@@ -430,8 +435,7 @@ lpc_status lpc_muon_step(const void* plan, const lpc_muon_work* work, lpc_dtype 
     if (work->matrices == 0) return LPC_OK;
     if (!plan || !workspace) return LPC_ERR_NULL;
     if (misaligned(plan) || misaligned(workspace) || misaligned4(grad_scale)) return LPC_ERR_ALIGN;
-    if (work->matrices > kMaxPieces || work->chunks > kMaxPieces || work->squares > kMaxPieces || work->updates > kMaxPieces || work->smalls > kMaxPieces ||
-        workspace_bytes < work->workspace_bytes || !(beta >= 0.0 && beta < 1.0) || iterations < 1 ||
+    if (too_much_work(*work) || workspace_bytes < work->workspace_bytes || !(beta >= 0.0 && beta < 1.0) || iterations < 1 ||
         iterations > LPC_MUON_MAX_ITERATIONS)
         return LPC_ERR_SHAPE;
     const uint8_t* b = static_cast<const uint8_t*>(plan);

@@ -338,8 +338,9 @@ size_t lpc_muon_plan_bytes(const lpc_muon_tensor *tensors, int count);
  * lpc_muon_plan_bytes bytes); the caller copies it to a 16-byte aligned device
  * buffer and keeps it as long as the tensors stay where they are.
  *   Tensors without elements are left out.  rows and cols at most
- *   LPC_MUON_MAX_SIDE, at most 2^24 tiles of 256 x 256 and as many chunks of 4096
- *   elements (else LPC_ERR_SHAPE).  Tensors must not overlap.                */
+ *   LPC_MUON_MAX_SIDE; of all matrices together at most 2^23 - 512 tiles of
+ *   256 x 256, and fewer than 2^24 matrices and chunks of 4096 elements (else
+ *   LPC_ERR_SHAPE).  Tensors must not overlap.                               */
 lpc_status lpc_muon_plan(const lpc_muon_tensor *tensors, int count, lpc_dtype grad_t,
                          void *plan, size_t plan_bytes, lpc_muon_work *work);
 

@@ -22,6 +22,24 @@ def test_products_past_a_launch(L):  # noqa: F811
     assert mxfp4(MOST * 256, 1, 128) == HIP and mxfp4((1 << 31) - 1, 1, 128) == SHAPE
 
 
+def muon_bytes(L, *rows):  # noqa: F811
+    return L.lpc_muon_plan_bytes((lpc._MuonTensor * len(rows))(*[lpc._MuonTensor(A, A, A, None, *r, 1.0) for r in rows]), len(rows))
+
+
+def test_muon_plans_what_its_steps_can_launch(L):  # noqa: F811
+    """A plan that no step takes is refused when it is made, and a step refuses it before its first launch, which changes the momenta."""
+    few = (1 << 24) - 1
+    assert muon_bytes(L, (MOST, 33, 33)) and not muon_bytes(L, (MOST + 1, 33, 33))          # tiles of both products
+    assert muon_bytes(L, (few, 4, 4)) and not muon_bytes(L, (few + 1, 4, 4))                # small matrices
+    assert muon_bytes(L, (MOST, 33, 33), (1 << 23, 4, 4)) and not muon_bytes(L, (MOST, 33, 33), (few, 4, 4))   # all matrices
+    step = lambda work: L.lpc_muon_step(A, work, 0, 0.1, 0.9, 1, 0.0, 5, None, A, 1 << 40, None)  # noqa: E731
+    for field, most in (("matrices", few), ("chunks", few), ("smalls", few), ("squares", MOST), ("updates", MOST)):
+        for n, status in ((most, HIP), (most + 1, SHAPE)):
+            work = lpc._MuonWork(1, 1, 1, 1, 1, 64)
+            setattr(work, field, n)
+            assert step(work) == status, (field, n)
+
+
 def room(gib):
     if torch.cuda.mem_get_info()[0] < gib << 30:
         pytest.skip("needs %d GiB of device memory" % gib)
