@@ -1,6 +1,8 @@
 // lpc_mxfp4.hip -- microscaled 4-bit floating point: E2M1 codes, two to a byte (the first in the low bits), with one
 // power-of-two scale, an exponent byte e standing for 2^(e - 127), per 32 elements.  Quantization, its inverse, and the
 // product of two matrices held so, dense or with one weight per group of rows.
+#include <algorithm>
+
 #include "lpc_tile.hpp"
 
 namespace lpc {
@@ -74,6 +76,34 @@ __global__ __launch_bounds__(kCodecLanes) void mx_dequantize_kernel(const uint8_
         __builtin_nontemporal_store(u32x4_t{pack_bf16x2(a[0], a[1]), pack_bf16x2(b[0], b[1]), pack_bf16x2(c[0], c[1]), pack_bf16x2(d[0], d[1])},
                                     reinterpret_cast<u32x4_t*>(out) + i);
     }
+}
+
+// Lanes of one launch, which counts them in 32 bits: longer tensors take several.
+constexpr size_t kMostLanes = (size_t)1 << 31;
+
+uint32_t codec_workgroups(size_t lanes) { return (uint32_t)((lanes + kCodecLanes - 1) / kCodecLanes); }
+
+template <typename In>
+hipError_t quantize(const In* x, size_t n, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+    constexpr size_t kElems = 32 / sizeof(In);
+    hipError_t e = hipSuccess;
+    for (size_t at = 0; at < n && e == hipSuccess; at += kMostLanes * kElems) {
+        const size_t lanes = std::min((n - at) / kElems, kMostLanes);
+        e = enqueue(mx_quantize_kernel<In>, dim3(codec_workgroups(lanes)), dim3(kCodecLanes), stream, x + at, reinterpret_cast<uint32_t*>(codes + at / 2),
+                    scales + at / 32, lanes);
+    }
+    return e;
+}
+
+template <typename Out>
+hipError_t dequantize(const uint8_t* codes, const uint8_t* scales, size_t n, Out* out, hipStream_t stream) {
+    constexpr size_t kElems = 16 / sizeof(Out);
+    hipError_t e = hipSuccess;
+    for (size_t at = 0; at < n && e == hipSuccess; at += kMostLanes * kElems) {
+        const size_t lanes = std::min((n - at) / kElems, kMostLanes);
+        e = enqueue(mx_dequantize_kernel<Out>, dim3(codec_workgroups(lanes)), dim3(kCodecLanes), stream, codes + at / 2, scales + at / 32, out + at, lanes);
+    }
+    return e;
 }
 
 // ---------------------------------------------------------------------------
@@ -192,18 +222,11 @@ hipError_t launch(const Mxfp4Args& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_mx_quantize(const void* x, int in_bf16, size_t n, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
-    const size_t lanes = n / (in_bf16 ? 16 : 8), wgs = (lanes + kCodecLanes - 1) / kCodecLanes;
-    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
-    uint32_t* c = reinterpret_cast<uint32_t*>(codes);
-    return in_bf16 ? enqueue(mx_quantize_kernel<uint16_t>, dim3((uint32_t)wgs), dim3(kCodecLanes), stream, static_cast<const uint16_t*>(x), c, scales, lanes)
-                   : enqueue(mx_quantize_kernel<float>, dim3((uint32_t)wgs), dim3(kCodecLanes), stream, static_cast<const float*>(x), c, scales, lanes);
+    return in_bf16 ? quantize(static_cast<const uint16_t*>(x), n, codes, scales, stream) : quantize(static_cast<const float*>(x), n, codes, scales, stream);
 }
 
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, size_t n, void* out, int out_bf16, hipStream_t stream) {
-    const size_t lanes = n / (out_bf16 ? 8 : 4), wgs = (lanes + kCodecLanes - 1) / kCodecLanes;
-    if (wgs >= (1ull << 31)) return hipErrorInvalidConfiguration;
-    return out_bf16 ? enqueue(mx_dequantize_kernel<uint16_t>, dim3((uint32_t)wgs), dim3(kCodecLanes), stream, codes, scales, static_cast<uint16_t*>(out), lanes)
-                    : enqueue(mx_dequantize_kernel<float>, dim3((uint32_t)wgs), dim3(kCodecLanes), stream, codes, scales, static_cast<float*>(out), lanes);
+    return out_bf16 ? dequantize(codes, scales, n, static_cast<uint16_t*>(out), stream) : dequantize(codes, scales, n, static_cast<float*>(out), stream);
 }
 
 hipError_t launch_gemm_mxfp4(const uint8_t* x, const uint8_t* xs, size_t rows, size_t k, const uint8_t* w, const uint8_t* ws, size_t n,

@@ -41,6 +41,7 @@ def test_muon_plans_what_its_steps_can_launch(L):  # noqa: F811
 
 
 def room(gib):
+    torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < gib << 30:
         pytest.skip("needs %d GiB of device memory" % gib)
 
@@ -80,3 +81,34 @@ def test_mxfp4_few_rows_and_many_outputs(dev):  # noqa: F811
     for g, (a, b) in enumerate(((0, 33), (33, 64))):
         near(out[a:b, at.to(dev)], x[a:b] @ w[g].t(), x[a:b].abs() @ w[g].abs().t(), k, BF16, "group %d" % g)
     assert not out[:, 1000:2000].any()
+
+
+END = 96  # elements at each of the places looked at
+
+
+@pytest.mark.gpu
+def test_codec_past_a_launch(dev):  # noqa: F811
+    """More lanes than a launch can have: 2^35 elements from fp32 or to bf16, 8 to a lane.  The first elements, the last, and those around each
+    2^33 of them."""
+    n, step = (1 << 35) + END, 1 << 33
+    room(170)
+    where = [slice(0, END)] + [slice(i * step + d, i * step + d + END) for i in range(1, 5) for d in (-END, 0) if i * step + d + END <= n]
+    ends = randn(len(where), END, seed=1)
+    c, s, v = mx_oracle(ends)
+    parts = lambda w, d: slice(w.start // d, w.stop // d)  # noqa: E731
+    codes, scales = torch.full((n // 2,), 0x99, dtype=torch.uint8, device=dev), torch.full((n // MX,), 9, dtype=torch.uint8, device=dev)
+    x = torch.zeros(n, device=dev)
+    for i, w in enumerate(where):
+        x[w] = ends[i].to(dev)
+    say("quantize", n)
+    lpc.lpc_quantize_mxfp4(x, codes, scales)
+    for i, w in enumerate(where):
+        assert torch.equal(codes[parts(w, 2)].cpu(), c[i]) and torch.equal(scales[parts(w, MX)].cpu(), s[i]), i
+    del x
+    out = torch.full((n,), 7.0, dtype=BF16, device=dev)
+    say("dequantize", n)
+    lpc.lpc_dequantize_mxfp4(codes, scales, out)
+    for i, w in enumerate(where):
+        assert torch.equal(out[w].cpu(), v[i].to(BF16)), i
+    for i in range(4):
+        assert not out[i * step + END:(i + 1) * step - END].any(), i
