@@ -26,7 +26,7 @@ constexpr float kHeld = 1024.0f, kLow = 2048.0f;  // what X, A and B are held ti
 constexpr double kA = 3.4445, kB = -4.7750, kC = 2.0315;
 
 // The plan does not change during a launch and a workgroup's part of it is the same for all lanes: read by scalar loads.
-typedef uint32_t u32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x16_t __attribute__((ext_vector_type(16), aligned(16)));
 template <typename V, typename T>
 __device__ __forceinline__ T scalar_load(const T* p) {
     static_assert(sizeof(V) == sizeof(T), "as a vector");

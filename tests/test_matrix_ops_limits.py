@@ -112,3 +112,88 @@ def test_codec_past_a_launch(dev):  # noqa: F811
         assert torch.equal(out[w].cpu(), v[i].to(BF16)), i
     for i in range(4):
         assert not out[i * step + END:(i + 1) * step - END].any(), i
+
+
+@pytest.mark.gpu
+def test_bf16_most_rows(dev):  # noqa: F811
+    """As many rows as their tiles allow, 8 long: offsets of both operands and of the results pass 32 bits."""
+    room(130)
+    rows, k = MOST * 256, 8
+    at = torch.tensor([0, 1, 255, 256, (1 << 29) - 1, 1 << 29, (1 << 30) + 77, rows - 257, rows - 256, rows - 1], device=dev)
+    x, some = torch.zeros(rows, k, dtype=BF16, device=dev), randn(len(at), k, seed=1).to(BF16)
+    x[at] = some.to(dev)
+    for n, counts in ((1, None), (1, [1 << 29, rows - (1 << 29) - 5])):
+        g = 1 if counts is None else 2
+        w = randn(g, n, k, seed=2).to(BF16)
+        out = torch.full((rows, n), 7.0, device=dev)
+        say("bf16 product", rows, n, counts)
+        lpc.lpc_gemm_bf16(x, w.to(dev), out, counts=None if counts is None else torch.tensor(counts, dtype=torch.int32, device=dev))
+        for i, r in enumerate(at.tolist()):
+            group = 0 if counts is None or r < counts[0] else 1
+            wd = w[group].double() * (counts is None or r < sum(counts))  # the rows past the last group give zeros
+            near(out[r], some[i].double() @ wd.t(), some[i].double().abs() @ wd.abs().t(), k, torch.float32, "row %d" % r)
+        assert int((out != 0).sum()) <= len(at)
+    del out
+    dx, w = torch.full((rows, 8), 7.0, dtype=BF16, device=dev), randn(8, 8, seed=3).to(BF16)
+    say("bf16 dgrad", rows)
+    lpc.lpc_gemm_bf16_dgrad(x, w.to(dev), dx)
+    wd = w.double()
+    near(dx[at], some.double() @ wd, some.double().abs() @ wd.abs(), 8, BF16, "dgrad")
+    assert int((dx != 0).any(1).sum()) <= len(at)
+
+
+class Shifted:
+    """Copies of tensors that start 16 bytes into a buffer (row counts and single numbers: 4), the least alignment that is taken."""
+
+    def __init__(self, dev):
+        self.dev = dev
+
+    def __call__(self, t, by=16):
+        size = t.element_size()
+        buffer = torch.zeros(t.numel() + by // size, dtype=t.dtype, device=self.dev)
+        view = buffer[by // size:by // size + t.numel()].view(t.shape)
+        view.copy_(t)
+        assert view.data_ptr() % 256 == by
+        return view
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,k,n,counts", [(20, 128, 72, [9, 11]), (300, 384, 520, [100, 0, 150]), (2100, 128, 2056, [2100])])
+def test_operands_of_the_least_alignment(dev, rows, k, n, counts):  # noqa: F811
+    say("alignment", rows, k, n, counts)
+    at, g = Shifted(dev), len(counts)
+    same = lambda t, by=16: t.to(dev)  # noqa: E731
+    x, w, dy = randn(rows, k, seed=1).to(BF16), randn(g, n, k, seed=2).to(BF16), randn(rows, n, seed=3).to(BF16)
+    results = []
+    for put in (same, at):
+        c, q, p, d = put(torch.tensor(counts, dtype=torch.int32), 4), put(x), put(w), put(dy)
+        out, dx, dw = put(torch.zeros(rows, n, dtype=BF16)), put(torch.zeros(rows, k)), put(torch.zeros(g, n, k))
+        lpc.lpc_gemm_bf16(q, p, out, counts=c)
+        lpc.lpc_gemm_bf16_dgrad(d, p, dx, counts=c)
+        lpc.lpc_gemm_bf16_wgrad(d, q, dw, counts=c)
+        codes, scales = put(torch.zeros(rows, k // 2, dtype=torch.uint8)), put(torch.zeros(rows, k // MX, dtype=torch.uint8))
+        wc, ws = put(torch.zeros(g, n, k // 2, dtype=torch.uint8)), put(torch.zeros(g, n, k // MX, dtype=torch.uint8))
+        lpc.lpc_quantize_mxfp4(q, codes, scales)
+        lpc.lpc_quantize_mxfp4(p, wc, ws)
+        served, back = put(torch.zeros(rows, n)), put(torch.zeros(rows, k, dtype=BF16))
+        lpc.lpc_gemm_mxfp4(codes, scales, wc, ws, served, counts=c)
+        lpc.lpc_dequantize_mxfp4(codes, scales, back)
+        results.append([t.clone() for t in (out, dx, dw, codes, scales, wc, ws, served, back)])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.gpu
+def test_muon_of_the_least_alignment(dev):  # noqa: F811
+    """Parameters, gradients, momenta, copies, the plan and the workspace."""
+    shapes = [(3, 33, 35), (16, 300), (2, 300, 520), (9, 7)]
+    same, results = (lambda t, by=16: t.to(dev)), []
+    for put in (same, Shifted(dev)):
+        p, g, m = ([put(randn(*s, seed=10 * i + j)) for j, s in enumerate(shapes)] for i in range(3))
+        copies = [put(t.to(BF16).cpu()) for t in p]
+        opt = lpc.Muon(p, g, m, copies=copies)
+        if put is not same:
+            opt._plan, opt._space = put(opt._plan), put(opt._space)
+        say("muon", shapes)
+        opt.step(lr=0.1, grad_scale=put(torch.tensor([0.5]), 4))
+        results.append([t.clone() for t in p + m + copies])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
