@@ -851,6 +851,9 @@ class Muon:
                 if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
                     raise ValueError("params[%d] must be a 2-D or 3-D tensor" % i)
                 shapes.append((1,) * (3 - t.dim()) + tuple(t.shape))
+                for what, ts in lists.items():  # a tensor that lies the other way round has as many elements
+                    if what != "scales" and ts is not None and getattr(ts[i], "ndim", 1) > 1 and ts[i].shape[-1] != t.shape[-1]:
+                        raise ValueError("%s[%d] has shape %s, params[%d] %s" % (what, i, tuple(ts[i].shape), i, tuple(t.shape)))
             sizes = [t.numel() for t in params]
             fields = {"param": p.many(params, "params", _F32, sizes),
                       "grad": p.many(grads, "grads", (getattr(grads[0], "dtype", None),) if getattr(grads[0], "dtype", None) in _FB else _FB, sizes),
