@@ -33,7 +33,7 @@
 // half of row l % 16's block.
 #include <stddef.h>
 
-#include "lpc_ops.hpp"
+#include "lpc_slots.hpp"
 
 namespace lpc {
 namespace {
@@ -283,10 +283,6 @@ hipError_t launch_split(const GemmArgs& a, uint32_t tiles_q, uint32_t z, hipStre
 // addresses it reads.
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
-}
-
 // 16 (4) bytes a lane from base + off to LDS at `to` + 16 (4) lane.  The compiler does not count
 // these loads: lds_arrived() waits until at most `Left` of them are on their way.  M0 is read one wait state after it is written,
 // and is named as overwritten, so that no use of it by the compiler is carried across (the warning says that it is not saved either).
@@ -299,10 +295,6 @@ __device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base) : "m0");
 }
 #pragma clang diagnostic pop
-template <int Left>
-__device__ __forceinline__ void lds_arrived() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Left) : "memory");
-}
 
 // a lane's part of a fragment from its row `r` in LDS; lo: where that row's piece l/16 is
 __device__ __forceinline__ i32x8_t read_fragment(const uint8_t* r, uint32_t lo) {
@@ -493,18 +485,6 @@ hipError_t launch_narrow(const GemmArgs& a, uint32_t tiles_q, hipStream_t stream
 // ---------------------------------------------------------------------------
 
 constexpr int kTiledWaves = 8;
-// Tiles along q that neighbouring workgroups share P with: an XCD's 32 CUs then work on about 6 x 5 tiles, whose
-// operands its L2 serves.  16,384 x 7168 x 4096 over 8 groups of Zipf-distributed rows took 454 us with 6, 453 with 8 and
-// 471 with 2 or 4 (equal rows 424, 419, 425 and 435).
-constexpr uint32_t kBand = 6;
-
-// Ends a slot: this wavefront's reads of LDS are done, and no instruction moves across.
-__device__ __forceinline__ void end_slot() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
 // Shape of a tile: WavesQ wavefronts along q, each with 16 F Phases x 16 PF outputs.
 template <int WQ, int F_, int Phases_, int PF_>
 struct Shape {
@@ -758,19 +738,8 @@ __device__ __forceinline__ void tile(const GemmArgs& a, const Work& w, uint32_t 
     }
 }
 
-// Tile number t of tiles_q x tiles_p: bands of kBand tiles along q, and in a band tile after tile along p.
-__device__ __forceinline__ uint2 in_bands(uint32_t t, uint32_t tiles_q, uint32_t tiles_p) {
-    const uint32_t band = t / (kBand * tiles_p), in = t - band * kBand * tiles_p;
-    const uint32_t high = min(kBand, tiles_q - band * kBand), tp = in / high;
-    return make_uint2(band * kBand + in - tp * high, tp);
-}
-
-// A workgroup has a CU to itself, and each XCD works through its own run of tiles, 32 at a time.  Where a last round
-// would leave half of the CUs or more without a tile, its tiles are split into parts of 128 x 128, which take about a
-// third of a tile's time.  Product 16,384 x 7168 x 4096 over 8 groups of Zipf-distributed rows: 454 us against 482; 512 x
-// 8192 x 8192, 8 tiles an XCD: 52 us against 99.  How many tiles the counts make is known here and not on the host.
-constexpr uint32_t kXcds = 8, kXcdCus = 32, kMostSplit = kXcdCus / 2;
-
+// The parts that a last round's tiles are split into, of 128 x 128, take about a third of a tile's time.  Product 16,384 x
+// 7168 x 4096 over 8 groups of Zipf-distributed rows: 454 us against 482; 512 x 8192 x 8192, 8 tiles an XCD: 52 us against 99.
 template <typename Out>
 __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_product_kernel(GemmArgs a) {
     using L = Large<Out>;
@@ -803,26 +772,12 @@ __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_product_kernel(GemmA
     }
 }
 
-// The group with the z-th most rows, for up to 64 groups: their tiles take times that differ as their rows do, and the
-// long ones come first, so that short ones fill the end.
-__device__ __forceinline__ GroupTile group_by_rows(const GemmArgs& a, uint32_t z) {
-    if (a.groups > 64) return find_group(a.counts, a.groups, a.rows, kBlock, z);
-    const GroupScan s(a.counts, a.groups, a.rows, kBlock, 0, 0, 0);
-    const uint32_t lane = threadIdx.x & 63, mine = s.end - s.begin;
-    uint32_t rank = 0;
-    for (uint32_t g = 0; g < a.groups; ++g) {
-        const uint32_t other = from_lane(mine, g);
-        rank += other > mine || (other == mine && g < lane);
-    }
-    return group_of_lane(s, 0, (uint32_t)__builtin_ctzll(__ballot(lane < a.groups && rank == z)));
-}
-
 template <typename S>
 __global__ __launch_bounds__(kTiledWaves * 64, 2) void gemm_wgrad_kernel(GemmArgs a) {
     __shared__ __attribute__((aligned(128))) uint8_t lds[S::kBytes];
     const uint32_t tiles_p = (a.np + S::BP - 1) / S::BP;
     const uint2 t = in_bands((uint32_t)xcd_tile(), gridDim.x / tiles_p, tiles_p);
-    tile<kWgrad, float, S>(a, wgrad_work(a, group_by_rows(a, blockIdx.y), t.x * S::BQ, S::BQ), t.y * S::BP, lds);
+    tile<kWgrad, float, S>(a, wgrad_work(a, group_by_rows(a.counts, a.groups, a.rows, kBlock, blockIdx.y), t.x * S::BQ, S::BQ), t.y * S::BP, lds);
 }
 
 template <typename Out>

@@ -116,7 +116,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm16_wgrad_kernel(Gemm16
     __shared__ __attribute__((aligned(128))) uint8_t lds[S::kBytes];
     const uint32_t tiles_p = (a.k + S::BP - 1) / S::BP;
     const uint2 t = in_bands((uint32_t)xcd_tile(), gridDim.x / tiles_p, tiles_p);
-    const GroupTile g = group_by_rows(a.counts, a.groups, a.rows, blockIdx.y);
+    const GroupTile g = group_by_rows(a.counts, a.groups, a.rows, 1, blockIdx.y);
     tile<kWgrad, Out, S>(a, g.group, t.x * S::BQ, min(S::BQ, a.n - t.x * S::BQ), t.y * S::BP, g.row, g.row + g.rows, lds);
 }
 

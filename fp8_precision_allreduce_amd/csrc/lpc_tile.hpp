@@ -19,7 +19,7 @@
 
 #include <type_traits>
 
-#include "lpc_ops.hpp"
+#include "lpc_slots.hpp"
 
 namespace lpc {
 namespace {
@@ -85,10 +85,6 @@ struct MmaMxfp4 {
 // asynchronous loads to LDS
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
-}
-
 // 16 (4) bytes a lane from base + off, or from an address of its own, to LDS at `to` + 16 (4) lane.  The compiler does not
 // count these loads: lds_arrived() waits until at most `Left` of them are on their way.  M0 is read one wait state after it
 // is written, and is named as overwritten, so that no use of it by the compiler is carried across (the warning says that it
@@ -105,11 +101,6 @@ __device__ __forceinline__ void load_lds4_at(const void* from, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "m0");
 }
 #pragma clang diagnostic pop
-template <int Left>
-__device__ __forceinline__ void lds_arrived() {
-    static_assert(Left < 64, "what the wait instruction can count");
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Left) : "memory");
-}
 
 // ---------------------------------------------------------------------------
 // operands
@@ -269,13 +260,6 @@ __device__ __forceinline__ void cut(Fragment& f, uint32_t lane, uint32_t count) 
 // ---------------------------------------------------------------------------
 
 constexpr int kTileWaves = 8;
-
-// Ends a slot: this wavefront's reads of LDS are done, and no instruction moves across.
-__device__ __forceinline__ void end_slot() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
 
 // Exponent bytes come for four slabs at a time, 32 bytes of each row, into one of two buffers behind the stages: a slab's 8 bytes
 // of each row by themselves were 512 lines for 4 KB, as many as of the codes (16,384 x 7168 x 4096 over 8 groups 314 us against 281).
@@ -774,22 +758,6 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[S::AQ][S::AP], O
 // which tile a workgroup takes
 // ---------------------------------------------------------------------------
 
-// Tiles along q that neighbouring workgroups share P with: an XCD's 32 CUs then work on about 6 x 5 tiles, whose operands
-// its L2 serves.
-constexpr uint32_t kBand = 6;
-
-// Tile number t of tiles_q x tiles_p: bands of kBand tiles along q, and in a band tile after tile along p.
-__device__ __forceinline__ uint2 in_bands(uint32_t t, uint32_t tiles_q, uint32_t tiles_p) {
-    const uint32_t band = t / (kBand * tiles_p), in = t - band * kBand * tiles_p;
-    const uint32_t high = min(kBand, tiles_q - band * kBand), tp = in / high;
-    return make_uint2(band * kBand + in - tp * high, tp);
-}
-
-// A large tile's workgroup has a CU to itself, and each XCD works through its own run of tiles, 32 at a time.  Where a last
-// round would leave half of the CUs or more without a tile, its tiles are split into parts of the small size.  How many tiles
-// the counts make is known here and not on the host.
-constexpr uint32_t kXcds = 8, kXcdCus = 32, kMostSplit = kXcdCus / 2;
-
 // Rows [w.row, + w.rows) of a group and outputs [p0, p1) for one workgroup: as one tile of the large shape, or as small tiles.
 struct Share {
     GroupTile w;
@@ -858,20 +826,6 @@ __device__ __forceinline__ bool find_even(const int32_t* counts, uint32_t groups
     return true;
 }
 inline uint64_t even_workgroups(uint64_t tiles) { return (tiles + kXcds - 1) / kXcds * kXcds; }
-
-// The group with the z-th most rows, for up to 64 groups: their tiles take times that differ as their rows do, and the
-// long ones come first, so that short ones fill the end.
-__device__ __forceinline__ GroupTile group_by_rows(const int32_t* counts, uint32_t groups, uint32_t rows, uint32_t z) {
-    if (groups > 64) return find_group(counts, groups, rows, 1, z);
-    const GroupScan s(counts, groups, rows, 1, 0, 0, 0);
-    const uint32_t lane = threadIdx.x & 63, mine = s.end - s.begin;
-    uint32_t rank = 0;
-    for (uint32_t g = 0; g < groups; ++g) {
-        const uint32_t other = from_lane(mine, g);
-        rank += other > mine || (other == mine && g < lane);
-    }
-    return group_of_lane(s, 0, (uint32_t)__builtin_ctzll(__ballot(lane < groups && rank == z)));
-}
 
 }  // namespace
 }  // namespace lpc
