@@ -7,16 +7,16 @@
 // shorter side (for a tall matrix X^T X, and X B).  All three products are matrix instructions on fp16 with FP32 sums.
 //
 // Precision.  X is held as fp16 high and low halves of together 22 bits: products take the high half, the term a X both.
-// Directions of small singular values live on that term alone (B is small there), so that they keep their precision.  Without the
-// low half of the last two X, as what rounding adds to them is multiplied by 3.4445^2 at most, five iterations took 2.7% less and
-// were 2 to 3 times as far off on updates of low rank or with a few strong directions (three of rank 3: 3.9e-3 of the update
-// against 8e-4, 2-norm).  With the high half alone the update was off by 4e-2 where a few strong directions hide the rest, and bf16 in its place gave 3e-1.  fp16 rather
-// than bf16 as matrices stay within known bounds: X, A and B are held times 2^10, which keeps elements of 2^-24 and up normal and the largest
-// (singular values stay below 1.3, A's below 1.7, B's below 3) far below 65504.
+// Directions of small singular values live on that term alone (B is small there), so that they keep their precision: after five
+// iterations the update is off by 8e-4 to 3.2e-3 of itself (2-norm) over matrices of full and of low rank, with equal rows and with
+// a few strong directions.  Without the low half of the last two X the large updates took 2.7% less and were 2 to 3.5 times as far off
+// where the rank is low or few directions are strong; with the high half alone 4e-2, and bf16 in its place gave 3e-1.  fp16 rather
+// than bf16 as matrices stay within known bounds: X, A and B are held times 2^10, which keeps elements of 2^-24 and up normal and
+// the largest (singular values stay below 1.3, A's below 1.7, B's below 3) far below 65504.
 //
-// What bounds it: eight matrices of 2048 x 7168 (4.8 ms) the updates, 500 us an iteration of which 350 are products and the rest
-// moves X's halves, 8 bytes an element, between rounds of tiles that no compute hides; one of 2048 x 2048 (373 to 384 us) the chain of 15
-// products, each one round of small tiles of 23 to 27 us; nine odd ones of 1000 x 1500 and around (315 us) the same chain.
+// What bounds it: eight matrices of 2048 x 7168 (4.8 ms) the updates, 510 us an iteration of which 350 are products and the rest
+// moves X's halves, 8 bytes an element, between rounds of tiles that no compute hides; one of 2048 x 2048 (378 to 389 us) the chain of 15
+// products, each one round of small tiles of 23 to 28 us; nine odd ones of 1000 x 1500 and around (322 us) the same chain.
 #include "lpc_tile.hpp"
 
 namespace lpc {
